@@ -17,13 +17,25 @@ binding over that ABI, with the same names:
 * ``wait_timeout_selftest`` -- runs the kernels' bounded-wait error path on events
   that never come, leaving the flag ``workspace_status`` reads.
 
+The stack KDA comes from interleaves it with latent attention (MLA) layers; their
+operators (``include/mla.h``, same library) stand beside it:
+
+* ``mla_append``   -- RMSNorm of the latent, position rotation, the write into a paged cache;
+* ``mla_decode``   -- absorbed attention of a few new tokens per sequence over that cache;
+* ``mla_prefill``  -- expanded attention over packed sequences;
+* ``mla_backward`` -- its gradients;
+* ``mla_decode_workspace_size``, ``mla_backward_workspace_size``.
+
 ``inputs`` holds the seeded synthetic input generators.  Importing the package
 does not load the CUDA library; the first call does, and raises if it is missing.
 """
 from ._binding import (KdaError, backward_workspace_size, kda_backward, kda_decode_step,
                        kda_decode_tokens, kda_prefill, kda_prefill_gated, kda_prologue, load,
                        prefill_workspace_size, wait_timeout_selftest, workspace_status)
+from ._mla_binding import (mla_append, mla_backward, mla_backward_workspace_size, mla_decode,
+                           mla_decode_workspace_size, mla_prefill)
 
 __all__ = ["KdaError", "backward_workspace_size", "kda_backward", "kda_decode_step", "kda_decode_tokens",
-           "kda_prefill", "kda_prefill_gated", "kda_prologue", "load", "prefill_workspace_size",
-           "wait_timeout_selftest", "workspace_status"]
+           "kda_prefill", "kda_prefill_gated", "kda_prologue", "load", "mla_append", "mla_backward",
+           "mla_backward_workspace_size", "mla_decode", "mla_decode_workspace_size", "mla_prefill",
+           "prefill_workspace_size", "wait_timeout_selftest", "workspace_status"]

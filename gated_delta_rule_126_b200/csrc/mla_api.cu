@@ -1,0 +1,197 @@
+// C-ABI entry points of the latent-attention operators: argument checks on the host, then
+// kernel launches on the caller's stream.  See include/mla.h for the contract.
+#include <cmath>
+#include <cstdint>
+
+#include "mla_internal.h"
+
+namespace {
+
+bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+bool dtype_ok(kda_dtype_t t) { return t == KDA_DTYPE_F32 || t == KDA_DTYPE_BF16; }
+size_t elem(kda_dtype_t t) { return t == KDA_DTYPE_F32 ? 4 : 2; }
+kda_status_t from_cuda(cudaError_t e) { return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA; }
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
+kda_status_t check_decode_sizes(int B, int n, int H, int d_latent, int d_rope, kda_dtype_t dtype) {
+    if (B < 0 || n < 0 || H < 1 || d_latent < 1 || d_rope < 0 || !dtype_ok(dtype)) return KDA_ERR_INVALID_ARG;
+    if (d_latent > 512 || d_rope > 64 || int64_t(n) * H > 65536 || B > 65536) return KDA_ERR_UNSUPPORTED;
+    return KDA_OK;
+}
+
+kda_status_t check_head_sizes(int H, int d_nope, int d_rope, int d_v, kda_dtype_t dtype) {
+    if (H < 1 || d_nope < 1 || d_rope < 0 || d_v < 1 || !dtype_ok(dtype)) return KDA_ERR_INVALID_ARG;
+    if (d_nope > 128 || d_rope > 64 || d_v > 128 || H > 65535) return KDA_ERR_UNSUPPORTED;
+    return KDA_OK;
+}
+
+// cu[0] = 0 and non-decreasing.
+bool offsets_ok(const int32_t *cu, int n) {
+    if (!cu || cu[0] != 0) return false;
+    for (int i = 0; i < n; ++i)
+        if (cu[i + 1] < cu[i]) return false;
+    return true;
+}
+
+// Checks shared by mla_prefill and mla_backward; fills `a`.
+kda_status_t prepare(const void *q, int64_t q_st, int64_t q_sh, const void *k, int64_t k_st, int64_t k_sh,
+                     const void *k_rope, int64_t kr_st, const void *v, int64_t v_st, int64_t v_sh, kda_dtype_t dtype,
+                     const int32_t *cu_q_dev, const int32_t *cu_q_host, const int32_t *cu_k_dev,
+                     const int32_t *cu_k_host, int num_seqs, int H, int dn, int dr, int dv, float scale, int causal,
+                     kda::MlaArgs &a) {
+    if (num_seqs < 0) return KDA_ERR_INVALID_ARG;
+    const kda_status_t s = check_head_sizes(H, dn, dr, dv, dtype);
+    if (s != KDA_OK) return s;
+    if (!std::isfinite(scale)) return KDA_ERR_INVALID_ARG;
+    if (!cu_q_dev || !cu_k_dev || !offsets_ok(cu_q_host, num_seqs) || !offsets_ok(cu_k_host, num_seqs))
+        return KDA_ERR_INVALID_ARG;
+    a.Tq = cu_q_host[num_seqs];
+    a.Tk = cu_k_host[num_seqs];
+    if (q_st < 0 || q_sh < 0 || k_st < 0 || k_sh < 0 || kr_st < 0 || v_st < 0 || v_sh < 0) return KDA_ERR_INVALID_ARG;
+    if (a.Tq > 0 && !q) return KDA_ERR_INVALID_ARG;
+    if (a.Tk > 0 && (!k || !v || (dr > 0 && !k_rope))) return KDA_ERR_INVALID_ARG;
+    const size_t es = elem(dtype);
+    for (const void *p : {q, k, v, dr > 0 ? k_rope : nullptr})
+        if (!aligned(p, es)) return KDA_ERR_INVALID_ARG;
+    a.q = q; a.q_st = q_st; a.q_sh = q_sh;
+    a.k = k; a.k_st = k_st; a.k_sh = k_sh;
+    a.k_rope = k_rope; a.kr_st = kr_st;
+    a.v = v; a.v_st = v_st; a.v_sh = v_sh;
+    a.dtype = dtype;
+    a.cu_q = cu_q_dev; a.cu_k = cu_k_dev; a.cu_q_host = cu_q_host; a.cu_k_host = cu_k_host;
+    a.num_seqs = num_seqs; a.H = H; a.dn = dn; a.dr = dr; a.dv = dv;
+    a.scale = scale; a.causal = causal != 0;
+    return KDA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+kda_status_t mla_append(const void *c, int64_t c_stride, const void *k_rope, int64_t k_rope_stride, kda_dtype_t dtype,
+                        const float *norm_weight, float eps, const float *inv_freq, int interleaved,
+                        const int32_t *cu_seqlens_dev, const int32_t *past_lens, int num_seqs, int64_t total_tokens,
+                        const int32_t *page_table, int max_pages, void *cache, int num_pages, int page_size,
+                        int d_latent, int d_rope, const void *q_rope, int64_t q_stride_t, int64_t q_stride_h, int H,
+                        void *q_out, int64_t qo_stride_t, int64_t qo_stride_h, void *c_out, void *k_rope_out,
+                        kda_stream_t stream) {
+    if (num_seqs < 0 || total_tokens < 0 || max_pages < 0 || num_pages < 0 || page_size < 1 || d_latent < 1 ||
+        d_rope < 0 || !dtype_ok(dtype))
+        return KDA_ERR_INVALID_ARG;
+    if (d_latent > 512 || d_rope > 64 || (d_rope & 1)) return KDA_ERR_UNSUPPORTED;
+    if (total_tokens > INT32_MAX) return KDA_ERR_UNSUPPORTED;
+    if (norm_weight && (!(eps >= 0.f) || !std::isfinite(eps))) return KDA_ERR_INVALID_ARG;
+    if (q_rope && (H < 1 || !q_out || d_rope == 0)) return KDA_ERR_INVALID_ARG;
+    if (q_rope && H > 65535) return KDA_ERR_UNSUPPORTED;
+    if (c_stride < 0 || k_rope_stride < 0 || q_stride_t < 0 || q_stride_h < 0 || qo_stride_t < 0 || qo_stride_h < 0)
+        return KDA_ERR_INVALID_ARG;
+    if (num_seqs == 0 || total_tokens == 0) return KDA_OK;
+    if (!c || (d_rope > 0 && !k_rope) || !cu_seqlens_dev || !past_lens) return KDA_ERR_INVALID_ARG;
+    if ((max_pages > 0 && !page_table) || (num_pages > 0 && !cache)) return KDA_ERR_INVALID_ARG;
+    const size_t es = elem(dtype);
+    for (const void *p : {c, d_rope > 0 ? k_rope : nullptr, static_cast<const void *>(cache), q_rope,
+                          static_cast<const void *>(q_rope ? q_out : nullptr), static_cast<const void *>(c_out),
+                          static_cast<const void *>(k_rope_out)})
+        if (!aligned(p, es)) return KDA_ERR_INVALID_ARG;
+    kda::MlaAppendArgs a;
+    a.c = c; a.c_stride = c_stride;
+    a.k_rope = d_rope ? k_rope : nullptr; a.k_rope_stride = k_rope_stride;
+    a.dtype = dtype; a.norm_weight = norm_weight; a.eps = eps; a.inv_freq = inv_freq; a.interleaved = interleaved != 0;
+    a.cu = cu_seqlens_dev; a.past = past_lens; a.num_seqs = num_seqs; a.total_tokens = total_tokens;
+    a.page_table = page_table; a.max_pages = max_pages; a.cache = cache; a.num_pages = num_pages;
+    a.page_size = page_size; a.dc = d_latent; a.dr = d_rope;
+    a.q_rope = q_rope; a.q_st = q_stride_t; a.q_sh = q_stride_h; a.H = H;
+    a.q_out = q_rope ? q_out : nullptr; a.qo_st = qo_stride_t; a.qo_sh = qo_stride_h;
+    a.c_out = c_out; a.k_rope_out = d_rope ? k_rope_out : nullptr;
+    return from_cuda(kda::launch_mla_append(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t mla_decode_workspace_size(int B, int n, int H, int d_latent, int d_rope, kda_dtype_t dtype) {
+    if (check_decode_sizes(B, n, H, d_latent, d_rope, dtype) != KDA_OK) return 0;
+    return align256(kda::mla_decode_scratch(B, n, H, d_latent, d_rope, dtype));
+}
+
+kda_status_t mla_decode(const void *q, kda_dtype_t dtype, const void *cache, int num_pages, int page_size,
+                        const int32_t *page_table, int max_pages, const int32_t *seq_lens, int B, int n, int H,
+                        int d_latent, int d_rope, float scale, void *o, float *lse, void *workspace,
+                        size_t workspace_bytes, kda_stream_t stream) {
+    const kda_status_t s = check_decode_sizes(B, n, H, d_latent, d_rope, dtype);
+    if (s != KDA_OK) return s;
+    if (num_pages < 0 || max_pages < 0 || page_size < 1 || !std::isfinite(scale)) return KDA_ERR_INVALID_ARG;
+    if (B == 0 || n == 0) return KDA_OK;
+    if (!q || !o || !seq_lens || (max_pages > 0 && !page_table) || (num_pages > 0 && !cache))
+        return KDA_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(cache, 16) || !aligned(o, 16)) return KDA_ERR_INVALID_ARG;
+    if (!workspace || !aligned(workspace, 256) ||
+        workspace_bytes < kda::mla_decode_scratch(B, n, H, d_latent, d_rope, dtype))
+        return KDA_ERR_WORKSPACE;
+    kda::MlaDecodeArgs a;
+    a.q = q; a.cache = cache; a.dtype = dtype;
+    a.num_pages = num_pages; a.page_size = page_size; a.max_pages = max_pages;
+    a.page_table = page_table; a.seq_lens = seq_lens;
+    a.B = B; a.n = n; a.H = H; a.dc = d_latent; a.dr = d_rope; a.scale = scale;
+    a.o = o; a.lse = lse; a.workspace = workspace;
+    return from_cuda(kda::launch_mla_decode(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+kda_status_t mla_prefill(const void *q, int64_t q_stride_t, int64_t q_stride_h, const void *k, int64_t k_stride_t,
+                         int64_t k_stride_h, const void *k_rope, int64_t k_rope_stride, const void *v,
+                         int64_t v_stride_t, int64_t v_stride_h, kda_dtype_t dtype, const int32_t *cu_q_dev,
+                         const int32_t *cu_q_host, const int32_t *cu_k_dev, const int32_t *cu_k_host, int num_seqs,
+                         int H, int d_nope, int d_rope, int d_v, float scale, int causal, void *o, float *lse,
+                         kda_stream_t stream) {
+    kda::MlaArgs a{};
+    const kda_status_t s = prepare(q, q_stride_t, q_stride_h, k, k_stride_t, k_stride_h, k_rope, k_rope_stride, v,
+                                   v_stride_t, v_stride_h, dtype, cu_q_dev, cu_q_host, cu_k_dev, cu_k_host, num_seqs,
+                                   H, d_nope, d_rope, d_v, scale, causal, a);
+    if (s != KDA_OK) return s;
+    if (a.Tq == 0) return KDA_OK;
+    if (!o || !aligned(o, elem(dtype))) return KDA_ERR_INVALID_ARG;
+    a.o = o;
+    a.lse = lse;
+    return from_cuda(kda::launch_mla_prefill_simt(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t mla_backward_workspace_size(int64_t total_q, int64_t total_k, int H, int d_nope, int d_rope, int d_v,
+                                   kda_dtype_t dtype) {
+    if (check_head_sizes(H, d_nope, d_rope, d_v, dtype) != KDA_OK) return 0;
+    if (total_q < 0 || total_k < 0 || total_q > INT32_MAX || total_k > INT32_MAX) return 0;
+    return 256 + align256(size_t(total_q) * H * sizeof(float)) + align256(size_t(total_k) * H * d_rope * sizeof(float));
+}
+
+kda_status_t mla_backward(const void *q, int64_t q_stride_t, int64_t q_stride_h, const void *k, int64_t k_stride_t,
+                          int64_t k_stride_h, const void *k_rope, int64_t k_rope_stride, const void *v,
+                          int64_t v_stride_t, int64_t v_stride_h, kda_dtype_t dtype, const int32_t *cu_q_dev,
+                          const int32_t *cu_q_host, const int32_t *cu_k_dev, const int32_t *cu_k_host, int num_seqs,
+                          int H, int d_nope, int d_rope, int d_v, float scale, int causal, const void *o,
+                          const float *lse, const void *dO, void *dq, void *dk, void *dk_rope, void *dv,
+                          void *workspace, size_t workspace_bytes, kda_stream_t stream) {
+    kda::MlaArgs a{};
+    const kda_status_t s = prepare(q, q_stride_t, q_stride_h, k, k_stride_t, k_stride_h, k_rope, k_rope_stride, v,
+                                   v_stride_t, v_stride_h, dtype, cu_q_dev, cu_q_host, cu_k_dev, cu_k_host, num_seqs,
+                                   H, d_nope, d_rope, d_v, scale, causal, a);
+    if (s != KDA_OK) return s;
+    if (a.Tq * H > (int64_t(1) << 33) || a.Tk * d_rope > (int64_t(1) << 38)) return KDA_ERR_UNSUPPORTED;
+    if (a.Tq == 0 && a.Tk == 0) return KDA_OK;
+    if (a.Tq > 0 && (!o || !lse || !dO || !dq)) return KDA_ERR_INVALID_ARG;
+    if (a.Tk > 0 && (!dk || !dv || (d_rope > 0 && !dk_rope))) return KDA_ERR_INVALID_ARG;
+    for (const void *p : {o, dO, static_cast<const void *>(dq), static_cast<const void *>(dk),
+                          static_cast<const void *>(d_rope ? dk_rope : nullptr), static_cast<const void *>(dv)})
+        if (!aligned(p, elem(dtype))) return KDA_ERR_INVALID_ARG;
+    if (!workspace || !aligned(workspace, 256) ||
+        workspace_bytes < mla_backward_workspace_size(a.Tq, a.Tk, H, d_nope, d_rope, d_v, dtype))
+        return KDA_ERR_WORKSPACE;
+    a.o = const_cast<void *>(o);
+    a.lse = const_cast<float *>(lse);
+    a.dO = dO; a.dq = dq; a.dk = dk; a.dk_rope = d_rope ? dk_rope : nullptr; a.dv_out = dv;
+    a.delta = reinterpret_cast<float *>(static_cast<char *>(workspace) + 256);
+    a.dkr_partial = reinterpret_cast<float *>(static_cast<char *>(workspace) + 256 +
+                                              align256(size_t(a.Tq) * H * sizeof(float)));
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    cudaError_t e = kda::launch_mla_delta(a, st);
+    if (e == cudaSuccess) e = kda::launch_mla_backward_simt(a, st);
+    if (e == cudaSuccess && d_rope > 0) e = kda::launch_mla_dkr_reduce(a, st);
+    return from_cuda(e);
+}
+
+}  // extern "C"

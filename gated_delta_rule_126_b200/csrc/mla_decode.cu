@@ -1,0 +1,264 @@
+// mla_decode on the CUDA cores in float32 (every type and size the call takes), the join
+// of split items, and the choice between this kernel and the tensor-core one.
+//
+// A block works through its run of tiles (mla_decode_plan.cuh): kRows query rows against
+// kKeys cache rows at a time, both in shared memory as float32, so that each cache row is
+// read from memory once for all heads and tokens of a row tile.  The softmax is online.
+#include <cmath>
+
+#include "mla_decode_plan.cuh"
+#include "mla_internal.h"
+#include "mla_simt.cuh"
+
+namespace kda {
+
+int device_sm_count();
+bool mla_decode_tc_supported(int n, int H, int dc, int dr, kda_dtype_t dtype);
+MlaDecodeShape mla_decode_tc_shape(int n, int H);
+cudaError_t launch_mla_decode_tc(const MlaDecodeArgs &a, const MlaDecodeShape &s, cudaStream_t st);
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kRows = 16;
+constexpr int kKeys = 32;
+
+size_t simt_smem(int W) { return sizeof(float) * ((kRows + kKeys) * simt_row(W) + kKeys * kRows + 3 * kRows); }
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) decode_kernel(const MlaDecodeArgs a, const MlaDecodeShape shape) {
+    extern __shared__ float sm[];
+    __shared__ int64_t buf[kThreads / 32 + 4];
+    const int W = a.dc + a.dr, W4 = (W + 3) & ~3, ld = simt_row(W), R = a.n * a.H, RT = (R + kRows - 1) / kRows;
+    float *Q = sm, *K = Q + kRows * ld, *P = K + kKeys * ld, *Keep = P + kKeys * kRows, *M = Keep + kRows, *L = M + kRows;
+    const int tid = threadIdx.x, sr = tid >> 4, sk = tid & 15;
+    MlaJoin *join = static_cast<MlaJoin *>(a.workspace);
+    float *slots = reinterpret_cast<float *>(static_cast<char *>(a.workspace) + mla_meta_bytes(shape.grid));
+    const size_t slot_floats = mla_slot_floats(kRows, a.dc);
+
+    const MlaRun run = mla_find_run<kThreads>(a, RT, kKeys, buf);
+    // sequences without a key
+    for (int b = blockIdx.x; b < a.B; b += gridDim.x)
+        if (mla_len(a, b) == 0) {
+            for (int64_t i = tid; i < int64_t(R) * a.dc; i += kThreads)
+                static_cast<T *>(a.o)[int64_t(b) * R * a.dc + i] = from_f32<T>(0.f);
+            if (a.lse)
+                for (int i = tid; i < R; i += kThreads) a.lse[int64_t(b) * R + i] = -INFINITY;
+        }
+    if (tid == 0) join[blockIdx.x].parts = 0;
+    if (int(blockIdx.x) >= run.grid) return;
+    zero_columns<kThreads>(Q, ld, W, W4, kRows);
+    zero_columns<kThreads>(K, ld, W, W4, kKeys);
+
+    int b = run.b;
+    int64_t before = run.before;  // tiles of the sequences before b
+    for (int64_t x = run.start; x < run.end;) {
+        const int len = mla_len(a, b), nt = (len + kKeys - 1) / kKeys;
+        if (x >= before + int64_t(nt) * RT) {
+            before += int64_t(nt) * RT;
+            ++b;
+            continue;
+        }
+        const int rt = int((x - before) / nt);
+        const int64_t item = before + int64_t(rt) * nt;  // the item's first tile
+        const int t0 = int(x - item), t1 = int(min(int64_t(nt), run.end - item));
+        const int r0 = rt * kRows, rows = min(kRows, R - r0);
+        __syncthreads();
+        load_tile<T, kThreads>(Q, ld, 0, static_cast<const T *>(a.q) + (int64_t(b) * R + r0) * W, W, W, kRows, rows);
+        float m = -INFINITY, l = 0.f;  // of row sr, the same in its 16 threads
+        float o[kRows][2] = {};        // columns tid and tid + 256
+        for (int t = t0; t < t1; ++t) {
+            const int j0 = t * kKeys;
+            __syncthreads();
+            for (int i = tid; i < kKeys * W; i += kThreads) {
+                const int j = i / W, c = i - j * W, key = j0 + j;
+                float v = 0.f;
+                if (key < len) {
+                    const int page = a.page_table[int64_t(b) * a.max_pages + key / a.page_size];
+                    if (page >= 0 && page < a.num_pages)
+                        v = to_f32(static_cast<const T *>(a.cache)[(int64_t(page) * a.page_size + key % a.page_size) * W + c]);
+                }
+                K[j * ld + c] = v;
+            }
+            __syncthreads();
+            float s[2] = {0.f, 0.f};
+            for (int c = 0; c < W4; c += 4) {
+                const float4 q = *reinterpret_cast<const float4 *>(Q + sr * ld + c);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float4 k = *reinterpret_cast<const float4 *>(K + (sk + 16 * e) * ld + c);
+                    s[e] = fmaf(q.x, k.x, fmaf(q.y, k.y, fmaf(q.z, k.z, fmaf(q.w, k.w, s[e]))));
+                }
+            }
+            const int end = len - (a.n - 1) + (r0 + sr) / a.H;  // keys that row sr's token sees
+            float top = m;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int key = j0 + sk + 16 * e;
+                bool seen = key < end && key < len;
+                if (seen) {
+                    const int page = a.page_table[int64_t(b) * a.max_pages + key / a.page_size];
+                    seen = page >= 0 && page < a.num_pages;
+                }
+                s[e] = seen ? s[e] * a.scale : -INFINITY;
+                top = fmaxf(top, s[e]);
+            }
+#pragma unroll
+            for (int d = 8; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+            const float base = top == -INFINITY ? 0.f : top;
+            const float keep = expf(m - base);
+            float sum = 0.f;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float p = expf(s[e] - base);
+                P[(sk + 16 * e) * kRows + sr] = p;
+                sum += p;
+            }
+#pragma unroll
+            for (int d = 8; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+            l = l * keep + sum;
+            m = top;
+            if (sk == 0) Keep[sr] = keep;
+            __syncthreads();
+#pragma unroll
+            for (int r = 0; r < kRows; ++r) {
+                const float f = Keep[r];
+                o[r][0] *= f;
+                o[r][1] *= f;
+            }
+            for (int j = 0; j < kKeys; ++j) {
+                const float v0 = tid < a.dc ? K[j * ld + tid] : 0.f;
+                const float v1 = tid + kThreads < a.dc ? K[j * ld + tid + kThreads] : 0.f;
+#pragma unroll
+                for (int r = 0; r < kRows; r += 4) {
+                    const float4 p = *reinterpret_cast<const float4 *>(P + j * kRows + r);
+                    o[r + 0][0] = fmaf(p.x, v0, o[r + 0][0]);
+                    o[r + 0][1] = fmaf(p.x, v1, o[r + 0][1]);
+                    o[r + 1][0] = fmaf(p.y, v0, o[r + 1][0]);
+                    o[r + 1][1] = fmaf(p.y, v1, o[r + 1][1]);
+                    o[r + 2][0] = fmaf(p.z, v0, o[r + 2][0]);
+                    o[r + 2][1] = fmaf(p.z, v1, o[r + 2][1]);
+                    o[r + 3][0] = fmaf(p.w, v0, o[r + 3][0]);
+                    o[r + 3][1] = fmaf(p.w, v1, o[r + 3][1]);
+                }
+            }
+        }
+        if (sk == 0) M[sr] = m, L[sr] = l;
+        __syncthreads();
+        const bool whole = t0 == 0 && t1 == nt;
+        if (whole) {
+            T *out = static_cast<T *>(a.o) + (int64_t(b) * R + r0) * a.dc;
+#pragma unroll
+            for (int r = 0; r < kRows; ++r)
+                if (r < rows) {
+                    const float lr = L[r], inv = lr == 0.f ? 0.f : 1.f / lr;
+                    if (tid < a.dc) out[r * a.dc + tid] = from_f32<T>(o[r][0] * inv);
+                    if (tid + kThreads < a.dc) out[r * a.dc + tid + kThreads] = from_f32<T>(o[r][1] * inv);
+                }
+            if (a.lse && tid < rows)
+                a.lse[int64_t(b) * R + r0 + tid] = L[tid] == 0.f ? -INFINITY : M[tid] + logf(L[tid]);
+        } else {
+            const int slot = 2 * blockIdx.x + (x == run.start ? 0 : 1);
+            float *p = slots + slot * slot_floats;
+#pragma unroll
+            for (int r = 0; r < kRows; ++r) {
+                if (tid < a.dc) p[r * a.dc + tid] = o[r][0];
+                if (tid + kThreads < a.dc) p[r * a.dc + tid + kThreads] = o[r][1];
+            }
+            if (tid < kRows) {
+                p[kRows * a.dc + 2 * tid] = M[tid];
+                p[kRows * a.dc + 2 * tid + 1] = L[tid];
+            }
+            if (t0 == 0 && tid == 0) {  // the item begins here: this block's entry names it
+                const int last = mla_block_of(item + nt - 1, run.total, run.grid);
+                join[blockIdx.x] = MlaJoin{last - int(blockIdx.x) + 1, b, rt, slot};
+            }
+        }
+        x = item + t1;
+    }
+}
+
+// Joins the parts of the items that are split over blocks: o = sum_i e^(m_i - m) o_i / sum_i e^(m_i - m) l_i.
+// One block per (block of the main kernel, query row); four groups of 128 threads take the
+// parts in turn, group sums are added in a fixed order.
+constexpr int kJoinThreads = 512;
+template <typename T>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const MlaDecodeArgs a, const MlaDecodeShape shape) {
+    __shared__ float acc[4][512];
+    __shared__ float top[kJoinThreads / 32], sums[kJoinThreads / 32];
+    const int g = blockIdx.x, row = blockIdx.y, tid = threadIdx.x;
+    const MlaJoin j = static_cast<const MlaJoin *>(a.workspace)[g];
+    if (j.parts == 0) return;
+    const int R = a.n * a.H, r0 = j.row_tile * shape.row_tile;
+    if (r0 + row >= R) return;
+    const float *slots = reinterpret_cast<const float *>(static_cast<const char *>(a.workspace) + mla_meta_bytes(shape.grid));
+    const size_t slot_floats = mla_slot_floats(shape.row_tile, a.dc);
+    auto part = [&](int i) { return slots + size_t(i == 0 ? j.first_slot : 2 * (g + i)) * slot_floats; };
+    const int ml = shape.row_tile * a.dc + 2 * row;
+    float m = -INFINITY;
+    for (int i = tid; i < j.parts; i += kJoinThreads) m = fmaxf(m, part(i)[ml]);
+#pragma unroll
+    for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    if ((tid & 31) == 0) top[tid >> 5] = m;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kJoinThreads / 32; ++w) m = fmaxf(m, top[w]);
+    const float base = m == -INFINITY ? 0.f : m;
+    float l = 0.f;
+    for (int i = tid; i < j.parts; i += kJoinThreads) l += expf(part(i)[ml] - base) * part(i)[ml + 1];
+#pragma unroll
+    for (int d = 16; d; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+    if ((tid & 31) == 0) sums[tid >> 5] = l;
+    const int group = tid >> 7, lane = tid & 127;
+    float o[4] = {};  // columns lane + 128 e
+    for (int i = group; i < j.parts; i += 4) {
+        const float *p = part(i);
+        const float f = expf(p[ml] - base);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (lane + 128 * e < a.dc) o[e] = fmaf(f, p[row * a.dc + lane + 128 * e], o[e]);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[group][lane + 128 * e] = o[e];
+    __syncthreads();
+    l = 0.f;
+#pragma unroll
+    for (int w = 0; w < kJoinThreads / 32; ++w) l += sums[w];
+    const int64_t at = int64_t(j.b) * R + r0 + row;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    if (tid < a.dc)
+        static_cast<T *>(a.o)[at * a.dc + tid] = from_f32<T>((acc[0][tid] + acc[1][tid] + acc[2][tid] + acc[3][tid]) * inv);
+    if (a.lse && tid == 0) a.lse[at] = l == 0.f ? -INFINITY : m + logf(l);
+}
+
+template <typename T> cudaError_t launch_simt(const MlaDecodeArgs &a, const MlaDecodeShape &s, cudaStream_t st) {
+    const size_t smem = simt_smem(a.dc + a.dr);
+    const cudaError_t e = cudaFuncSetAttribute(decode_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    if (e != cudaSuccess) return e;
+    decode_kernel<T><<<s.grid, kThreads, smem, st>>>(a, s);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+MlaDecodeShape mla_decode_shape(int B, int n, int H, int dc, int dr, kda_dtype_t dtype) {
+    (void)B;
+    return MlaDecodeShape{kRows, kKeys, 2 * device_sm_count()};
+}
+
+size_t mla_decode_scratch(int B, int n, int H, int dc, int dr, kda_dtype_t dtype) {
+    const MlaDecodeShape s = mla_decode_shape(B, n, H, dc, dr, dtype);
+    return mla_meta_bytes(s.grid) + 2 * size_t(s.grid) * mla_slot_floats(s.row_tile, dc) * sizeof(float);
+}
+
+cudaError_t launch_mla_decode(const MlaDecodeArgs &a, cudaStream_t st) {
+    const MlaDecodeShape s = mla_decode_shape(a.B, a.n, a.H, a.dc, a.dr, a.dtype);
+    cudaError_t e = a.dtype == KDA_DTYPE_F32 ? launch_simt<float>(a, s, st) : launch_simt<__nv_bfloat16>(a, s, st);
+    if (e != cudaSuccess) return e;
+    const dim3 grid(s.grid, s.row_tile < a.n * a.H ? s.row_tile : a.n * a.H);
+    if (a.dtype == KDA_DTYPE_F32) join_kernel<float><<<grid, kJoinThreads, 0, st>>>(a, s);
+    else join_kernel<__nv_bfloat16><<<grid, kJoinThreads, 0, st>>>(a, s);
+    return cudaGetLastError();
+}
+
+}  // namespace kda

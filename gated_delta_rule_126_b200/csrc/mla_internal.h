@@ -1,0 +1,80 @@
+// Internal declarations of the latent-attention operators (not part of the ABI).
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "mla.h"
+
+namespace kda {
+
+struct MlaAppendArgs {
+    const void *c, *k_rope, *q_rope;
+    int64_t c_stride, k_rope_stride, q_st, q_sh, qo_st, qo_sh;
+    kda_dtype_t dtype;
+    const float *norm_weight, *inv_freq;
+    float eps;
+    int interleaved;
+    const int32_t *cu, *past, *page_table;
+    int num_seqs;
+    int64_t total_tokens;
+    int max_pages, num_pages, page_size, dc, dr, H;
+    void *cache, *q_out, *c_out, *k_rope_out;
+};
+
+struct MlaDecodeArgs {
+    const void *q, *cache;
+    kda_dtype_t dtype;
+    int num_pages, page_size, max_pages;
+    const int32_t *page_table, *seq_lens;
+    int B, n, H, dc, dr;
+    float scale;
+    void *o;
+    float *lse;
+    void *workspace;
+};
+
+struct MlaArgs {  // mla_prefill and mla_backward
+    const void *q, *k, *k_rope, *v;
+    int64_t q_st, q_sh, k_st, k_sh, kr_st, v_st, v_sh;
+    kda_dtype_t dtype;
+    const int32_t *cu_q, *cu_k;            // device
+    const int32_t *cu_q_host, *cu_k_host;  // host
+    int num_seqs, H, dn, dr, dv;
+    int64_t Tq, Tk;
+    float scale;
+    int causal;
+    void *o;
+    float *lse;
+    // backward
+    const void *dO;
+    void *dq, *dk, *dk_rope, *dv_out;
+    float *delta;       // [Tq, H]: sum_c dO * o
+    float *dkr_partial; // [H, Tk, dr]: each head's share of dk_rope
+};
+
+// How mla_decode's work is cut (see mla_decode_plan.cuh).
+struct MlaDecodeShape {
+    int row_tile;   // query rows (token, head) a block works on
+    int key_tile;   // keys per tile
+    int grid;       // blocks
+};
+MlaDecodeShape mla_decode_shape(int B, int n, int H, int dc, int dr, kda_dtype_t dtype);
+size_t mla_decode_scratch(int B, int n, int H, int dc, int dr, kda_dtype_t dtype);
+
+// Tiles of `tile` rows over the sequences of a host offset array.
+inline int64_t count_tiles(const int32_t *cu, int n, int tile) {
+    int64_t s = 0;
+    for (int i = 0; i < n; ++i) s += (int64_t(cu[i + 1]) - cu[i] + tile - 1) / tile;
+    return s;
+}
+
+cudaError_t launch_mla_append(const MlaAppendArgs &a, cudaStream_t st);
+cudaError_t launch_mla_decode(const MlaDecodeArgs &a, cudaStream_t st);
+cudaError_t launch_mla_prefill_simt(const MlaArgs &a, cudaStream_t st);
+cudaError_t launch_mla_backward_simt(const MlaArgs &a, cudaStream_t st);
+cudaError_t launch_mla_delta(const MlaArgs &a, cudaStream_t st);
+cudaError_t launch_mla_dkr_reduce(const MlaArgs &a, cudaStream_t st);
+
+}  // namespace kda

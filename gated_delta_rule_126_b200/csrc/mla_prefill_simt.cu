@@ -1,0 +1,323 @@
+// mla_prefill and mla_backward on the CUDA cores, in float32: every type, head size and
+// stride the calls take.  64 x 64 tiles of scores, 256 threads with 4 x 4 scores each; the
+// softmax is kept online (running maximum and sum), so scores never leave the SM.  The
+// backward pass recomputes the scores from lse in two kernels, one per key tile (dk, dv)
+// and one per query tile (dq), so that every sum has one owner and no atomics.
+// Bound by the float32 FMA pipes.
+#include <cmath>
+
+#include "mla_internal.h"
+#include "mla_simt.cuh"
+
+namespace kda {
+namespace {
+
+constexpr int kT = 64;         // rows of queries and of keys per tile
+constexpr int kThreads = 256;  // 16 x 16
+constexpr int kLdP = kT + 4;
+
+struct Rows {  // one sequence's place
+    int q0, lq, k0, lk;
+};
+__device__ __forceinline__ Rows rows_of(const MlaArgs &a, int s) {
+    return Rows{a.cu_q[s], a.cu_q[s + 1] - a.cu_q[s], a.cu_k[s], a.cu_k[s + 1] - a.cu_k[s]};
+}
+
+template <typename T>
+__device__ __forceinline__ void load_q(float *Q, int ld, const MlaArgs &a, const Rows &w, int h, int i0) {
+    const int d = a.dn + a.dr, n = min(kT, w.lq - i0);
+    load_tile<T, kThreads>(Q, ld, 0, static_cast<const T *>(a.q) + (w.q0 + i0) * a.q_st + h * a.q_sh, a.q_st, d, kT, n);
+}
+template <typename T>
+__device__ __forceinline__ void load_k(float *K, int ld, const MlaArgs &a, const Rows &w, int h, int j0) {
+    const int n = min(kT, w.lk - j0);
+    load_tile<T, kThreads>(K, ld, 0, static_cast<const T *>(a.k) + (w.k0 + j0) * a.k_st + h * a.k_sh, a.k_st, a.dn, kT, n);
+    if (a.dr)
+        load_tile<T, kThreads>(K, ld, a.dn, static_cast<const T *>(a.k_rope) + (w.k0 + j0) * a.kr_st, a.kr_st, a.dr, kT, n);
+}
+template <typename T>
+__device__ __forceinline__ void load_v(float *V, int ld, const MlaArgs &a, const Rows &w, int h, int j0) {
+    const int n = min(kT, w.lk - j0);
+    load_tile<T, kThreads>(V, ld, 0, static_cast<const T *>(a.v) + (w.k0 + j0) * a.v_st + h * a.v_sh, a.v_st, a.dv, kT, n);
+}
+template <typename T>
+__device__ __forceinline__ void load_dO(float *D, int ld, const MlaArgs &a, const Rows &w, int h, int i0) {
+    const int n = min(kT, w.lq - i0);
+    load_tile<T, kThreads>(D, ld, 0, static_cast<const T *>(a.dO) + (int64_t(w.q0 + i0) * a.H + h) * a.dv,
+                           int64_t(a.H) * a.dv, a.dv, kT, n);
+}
+// Keys that query i may see end here (bottom-right causal).
+__device__ __forceinline__ int key_end(const MlaArgs &a, const Rows &w, int i) {
+    return a.causal ? max(0, min(w.lk, i + 1 + w.lk - w.lq)) : w.lk;
+}
+__device__ __forceinline__ float half_warp_max(float x) {
+#pragma unroll
+    for (int d = 8; d; d >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+    return x;
+}
+__device__ __forceinline__ float half_warp_sum(float x) {
+#pragma unroll
+    for (int d = 8; d; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+    return x;
+}
+
+template <typename T> __global__ void __launch_bounds__(kThreads) prefill_kernel(const MlaArgs a) {
+    extern __shared__ float sm[];
+    __shared__ int64_t buf[kThreads / 32 + 2];
+    const int d = a.dn + a.dr, d4 = (d + 3) & ~3, ldd = simt_row(d), ldv = simt_row(a.dv), h = blockIdx.y;
+    float *Q = sm, *K = Q + kT * ldd, *V = K + kT * ldd, *P = V + kT * ldv;
+    int seq, tile;
+    if (!find_tile<kThreads>(a.cu_q, a.num_seqs, kT, gridDim.x - 1 - blockIdx.x, buf, &seq, &tile)) return;
+    const Rows w = rows_of(a, seq);
+    const int i0 = tile * kT, tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+    zero_columns<kThreads>(Q, ldd, d, d4, kT);
+    zero_columns<kThreads>(K, ldd, d, d4, kT);
+    zero_columns<kThreads>(V, ldv, a.dv, (a.dv + 3) & ~3, kT);
+    load_q<T>(Q, ldd, a, w, h, i0);
+    float m[4], l[4], o[4][8] = {};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m[i] = -INFINITY, l[i] = 0.f;
+    const int last = key_end(a, w, min(i0 + kT, w.lq) - 1);
+    for (int j0 = 0; j0 < last; j0 += kT) {
+        __syncthreads();
+        load_k<T>(K, ldd, a, w, h, j0);
+        load_v<T>(V, ldv, a, w, h, j0);
+        __syncthreads();
+        float s[4][4] = {};
+        tile_dot(s, Q, ldd, K, ldd, d4, ty, tx);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int end = key_end(a, w, i0 + 4 * ty + i) - j0;
+            float top = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                s[i][j] = tx + 16 * j < end ? s[i][j] * a.scale : -INFINITY;
+                top = fmaxf(top, s[i][j]);
+            }
+            top = fmaxf(m[i], half_warp_max(top));
+            const float base = top == -INFINITY ? 0.f : top;  // nothing seen yet: exp(-inf) = 0 throughout
+            const float keep = expf(m[i] - base);
+            float sum = 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float p = expf(s[i][j] - base);
+                P[(4 * ty + i) * kLdP + tx + 16 * j] = p;
+                sum += p;
+            }
+            l[i] = l[i] * keep + half_warp_sum(sum);
+            m[i] = top;
+#pragma unroll
+            for (int c = 0; c < 8; ++c) o[i][c] *= keep;
+        }
+        __syncwarp();  // a row of P is written and read by the same half warp
+        tile_apply<2>(o, P, kLdP, V, ldv, a.dv, ty, tx);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = i0 + 4 * ty + i;
+        if (r >= w.lq) continue;
+        const float inv = l[i] > 0.f ? 1.f / l[i] : 0.f;
+        T *out = static_cast<T *>(a.o) + (int64_t(w.q0 + r) * a.H + h) * a.dv;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            const int col = (c >> 2) * 64 + 4 * tx + (c & 3);
+            // a NaN among the seen scores makes l NaN: it reaches the output
+            if (col < a.dv) out[col] = from_f32<T>(l[i] == 0.f ? 0.f : l[i] > 0.f ? o[i][c] * inv : l[i]);
+        }
+        if (a.lse && tx == 0) a.lse[int64_t(w.q0 + r) * a.H + h] = m[i] == -INFINITY && l[i] == 0.f ? -INFINITY : m[i] + logf(l[i]);
+    }
+}
+
+// P and dS of one tile, from the recomputed scores: p = exp(s - lse), ds = p (dp - delta) scale.
+template <typename T>
+__device__ __forceinline__ void tile_grads(const MlaArgs &a, const Rows &w, int h, int i0, int j0, const float *Q,
+                                           const float *K, const float *V, const float *D, int ldd, int ldv, int d4,
+                                           int dv4, int ty, int tx, float (&p)[4][4], float (&ds)[4][4]) {
+    float s[4][4] = {}, dp[4][4] = {};
+    tile_dot(s, Q, ldd, K, ldd, d4, ty, tx);
+    tile_dot(dp, D, ldv, V, ldv, dv4, ty, tx);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = i0 + 4 * ty + i;
+        const bool in = r < w.lq;
+        const int end = in ? key_end(a, w, r) - j0 : 0;
+        const int64_t at = int64_t(w.q0 + r) * a.H + h;
+        const float lse = in ? a.lse[at] : 0.f, delta = in ? a.delta[at] : 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const bool seen = tx + 16 * j < end;
+            p[i][j] = seen ? expf(s[i][j] * a.scale - lse) : 0.f;
+            ds[i][j] = seen ? p[i][j] * (dp[i][j] - delta) * a.scale : 0.f;
+        }
+    }
+}
+
+template <typename T> __global__ void __launch_bounds__(kThreads) dkv_kernel(const MlaArgs a) {
+    extern __shared__ float sm[];
+    __shared__ int64_t buf[kThreads / 32 + 2];
+    const int d = a.dn + a.dr, d4 = (d + 3) & ~3, dv4 = (a.dv + 3) & ~3, h = blockIdx.y;
+    const int ldd = simt_row(d), ldv = simt_row(a.dv);
+    float *Q = sm, *K = Q + kT * ldd, *V = K + kT * ldd, *D = V + kT * ldv, *Pt = D + kT * ldv, *St = Pt + kT * kLdP;
+    int seq, tile;
+    if (!find_tile<kThreads>(a.cu_k, a.num_seqs, kT, blockIdx.x, buf, &seq, &tile)) return;
+    const Rows w = rows_of(a, seq);
+    const int j0 = tile * kT, tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+    zero_columns<kThreads>(Q, ldd, d, d4, kT);
+    zero_columns<kThreads>(K, ldd, d, d4, kT);
+    zero_columns<kThreads>(V, ldv, a.dv, dv4, kT);
+    zero_columns<kThreads>(D, ldv, a.dv, dv4, kT);
+    load_k<T>(K, ldd, a, w, h, j0);
+    load_v<T>(V, ldv, a, w, h, j0);
+    float dk[4][12] = {}, dv[4][8] = {};
+    // the first query that sees key j0
+    const int first = a.causal ? max(0, j0 - (w.lk - w.lq)) / kT * kT : 0;
+    for (int i0 = first; i0 < w.lq; i0 += kT) {
+        __syncthreads();
+        load_q<T>(Q, ldd, a, w, h, i0);
+        load_dO<T>(D, ldv, a, w, h, i0);
+        __syncthreads();
+        float p[4][4], ds[4][4];
+        tile_grads<T>(a, w, h, i0, j0, Q, K, V, D, ldd, ldv, d4, dv4, ty, tx, p, ds);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                Pt[(tx + 16 * j) * kLdP + 4 * ty + i] = p[i][j];
+                St[(tx + 16 * j) * kLdP + 4 * ty + i] = ds[i][j];
+            }
+        __syncthreads();
+        tile_apply<2>(dv, Pt, kLdP, D, ldv, a.dv, ty, tx);
+        tile_apply<3>(dk, St, kLdP, Q, ldd, d, ty, tx);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = j0 + 4 * ty + i;
+        if (r >= w.lk) continue;
+        const int64_t at = int64_t(w.k0 + r) * a.H + h;
+#pragma unroll
+        for (int c = 0; c < 12; ++c) {
+            const int col = (c >> 2) * 64 + 4 * tx + (c & 3);
+            if (col < a.dn) static_cast<T *>(a.dk)[at * a.dn + col] = from_f32<T>(dk[i][c]);
+            else if (col < d) a.dkr_partial[(int64_t(h) * a.Tk + w.k0 + r) * a.dr + col - a.dn] = dk[i][c];
+            if (c < 8 && col < a.dv) static_cast<T *>(a.dv_out)[at * a.dv + col] = from_f32<T>(dv[i][c & 7]);
+        }
+    }
+}
+
+template <typename T> __global__ void __launch_bounds__(kThreads) dq_kernel(const MlaArgs a) {
+    extern __shared__ float sm[];
+    __shared__ int64_t buf[kThreads / 32 + 2];
+    const int d = a.dn + a.dr, d4 = (d + 3) & ~3, dv4 = (a.dv + 3) & ~3, h = blockIdx.y;
+    const int ldd = simt_row(d), ldv = simt_row(a.dv);
+    float *Q = sm, *K = Q + kT * ldd, *V = K + kT * ldd, *D = V + kT * ldv, *S = D + kT * ldv;
+    int seq, tile;
+    if (!find_tile<kThreads>(a.cu_q, a.num_seqs, kT, gridDim.x - 1 - blockIdx.x, buf, &seq, &tile)) return;
+    const Rows w = rows_of(a, seq);
+    const int i0 = tile * kT, tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+    zero_columns<kThreads>(Q, ldd, d, d4, kT);
+    zero_columns<kThreads>(K, ldd, d, d4, kT);
+    zero_columns<kThreads>(V, ldv, a.dv, dv4, kT);
+    zero_columns<kThreads>(D, ldv, a.dv, dv4, kT);
+    load_q<T>(Q, ldd, a, w, h, i0);
+    load_dO<T>(D, ldv, a, w, h, i0);
+    float dq[4][12] = {};
+    const int last = key_end(a, w, min(i0 + kT, w.lq) - 1);
+    for (int j0 = 0; j0 < last; j0 += kT) {
+        __syncthreads();
+        load_k<T>(K, ldd, a, w, h, j0);
+        load_v<T>(V, ldv, a, w, h, j0);
+        __syncthreads();
+        float p[4][4], ds[4][4];
+        tile_grads<T>(a, w, h, i0, j0, Q, K, V, D, ldd, ldv, d4, dv4, ty, tx, p, ds);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) S[(4 * ty + i) * kLdP + tx + 16 * j] = ds[i][j];
+        __syncwarp();
+        tile_apply<3>(dq, S, kLdP, K, ldd, d, ty, tx);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = i0 + 4 * ty + i;
+        if (r >= w.lq) continue;
+        T *out = static_cast<T *>(a.dq) + (int64_t(w.q0 + r) * a.H + h) * d;
+#pragma unroll
+        for (int c = 0; c < 12; ++c) {
+            const int col = (c >> 2) * 64 + 4 * tx + (c & 3);
+            if (col < d) out[col] = from_f32<T>(dq[i][c]);
+        }
+    }
+}
+
+// delta[t][h] = sum_c dO o, one warp per (token, head) of the sequences' rows.
+template <typename T> __global__ void delta_kernel(const MlaArgs a) {
+    const int64_t row = int64_t(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
+    if (row >= a.Tq * a.H) return;
+    const T *x = static_cast<const T *>(a.dO) + row * a.dv, *y = static_cast<const T *>(a.o) + row * a.dv;
+    float s = 0.f;
+    for (int c = threadIdx.x & 31; c < a.dv; c += 32) s = fmaf(to_f32(x[c]), to_f32(y[c]), s);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if ((threadIdx.x & 31) == 0) a.delta[row] = s;
+}
+
+// dk_rope[t][c] = sum_h partial[h][t][c], in the order of the heads.
+template <typename T> __global__ void dkr_kernel(const MlaArgs a) {
+    const int64_t n = a.Tk * a.dr, i = int64_t(blockIdx.x) * blockDim.x + threadIdx.x;
+    if (i >= n) return;
+    float s = 0.f;
+    for (int h = 0; h < a.H; ++h) s += a.dkr_partial[h * n + i];
+    static_cast<T *>(a.dk_rope)[i] = from_f32<T>(s);
+}
+
+size_t prefill_smem(const MlaArgs &a) {
+    return sizeof(float) * kT * (2 * simt_row(a.dn + a.dr) + simt_row(a.dv) + kLdP);
+}
+size_t dq_smem(const MlaArgs &a) {
+    return sizeof(float) * kT * (2 * simt_row(a.dn + a.dr) + 2 * simt_row(a.dv) + kLdP);
+}
+size_t dkv_smem(const MlaArgs &a) { return dq_smem(a) + sizeof(float) * kT * kLdP; }
+
+template <typename K> cudaError_t launch(K *kernel, int64_t tiles, size_t smem, const MlaArgs &a, cudaStream_t st) {
+    if (tiles == 0) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    if (e != cudaSuccess) return e;
+    kernel<<<dim3(unsigned(tiles), unsigned(a.H)), kThreads, smem, st>>>(a);
+    return cudaGetLastError();
+}
+
+template <typename T> cudaError_t backward(const MlaArgs &a, cudaStream_t st) {
+    cudaError_t e = launch(dkv_kernel<T>, count_tiles(a.cu_k_host, a.num_seqs, kT), dkv_smem(a), a, st);
+    if (e == cudaSuccess) e = launch(dq_kernel<T>, count_tiles(a.cu_q_host, a.num_seqs, kT), dq_smem(a), a, st);
+    return e;
+}
+
+}  // namespace
+
+cudaError_t launch_mla_prefill_simt(const MlaArgs &a, cudaStream_t st) {
+    const int64_t tiles = count_tiles(a.cu_q_host, a.num_seqs, kT);
+    return a.dtype == KDA_DTYPE_F32 ? launch(prefill_kernel<float>, tiles, prefill_smem(a), a, st)
+                                    : launch(prefill_kernel<__nv_bfloat16>, tiles, prefill_smem(a), a, st);
+}
+
+cudaError_t launch_mla_delta(const MlaArgs &a, cudaStream_t st) {
+    const int64_t blocks = (a.Tq * a.H + 7) / 8;
+    if (blocks == 0) return cudaSuccess;
+    if (a.dtype == KDA_DTYPE_F32) delta_kernel<float><<<unsigned(blocks), 256, 0, st>>>(a);
+    else delta_kernel<__nv_bfloat16><<<unsigned(blocks), 256, 0, st>>>(a);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_mla_dkr_reduce(const MlaArgs &a, cudaStream_t st) {
+    const int64_t blocks = (a.Tk * a.dr + 255) / 256;
+    if (blocks == 0) return cudaSuccess;
+    if (a.dtype == KDA_DTYPE_F32) dkr_kernel<float><<<unsigned(blocks), 256, 0, st>>>(a);
+    else dkr_kernel<__nv_bfloat16><<<unsigned(blocks), 256, 0, st>>>(a);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_mla_backward_simt(const MlaArgs &a, cudaStream_t st) {
+    return a.dtype == KDA_DTYPE_F32 ? backward<float>(a, st) : backward<__nv_bfloat16>(a, st);
+}
+
+}  // namespace kda

@@ -1,0 +1,123 @@
+// Building blocks of the latent-attention kernels that run on the CUDA cores in float32:
+// tile loads with conversion, and register-tiled products over shared-memory tiles.
+#pragma once
+
+#include "mla_internal.h"
+
+namespace kda {
+
+template <typename T> __device__ __forceinline__ float to_f32(T x);
+template <> __device__ __forceinline__ float to_f32<float>(float x) { return x; }
+template <> __device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 x) { return __bfloat162float(x); }
+template <typename T> __device__ __forceinline__ T from_f32(float x);
+template <> __device__ __forceinline__ float from_f32<float>(float x) { return x; }
+template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+
+// Row length in floats of a shared tile of d channels: at least d, and 4 more than a
+// multiple of 32, so that eight neighbouring rows' float4 loads touch all 32 banks.
+__host__ __device__ constexpr int simt_row(int d) { return (d + 31) / 32 * 32 + 4; }
+
+// The sequence and tile of block x when every sequence's rows are cut into tiles of `tile`
+// rows, numbered in sequence order.  Called by all NT threads; `buf` holds NT / 32 + 2 int64.  False when x lies
+// behind the last tile.
+template <int NT>
+__device__ bool find_tile(const int32_t *cu, int num_seqs, int tile, int64_t x, int64_t *buf, int *seq, int *index) {
+    const int per = (num_seqs + NT - 1) / NT;
+    const int s0 = threadIdx.x * per, s1 = min(num_seqs, s0 + per);
+    int64_t own = 0;
+    for (int s = s0; s < s1; ++s) own += (cu[s + 1] - cu[s] + tile - 1) / tile;
+    int64_t scan = own;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int64_t o = __shfl_up_sync(0xffffffffu, scan, d);
+        if ((threadIdx.x & 31) >= d) scan += o;
+    }
+    if ((threadIdx.x & 31) == 31) buf[threadIdx.x >> 5] = scan;
+    __syncthreads();
+    int64_t total = 0;
+    for (int w = 0; w < NT / 32; ++w) {
+        if (w < int(threadIdx.x >> 5)) scan += buf[w];
+        total += buf[w];
+    }
+    if (x >= total) return false;
+    if (own > 0 && scan - own <= x && x < scan) {
+        int64_t at = scan - own;
+        int s = s0;
+        for (; s < s1; ++s) {
+            const int64_t nt = (cu[s + 1] - cu[s] + tile - 1) / tile;
+            if (x < at + nt) break;
+            at += nt;
+        }
+        buf[NT / 32] = s;
+        buf[NT / 32 + 1] = x - at;
+    }
+    __syncthreads();
+    *seq = int(buf[NT / 32]);
+    *index = int(buf[NT / 32 + 1]);
+    return true;
+}
+
+// dst[r][at + c] = src[r * stride + c] for r < rows, c < width, as float32; rows from `valid` on are zero.
+template <typename T, int NT>
+__device__ __forceinline__ void load_tile(float *dst, int ld, int at, const T *src, int64_t stride, int width, int rows,
+                                          int valid) {
+    for (int i = threadIdx.x; i < rows * width; i += NT) {
+        const int r = i / width, c = i - r * width;
+        dst[r * ld + at + c] = r < valid ? to_f32(src[r * stride + c]) : 0.f;
+    }
+}
+// Zeroes columns [from, to) of every row.
+template <int NT> __device__ __forceinline__ void zero_columns(float *dst, int ld, int from, int to, int rows) {
+    const int w = to - from;
+    for (int i = threadIdx.x; i < rows * w; i += NT) dst[(i / w) * ld + from + i % w] = 0.f;
+}
+
+// acc[i][j] += sum_c A[4 ty + i][c] * B[tx + 16 j][c] over c < d4 (a multiple of 4).
+__device__ __forceinline__ void tile_dot(float (&acc)[4][4], const float *A, int lda, const float *B, int ldb, int d4,
+                                         int ty, int tx) {
+    for (int c = 0; c < d4; c += 4) {
+        float4 x[4], y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const float4 *>(A + (4 * ty + i) * lda + c);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[j] = *reinterpret_cast<const float4 *>(B + (tx + 16 * j) * ldb + c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                acc[i][j] = fmaf(x[i].x, y[j].x, acc[i][j]);
+                acc[i][j] = fmaf(x[i].y, y[j].y, acc[i][j]);
+                acc[i][j] = fmaf(x[i].z, y[j].z, acc[i][j]);
+                acc[i][j] = fmaf(x[i].w, y[j].w, acc[i][j]);
+            }
+    }
+}
+
+// acc[i][4 j + e] += sum_r P[4 ty + i][r] * B[r][64 j + 4 tx + e] over r < 64, for the j with 64 j + 4 tx < width.
+template <int J>
+__device__ __forceinline__ void tile_apply(float (&acc)[4][4 * J], const float *P, int ldp, const float *B, int ldb,
+                                           int width, int ty, int tx) {
+    for (int r = 0; r < 64; r += 4) {
+        float4 p[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p[i] = *reinterpret_cast<const float4 *>(P + (4 * ty + i) * ldp + r);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                if (64 * j + 4 * tx < width) {
+                    const float4 b = *reinterpret_cast<const float4 *>(B + (r + e) * ldb + 64 * j + 4 * tx);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float w = e == 0 ? p[i].x : e == 1 ? p[i].y : e == 2 ? p[i].z : p[i].w;
+                        acc[i][4 * j + 0] = fmaf(w, b.x, acc[i][4 * j + 0]);
+                        acc[i][4 * j + 1] = fmaf(w, b.y, acc[i][4 * j + 1]);
+                        acc[i][4 * j + 2] = fmaf(w, b.z, acc[i][4 * j + 2]);
+                        acc[i][4 * j + 3] = fmaf(w, b.w, acc[i][4 * j + 3]);
+                    }
+                }
+            }
+    }
+}
+
+}  // namespace kda

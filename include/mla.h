@@ -1,0 +1,170 @@
+/*
+ * mla.h -- C ABI of the latent-attention (MLA) layer's operators on B200 (sm_100a), in
+ * the same library as kda.h.
+ *
+ * The wiki page "Kimi Linear 高效注意力架构" (section "模型架构") describes a hybrid stack
+ * in which three of four layers run KDA and the fourth is multi-head latent attention:
+ * softmax attention whose keys and values of every head come from one latent vector
+ * c_t (d_latent channels) a token, next to a key part kr_t (d_rope channels) that all
+ * heads share.  In a stack without position rotation kr_t is simply not rotated
+ * (inv_freq = NULL); d_rope = 0 leaves it out.  These calls are that layer's operators:
+ *
+ *   mla_append    RMSNorm of the latent, rotation of kr and of the queries' shared part,
+ *                 rows [c | kr] written to a paged cache
+ *   mla_decode    attention of a few new tokens per sequence over the paged cache, in the
+ *                 absorbed form: queries already multiplied by the key expansion, output in
+ *                 the latent space
+ *   mla_prefill   attention over packed sequences in the expanded form (per-head keys and
+ *                 values, shared kr)
+ *   mla_backward  its gradients
+ *
+ * Conventions are kda.h's: DEVICE pointers to caller-owned memory except *_host, work
+ * queued on `stream`, argument errors found on the host before anything is queued, no
+ * call aborts, throws, prints or allocates device memory.  `dtype` is the type of every
+ * tensor not said to be float32 or int32.  Strides count ELEMENTS; the last dimension is
+ * always contiguous.  Outputs must not overlap inputs unless said otherwise.
+ */
+#ifndef KDA_B200_MLA_H
+#define KDA_B200_MLA_H
+
+#include "kda.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/*
+ * mla_append -- for token t = cu_seqlens[b] + i of sequence b, at position
+ * p = past_lens[b] + i:
+ *
+ *   c'[t]  = c[t] / sqrt(mean_j c[t][j]^2 + eps) * norm_weight      (c itself when norm_weight = NULL)
+ *   kr'[t] = rot_p(k_rope[t]),  q'[t][h] = rot_p(q_rope[t][h])      (unrotated when inv_freq = NULL)
+ *   cache[page_table[b][p / page_size]][p % page_size] = [c'[t] | kr'[t]]
+ *
+ * rot_p turns the pairs (x_i, y_i) by the angle p * inv_freq[i], i < d_rope / 2:
+ * (x cos - y sin, x sin + y cos).  interleaved = 0 pairs channel i with i + d_rope/2,
+ * interleaved = 1 pairs 2i with 2i + 1.  The angle is formed and reduced in float64, so
+ * far positions lose nothing; the norm is summed in float32; every output is rounded once.
+ *
+ *   c        [total_tokens, d_latent], token stride c_stride
+ *   k_rope   [total_tokens, d_rope], token stride k_rope_stride; ignored when d_rope = 0
+ *   norm_weight [d_latent] float32 or NULL;  inv_freq [d_rope / 2] float32 or NULL
+ *   cu_seqlens  int32 [num_seqs + 1] on the device; past_lens int32 [num_seqs] on the device
+ *   page_table  int32 [num_seqs, max_pages] on the device
+ *   cache    [num_pages, page_size, d_latent + d_rope], written at the new tokens' rows only
+ *   q_rope   [total_tokens, H, d_rope] with strides (q_stride_t, q_stride_h), or NULL
+ *   q_out    the rotated queries, strides (qo_stride_t, qo_stride_h); q_out = q_rope with
+ *            equal strides rotates in place
+ *   c_out, k_rope_out  packed [total_tokens, d_latent] and [total_tokens, d_rope] copies of
+ *            c' and kr', or NULL.  c_out = c with c_stride = d_latent and k_rope_out =
+ *            k_rope with k_rope_stride = d_rope work in place.
+ *
+ * A token whose position is negative, lies behind the page table's width, or whose page
+ * is outside [0, num_pages) writes no cache row (its other outputs are written).  Rows t
+ * behind cu_seqlens[num_seqs] are left alone.  Two tokens of one call must not share a
+ * cache row (their writes race).  Offsets and lengths are read on the device only, so a
+ * captured graph follows them.
+ * Supported: 1 <= d_latent <= 512, d_rope even and <= 64, page_size >= 1, H <= 65535.
+ */
+KDA_API kda_status_t mla_append(const void *c, int64_t c_stride, const void *k_rope, int64_t k_rope_stride,
+                        kda_dtype_t dtype, const float *norm_weight, float eps, const float *inv_freq,
+                        int interleaved, const int32_t *cu_seqlens_dev, const int32_t *past_lens, int num_seqs,
+                        int64_t total_tokens, const int32_t *page_table, int max_pages, void *cache,
+                        int num_pages, int page_size, int d_latent, int d_rope, const void *q_rope,
+                        int64_t q_stride_t, int64_t q_stride_h, int H, void *q_out, int64_t qo_stride_t,
+                        int64_t qo_stride_h, void *c_out, void *k_rope_out, kda_stream_t stream);
+
+/*
+ * Bytes of device workspace mla_decode needs for these sizes on the current device
+ * (0 for sizes it would reject).  It does not depend on the sequences' lengths.
+ */
+KDA_API size_t mla_decode_workspace_size(int B, int n, int H, int d_latent, int d_rope, kda_dtype_t dtype);
+
+/*
+ * mla_decode -- n new tokens of each of B sequences over the paged latent cache.  With
+ * row j of sequence b at cache[page_table[b][j / page_size]][j % page_size] and
+ * L = seq_lens[b] rows in all (the new tokens' own among them, already appended):
+ *
+ *   s_j = scale * <q[b][i][h], row_j>  for j < L - (n - 1 - i)     (token i sees itself and what precedes it)
+ *   o[b][i][h] = sum_j softmax(s)_j * row_j[0 : d_latent],   lse[b][i][h] = log sum_j exp(s_j)
+ *
+ *   q     [B, n, H, d_latent + d_rope]: each head's query in the cache's space
+ *   o     [B, n, H, d_latent];   lse [B, n, H] float32 or NULL
+ *   seq_lens int32 [B], page_table int32 [B, max_pages], both read on the device only
+ *   workspace  mla_decode_workspace_size bytes, 256-byte aligned, contents on entry
+ *              ignored; not to be shared by two calls that may run at the same time
+ *
+ * A token that sees no row (L = 0, or L < n for the first ones) gets o = 0 and
+ * lse = -inf.  Rows behind the page table's width, and pages outside [0, num_pages), are
+ * left out of the softmax.  Rows that no token sees are not read into any sum: they may
+ * hold anything, NaN included.  Work is split over the keys by a fixed rule, so repeated
+ * calls give identical results.
+ * Supported: 1 <= d_latent <= 512, 0 <= d_rope <= 64, n * H <= 65536, B <= 65536;
+ * q, cache and o 16-byte aligned.  bf16 with d_latent a multiple of 128 and d_rope 0 or
+ * 64 runs on the tensor cores, everything else on the CUDA cores in float32.
+ */
+KDA_API kda_status_t mla_decode(const void *q, kda_dtype_t dtype, const void *cache, int num_pages, int page_size,
+                        const int32_t *page_table, int max_pages, const int32_t *seq_lens, int B, int n, int H,
+                        int d_latent, int d_rope, float scale, void *o, float *lse, void *workspace,
+                        size_t workspace_bytes, kda_stream_t stream);
+
+/*
+ * mla_prefill -- attention over packed sequences, expanded form.  Sequence b has queries
+ * cu_q[b] .. cu_q[b+1] and keys cu_k[b] .. cu_k[b+1]; with causal = 1 query i of Lq sees
+ * key j of Lk when j <= i + Lk - Lq (the last query sees every key), with causal = 0 all:
+ *
+ *   s_ij = scale * (<q_i[0:d_nope], k_j> + <q_i[d_nope:], k_rope_j>)
+ *   o_i = sum_j softmax_j(s_ij) v_j,   lse_i = log sum_j exp(s_ij)
+ *
+ *   q       [Tq, H, d_nope + d_rope] strides (q_stride_t, q_stride_h)
+ *   k       [Tk, H, d_nope] strides (k_stride_t, k_stride_h); v [Tk, H, d_v] likewise (both
+ *           may be slices of one [Tk, H, d_nope + d_v] expansion)
+ *   k_rope  [Tk, d_rope] token stride k_rope_stride, shared by the heads; ignored if d_rope = 0
+ *   cu_*_dev / cu_*_host  int32 [num_seqs + 1], equal copies as in kda_prefill
+ *   o       [Tq, H, d_v] contiguous;   lse [Tq, H] float32 or NULL
+ *
+ * A query that sees no key gets o = 0 and lse = -inf.  Rows outside the sequences are not
+ * read into any sum and not written.
+ * Supported: d_nope and d_v in 1..128, 0 <= d_rope <= 64.  bf16 with d_nope = d_v = 128,
+ * d_rope 0 or 64, strides that are multiples of 8 and 16-byte aligned tensors runs on
+ * the tensor cores (probabilities rounded to bf16, sums in float32), everything else on
+ * the CUDA cores in float32.
+ */
+KDA_API kda_status_t mla_prefill(const void *q, int64_t q_stride_t, int64_t q_stride_h, const void *k,
+                         int64_t k_stride_t, int64_t k_stride_h, const void *k_rope, int64_t k_rope_stride,
+                         const void *v, int64_t v_stride_t, int64_t v_stride_h, kda_dtype_t dtype,
+                         const int32_t *cu_q_dev, const int32_t *cu_q_host, const int32_t *cu_k_dev,
+                         const int32_t *cu_k_host, int num_seqs, int H, int d_nope, int d_rope, int d_v,
+                         float scale, int causal, void *o, float *lse, kda_stream_t stream);
+
+/* Bytes of device workspace mla_backward needs (0 for sizes it would reject). */
+KDA_API size_t mla_backward_workspace_size(int64_t total_q, int64_t total_k, int H, int d_nope, int d_rope, int d_v,
+                                   kda_dtype_t dtype);
+
+/*
+ * mla_backward -- gradients of mla_prefill.  Inputs as there, plus its outputs o and lse
+ * and dO = dL/do [Tq, H, d_v] contiguous.  Writes, in `dtype` and contiguous, every row
+ * that belongs to a sequence:
+ *
+ *   dq [Tq, H, d_nope + d_rope]   dk [Tk, H, d_nope]   dv [Tk, H, d_v]
+ *   dk_rope [Tk, d_rope] (summed over the heads in float32; ignored if d_rope = 0)
+ *
+ * No atomics: repeated calls give identical results.  The paths are chosen as in
+ * mla_prefill (dO, o and the outputs 16-byte aligned for the tensor cores; there P and dS
+ * are rounded to bf16 for their products, all sums are float32).
+ * workspace: mla_backward_workspace_size bytes, 256-byte aligned, contents ignored.
+ */
+KDA_API kda_status_t mla_backward(const void *q, int64_t q_stride_t, int64_t q_stride_h, const void *k,
+                          int64_t k_stride_t, int64_t k_stride_h, const void *k_rope, int64_t k_rope_stride,
+                          const void *v, int64_t v_stride_t, int64_t v_stride_h, kda_dtype_t dtype,
+                          const int32_t *cu_q_dev, const int32_t *cu_q_host, const int32_t *cu_k_dev,
+                          const int32_t *cu_k_host, int num_seqs, int H, int d_nope, int d_rope, int d_v,
+                          float scale, int causal, const void *o, const float *lse, const void *dO, void *dq,
+                          void *dk, void *dk_rope, void *dv, void *workspace, size_t workspace_bytes,
+                          kda_stream_t stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* KDA_B200_MLA_H */
