@@ -24,7 +24,7 @@ operators (``include/mla.h``, same library) stand beside it:
 * ``mla_decode``   -- absorbed attention of a few new tokens per sequence over that cache;
 * ``mla_prefill``  -- expanded attention over packed sequences;
 * ``mla_backward`` -- its gradients;
-* ``mla_decode_workspace_size``, ``mla_backward_workspace_size``.
+* ``mla_decode_workspace_size``, ``mla_backward_workspace_size``, ``mla_status``.
 
 ``inputs`` holds the seeded synthetic input generators.  Importing the package
 does not load the CUDA library; the first call does, and raises if it is missing.
@@ -33,9 +33,9 @@ from ._binding import (KdaError, backward_workspace_size, kda_backward, kda_deco
                        kda_decode_tokens, kda_prefill, kda_prefill_gated, kda_prologue, load,
                        prefill_workspace_size, wait_timeout_selftest, workspace_status)
 from ._mla_binding import (mla_append, mla_backward, mla_backward_workspace_size, mla_decode,
-                           mla_decode_workspace_size, mla_prefill)
+                           mla_decode_workspace_size, mla_prefill, mla_status)
 
 __all__ = ["KdaError", "backward_workspace_size", "kda_backward", "kda_decode_step", "kda_decode_tokens",
            "kda_prefill", "kda_prefill_gated", "kda_prologue", "load", "mla_append", "mla_backward",
            "mla_backward_workspace_size", "mla_decode", "mla_decode_workspace_size", "mla_prefill",
-           "prefill_workspace_size", "wait_timeout_selftest", "workspace_status"]
+           "mla_status", "prefill_workspace_size", "wait_timeout_selftest", "workspace_status"]

@@ -33,6 +33,8 @@ def _lib():
         lib.mla_backward_workspace_size.argtypes = [i64, i64] + [i32] * 5
         lib.mla_backward.restype = i32
         lib.mla_backward.argtypes = packed + [vp] * 8 + [sz, vp]
+        lib.mla_status.restype = i32
+        lib.mla_status.argtypes = [vp]
         _declared = lib
     return lib
 
@@ -285,3 +287,8 @@ def mla_backward(q, k, v, cu_q, cu_k, o, lse, dO, k_rope=None, scale=None, causa
                               workspace.numel() * workspace.element_size(), _stream_handle(use))
     _check(st, "mla_backward")
     return out
+
+
+def mla_status(stream=None):
+    """Waits for the stream; the status flagged by the mla_* kernels run so far on the current device (0 = fine)."""
+    return int(_lib().mla_status(_stream_handle(stream)))

@@ -194,4 +194,10 @@ kda_status_t mla_backward(const void *q, int64_t q_stride_t, int64_t q_stride_h,
     return from_cuda(e);
 }
 
+kda_status_t mla_status(kda_stream_t stream) {
+    unsigned int f = 0;
+    if (kda::mla_decode_fault(reinterpret_cast<cudaStream_t>(stream), &f) != cudaSuccess) return KDA_ERR_CUDA;
+    return f ? KDA_ERR_DEVICE_FAULT : KDA_OK;
+}
+
 }  // extern "C"

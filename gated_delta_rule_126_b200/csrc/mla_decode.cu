@@ -12,11 +12,6 @@
 
 namespace kda {
 
-int device_sm_count();
-bool mla_decode_tc_supported(int n, int H, int dc, int dr, kda_dtype_t dtype);
-MlaDecodeShape mla_decode_tc_shape(int n, int H);
-cudaError_t launch_mla_decode_tc(const MlaDecodeArgs &a, const MlaDecodeShape &s, cudaStream_t st);
-
 namespace {
 
 constexpr int kThreads = 256;
@@ -29,45 +24,29 @@ template <typename T>
 __global__ void __launch_bounds__(kThreads) decode_kernel(const MlaDecodeArgs a, const MlaDecodeShape shape) {
     extern __shared__ float sm[];
     __shared__ int64_t buf[kThreads / 32 + 4];
-    const int W = a.dc + a.dr, W4 = (W + 3) & ~3, ld = simt_row(W), R = a.n * a.H, RT = (R + kRows - 1) / kRows;
+    const int W = a.dc + a.dr, W4 = (W + 3) & ~3, ld = simt_row(W), R = a.n * a.H;
     float *Q = sm, *K = Q + kRows * ld, *P = K + kKeys * ld, *Keep = P + kKeys * kRows, *M = Keep + kRows, *L = M + kRows;
     const int tid = threadIdx.x, sr = tid >> 4, sk = tid & 15;
     MlaJoin *join = static_cast<MlaJoin *>(a.workspace);
-    float *slots = reinterpret_cast<float *>(static_cast<char *>(a.workspace) + mla_meta_bytes(shape.grid));
+    float *slots = reinterpret_cast<float *>(static_cast<char *>(a.workspace) + mla_meta_bytes(gridDim.x));
     const size_t slot_floats = mla_slot_floats(kRows, a.dc);
+    const int group = blockIdx.x / shape.row_tiles, r0 = (blockIdx.x % shape.row_tiles) * kRows, rows = min(kRows, R - r0);
 
-    const MlaRun run = mla_find_run<kThreads>(a, RT, kKeys, buf);
-    // sequences without a key
-    for (int b = blockIdx.x; b < a.B; b += gridDim.x)
-        if (mla_len(a, b) == 0) {
-            for (int64_t i = tid; i < int64_t(R) * a.dc; i += kThreads)
-                static_cast<T *>(a.o)[int64_t(b) * R * a.dc + i] = from_f32<T>(0.f);
-            if (a.lse)
-                for (int i = tid; i < R; i += kThreads) a.lse[int64_t(b) * R + i] = -INFINITY;
-        }
+    const MlaRun run = mla_find_run<kThreads>(a, group, shape.groups, kKeys, buf);
+    mla_empty_sequences<T, kThreads>(a, group, shape.groups, r0, rows);
     if (tid == 0) join[blockIdx.x].parts = 0;
-    if (int(blockIdx.x) >= run.grid) return;
+    if (group >= run.groups) return;
     zero_columns<kThreads>(Q, ld, W, W4, kRows);
     zero_columns<kThreads>(K, ld, W, W4, kKeys);
 
-    int b = run.b;
-    int64_t before = run.before;  // tiles of the sequences before b
-    for (int64_t x = run.start; x < run.end;) {
-        const int len = mla_len(a, b), nt = (len + kKeys - 1) / kKeys;
-        if (x >= before + int64_t(nt) * RT) {
-            before += int64_t(nt) * RT;
-            ++b;
-            continue;
-        }
-        const int rt = int((x - before) / nt);
-        const int64_t item = before + int64_t(rt) * nt;  // the item's first tile
-        const int t0 = int(x - item), t1 = int(min(int64_t(nt), run.end - item));
-        const int r0 = rt * kRows, rows = min(kRows, R - r0);
+    MlaWalk w(run);
+    while (w.next(a, kKeys, run)) {
+        const int b = w.b, len = w.len;
         __syncthreads();
         load_tile<T, kThreads>(Q, ld, 0, static_cast<const T *>(a.q) + (int64_t(b) * R + r0) * W, W, W, kRows, rows);
         float m = -INFINITY, l = 0.f;  // of row sr, the same in its 16 threads
         float o[kRows][2] = {};        // columns tid and tid + 256
-        for (int t = t0; t < t1; ++t) {
+        for (int t = w.t0; t < w.t1; ++t) {
             const int j0 = t * kKeys;
             __syncthreads();
             for (int i = tid; i < kKeys * W; i += kThreads) {
@@ -145,8 +124,7 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(const MlaDecodeArgs a,
         }
         if (sk == 0) M[sr] = m, L[sr] = l;
         __syncthreads();
-        const bool whole = t0 == 0 && t1 == nt;
-        if (whole) {
+        if (w.whole()) {
             T *out = static_cast<T *>(a.o) + (int64_t(b) * R + r0) * a.dc;
 #pragma unroll
             for (int r = 0; r < kRows; ++r)
@@ -158,8 +136,7 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(const MlaDecodeArgs a,
             if (a.lse && tid < rows)
                 a.lse[int64_t(b) * R + r0 + tid] = L[tid] == 0.f ? -INFINITY : M[tid] + logf(L[tid]);
         } else {
-            const int slot = 2 * blockIdx.x + (x == run.start ? 0 : 1);
-            float *p = slots + slot * slot_floats;
+            float *p = slots + mla_slot(w) * slot_floats;
 #pragma unroll
             for (int r = 0; r < kRows; ++r) {
                 if (tid < a.dc) p[r * a.dc + tid] = o[r][0];
@@ -169,12 +146,8 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(const MlaDecodeArgs a,
                 p[kRows * a.dc + 2 * tid] = M[tid];
                 p[kRows * a.dc + 2 * tid + 1] = L[tid];
             }
-            if (t0 == 0 && tid == 0) {  // the item begins here: this block's entry names it
-                const int last = mla_block_of(item + nt - 1, run.total, run.grid);
-                join[blockIdx.x] = MlaJoin{last - int(blockIdx.x) + 1, b, rt, slot};
-            }
+            if (w.t0 == 0 && tid == 0) join[blockIdx.x] = mla_join_entry(w, run, group);
         }
-        x = item + t1;
     }
 }
 
@@ -186,14 +159,14 @@ template <typename T>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const MlaDecodeArgs a, const MlaDecodeShape shape) {
     __shared__ float acc[4][512];
     __shared__ float top[kJoinThreads / 32], sums[kJoinThreads / 32];
-    const int g = blockIdx.x, row = blockIdx.y, tid = threadIdx.x;
-    const MlaJoin j = static_cast<const MlaJoin *>(a.workspace)[g];
+    const int x = blockIdx.x, row = blockIdx.y, tid = threadIdx.x;
+    const MlaJoin j = static_cast<const MlaJoin *>(a.workspace)[x];
     if (j.parts == 0) return;
-    const int R = a.n * a.H, r0 = j.row_tile * shape.row_tile;
+    const int R = a.n * a.H, r0 = (x % shape.row_tiles) * shape.row_tile;
     if (r0 + row >= R) return;
-    const float *slots = reinterpret_cast<const float *>(static_cast<const char *>(a.workspace) + mla_meta_bytes(shape.grid));
+    const float *slots = reinterpret_cast<const float *>(static_cast<const char *>(a.workspace) + mla_meta_bytes(gridDim.x));
     const size_t slot_floats = mla_slot_floats(shape.row_tile, a.dc);
-    auto part = [&](int i) { return slots + size_t(i == 0 ? j.first_slot : 2 * (g + i)) * slot_floats; };
+    auto part = [&](int i) { return slots + size_t(i == 0 ? j.first_slot : 2 * (x + i * shape.row_tiles)) * slot_floats; };
     const int ml = shape.row_tile * a.dc + 2 * row;
     float m = -INFINITY;
     for (int i = tid; i < j.parts; i += kJoinThreads) m = fmaxf(m, part(i)[ml]);
@@ -235,27 +208,35 @@ template <typename T> cudaError_t launch_simt(const MlaDecodeArgs &a, const MlaD
     const size_t smem = simt_smem(a.dc + a.dr);
     const cudaError_t e = cudaFuncSetAttribute(decode_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
     if (e != cudaSuccess) return e;
-    decode_kernel<T><<<s.grid, kThreads, smem, st>>>(a, s);
+    decode_kernel<T><<<s.grid(), kThreads, smem, st>>>(a, s);
     return cudaGetLastError();
+}
+
+MlaDecodeShape simt_shape(int n, int H) {  // two blocks fit on an SM
+    const int tiles = (n * H + kRows - 1) / kRows, groups = 2 * device_sm_count() / tiles;
+    return MlaDecodeShape{false, kRows, tiles, groups > 1 ? groups : 1};
+}
+
+size_t scratch(const MlaDecodeShape &s, int dc) {
+    return mla_meta_bytes(s.grid()) + 2 * size_t(s.grid()) * mla_slot_floats(s.row_tile, dc) * sizeof(float);
 }
 
 }  // namespace
 
-MlaDecodeShape mla_decode_shape(int B, int n, int H, int dc, int dr, kda_dtype_t dtype) {
-    (void)B;
-    return MlaDecodeShape{kRows, kKeys, 2 * device_sm_count()};
-}
-
 size_t mla_decode_scratch(int B, int n, int H, int dc, int dr, kda_dtype_t dtype) {
-    const MlaDecodeShape s = mla_decode_shape(B, n, H, dc, dr, dtype);
-    return mla_meta_bytes(s.grid) + 2 * size_t(s.grid) * mla_slot_floats(s.row_tile, dc) * sizeof(float);
+    (void)B, (void)dr, (void)dtype;
+    const size_t x = scratch(simt_shape(n, H), dc), y = scratch(mla_decode_tc_shape(n, H), dc);
+    return x > y ? x : y;
 }
 
 cudaError_t launch_mla_decode(const MlaDecodeArgs &a, cudaStream_t st) {
-    const MlaDecodeShape s = mla_decode_shape(a.B, a.n, a.H, a.dc, a.dr, a.dtype);
-    cudaError_t e = a.dtype == KDA_DTYPE_F32 ? launch_simt<float>(a, s, st) : launch_simt<__nv_bfloat16>(a, s, st);
+    const bool tensor = mla_decode_tc_supported(a);
+    const MlaDecodeShape s = tensor ? mla_decode_tc_shape(a.n, a.H) : simt_shape(a.n, a.H);
+    const cudaError_t e = tensor ? launch_mla_decode_tc(a, s, st)
+                          : a.dtype == KDA_DTYPE_F32 ? launch_simt<float>(a, s, st)
+                                                     : launch_simt<__nv_bfloat16>(a, s, st);
     if (e != cudaSuccess) return e;
-    const dim3 grid(s.grid, s.row_tile < a.n * a.H ? s.row_tile : a.n * a.H);
+    const dim3 grid(s.grid(), s.row_tile < a.n * a.H ? s.row_tile : a.n * a.H);
     if (a.dtype == KDA_DTYPE_F32) join_kernel<float><<<grid, kJoinThreads, 0, st>>>(a, s);
     else join_kernel<__nv_bfloat16><<<grid, kJoinThreads, 0, st>>>(a, s);
     return cudaGetLastError();

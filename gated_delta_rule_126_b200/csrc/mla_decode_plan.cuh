@@ -1,23 +1,27 @@
-// How mla_decode cuts its work.  An item is (sequence b, tile of query rows); its keys are
-// cut into tiles.  The tiles of all items, in the order (b, row tile, key tile), are dealt
-// to the blocks in equal contiguous runs: block g of G takes tiles [g W / G, (g+1) W / G) of
-// W, so every block has the same work however uneven the sequences are.  A run covers whole
-// items except at its ends; a block writes the part of an item that it shares with other
-// blocks (at most two: its first and its last) to the workspace as (running maximum, sum,
-// unnormalised output), and a second kernel joins the parts.  Everything follows from
-// seq_lens on the device, by a fixed rule.
+// How mla_decode cuts its work.  Blocks come in groups of row_tiles: block x belongs to group
+// x / row_tiles and works on query rows of tile x % row_tiles.  The keys of every sequence
+// are cut into tiles; the tiles of all sequences, in order, are dealt to the groups in equal
+// contiguous runs: group g of G takes tiles [g W / G, (g+1) W / G) of W, so every block has the
+// same work however uneven the sequences are, and the blocks of a group, which run side by
+// side, read the same rows at the same time (from memory once, then from L2).  A run covers
+// whole sequences except at its ends; a block writes its part of a sequence that it shares with other groups (at
+// most two: its first and its last) to the workspace as (running maximum, sum, unnormalised
+// output), and a second kernel joins the parts.  Everything follows from seq_lens on the
+// device, by a fixed rule.
 #pragma once
+
+#include <cmath>
 
 #include "mla_internal.h"
 
 namespace kda {
 
-// What block g of the main kernel leaves for the join, at the front of the workspace.
+// What a block of the main kernel leaves for the join, at the front of the workspace.
 struct MlaJoin {
-    int32_t parts;  // blocks that share the item that begins inside block g's run and ends behind it; 0: none
+    int32_t parts;       // groups that share the sequence that begins inside this block's run and ends behind it; 0: none
     int32_t b;
-    int32_t row_tile;
-    int32_t first_slot;  // slot of block g's part; the following blocks' parts are in slot 2 (g + i)
+    int32_t first_slot;  // slot of this block's part; part i is in slot 2 (block + i row_tiles)
+    int32_t pad;
 };
 
 __host__ __device__ inline size_t mla_meta_bytes(int grid) { return (size_t(grid) * sizeof(MlaJoin) + 255) & ~size_t(255); }
@@ -25,8 +29,8 @@ __host__ __device__ inline size_t mla_meta_bytes(int grid) { return (size_t(grid
 __host__ __device__ inline size_t mla_slot_floats(int row_tile, int dc) { return size_t(row_tile) * (dc + 2); }
 
 struct MlaRun {
-    int64_t total, start, end;  // tiles of the whole call; this block's run
-    int grid;                   // blocks that have work: min(grid, total)
+    int64_t total, start, end;  // tiles of the whole call; this group's run
+    int groups;                 // groups that have work: min(groups, total)
     int b;                      // sequence of tile `start`
     int64_t before;             // tiles of the sequences before b
 };
@@ -39,12 +43,11 @@ __device__ __forceinline__ int mla_len(const MlaDecodeArgs &a, int b) {
 
 // Called by every thread of a block of NT threads; `buf` is shared scratch of NT / 32 + 4 int64.
 template <int NT>
-__device__ MlaRun mla_find_run(const MlaDecodeArgs &a, int row_tiles, int key_tile, int64_t *buf) {
+__device__ MlaRun mla_find_run(const MlaDecodeArgs &a, int group, int groups, int key_tile, int64_t *buf) {
     const int per = (a.B + NT - 1) / NT;
     const int b0 = threadIdx.x * per, b1 = min(a.B, b0 + per);
     int64_t own = 0;
     for (int b = b0; b < b1; ++b) own += (mla_len(a, b) + key_tile - 1) / key_tile;
-    own *= row_tiles;
     int64_t scan = own;  // inclusive over the warp, then over the block
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -60,18 +63,18 @@ __device__ MlaRun mla_find_run(const MlaDecodeArgs &a, int row_tiles, int key_ti
     }
     MlaRun r;
     r.total = total;
-    r.grid = int(total < gridDim.x ? total : gridDim.x);
+    r.groups = int(total < groups ? total : groups);
     r.start = r.end = 0;
     r.b = 0;
     r.before = 0;
-    if (int(blockIdx.x) < r.grid) {
-        r.start = int64_t(blockIdx.x) * total / r.grid;
-        r.end = (int64_t(blockIdx.x) + 1) * total / r.grid;
+    if (group < r.groups) {
+        r.start = int64_t(group) * total / r.groups;
+        r.end = (int64_t(group) + 1) * total / r.groups;
         if (own > 0 && scan - own <= r.start && r.start < scan) {  // tile `start` is in this thread's sequences
             int64_t at = scan - own;
             int b = b0;
             for (; b < b1; ++b) {
-                const int64_t nt = int64_t((mla_len(a, b) + key_tile - 1) / key_tile) * row_tiles;
+                const int64_t nt = (mla_len(a, b) + key_tile - 1) / key_tile;
                 if (r.start < at + nt) break;
                 at += nt;
             }
@@ -80,16 +83,59 @@ __device__ MlaRun mla_find_run(const MlaDecodeArgs &a, int row_tiles, int key_ti
         }
     }
     __syncthreads();
-    if (int(blockIdx.x) < r.grid) {
+    if (group < r.groups) {
         r.b = int(buf[NT / 32]);
         r.before = buf[NT / 32 + 1];
     }
     return r;
 }
 
-// The block whose run holds tile x.
-__device__ __forceinline__ int mla_block_of(int64_t x, int64_t total, int grid) {
-    return int(((x + 1) * grid - 1) / total);
+// The group whose run holds tile x.
+__device__ __forceinline__ int mla_group_of(int64_t x, int64_t total, int groups) {
+    return int(((x + 1) * groups - 1) / total);
+}
+
+// Walks a run sequence by sequence: b, its length, its tiles [t0, t1) of nt in the run.
+struct MlaWalk {
+    int64_t x, end, before;
+    int b, len, nt, t0, t1;
+    bool first;  // the run's first sequence
+    __device__ explicit MlaWalk(const MlaRun &r) : x(r.start), end(r.end), before(r.before), b(r.b - 1), len(0), nt(0), t0(0), t1(0), first(false) {}
+    // Moves to the next sequence with tiles in the run; false at its end.
+    __device__ bool next(const MlaDecodeArgs &a, int key_tile, const MlaRun &r) {
+        if (x >= end) return false;
+        do {
+            before += nt;
+            len = mla_len(a, ++b);
+            nt = (len + key_tile - 1) / key_tile;
+        } while (x >= before + nt);
+        first = x == r.start;
+        t0 = int(x - before);
+        t1 = int(nt < end - before ? nt : end - before);
+        x = before + t1;
+        return true;
+    }
+    __device__ bool whole() const { return t0 == 0 && t1 == nt; }
+};
+
+// The workspace slot of a block's part of the walk's sequence.
+__device__ __forceinline__ int mla_slot(const MlaWalk &w) { return 2 * int(blockIdx.x) + (w.first ? 0 : 1); }
+// The join's entry of a part that begins its sequence.
+__device__ __forceinline__ MlaJoin mla_join_entry(const MlaWalk &w, const MlaRun &r, int group) {
+    return MlaJoin{mla_group_of(w.before + w.nt - 1, r.total, r.groups) - group + 1, w.b, mla_slot(w), 0};
+}
+
+// Outputs of the sequences without a key, for this block's query rows; NT threads.
+template <typename T, int NT>
+__device__ __forceinline__ void mla_empty_sequences(const MlaDecodeArgs &a, int group, int groups, int r0, int rows) {
+    const int R = a.n * a.H;
+    for (int b = group; b < a.B; b += groups)
+        if (mla_len(a, b) == 0) {
+            const int64_t at = int64_t(b) * R + r0;
+            for (int i = threadIdx.x; i < rows * a.dc; i += NT) static_cast<T *>(a.o)[at * a.dc + i] = T(0.f);
+            if (a.lse)
+                for (int i = threadIdx.x; i < rows; i += NT) a.lse[at + i] = -INFINITY;
+        }
 }
 
 }  // namespace kda

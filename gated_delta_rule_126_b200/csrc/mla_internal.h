@@ -56,12 +56,19 @@ struct MlaArgs {  // mla_prefill and mla_backward
 
 // How mla_decode's work is cut (see mla_decode_plan.cuh).
 struct MlaDecodeShape {
+    bool tensor;    // tensor-core kernel
     int row_tile;   // query rows (token, head) a block works on
-    int key_tile;   // keys per tile
-    int grid;       // blocks
+    int row_tiles;  // blocks of a group
+    int groups;
+    int grid() const { return groups * row_tiles; }
 };
-MlaDecodeShape mla_decode_shape(int B, int n, int H, int dc, int dr, kda_dtype_t dtype);
+// Workspace of the larger of the two kernels' needs (the page size, which helps to choose, is not known here).
 size_t mla_decode_scratch(int B, int n, int H, int dc, int dr, kda_dtype_t dtype);
+bool mla_decode_tc_supported(const MlaDecodeArgs &a);
+MlaDecodeShape mla_decode_tc_shape(int n, int H);
+cudaError_t launch_mla_decode_tc(const MlaDecodeArgs &a, const MlaDecodeShape &s, cudaStream_t st);
+cudaError_t mla_decode_fault(cudaStream_t st, unsigned int *out);  // waits, reads and clears the error flag
+int device_sm_count();
 
 // Tiles of `tile` rows over the sequences of a host offset array.
 inline int64_t count_tiles(const int32_t *cu, int n, int tile) {

@@ -1,0 +1,79 @@
+// What the tensor-core kernels of the latent-attention operators share: instruction
+// descriptors, tensor maps, bounded waits and their error flag.
+#pragma once
+
+#include <cuda.h>
+
+#include "mla_internal.h"
+#include "sm100_ptx.cuh"
+
+namespace kda {
+
+// Set by a kernel of this translation unit when one of its bounded waits ran out.
+static __device__ unsigned int mla_fault;
+
+// Waits for `st`, then reads and clears this translation unit's flag.
+static inline cudaError_t mla_fault_read(cudaStream_t st, unsigned int *out) {
+    cudaError_t e = cudaStreamSynchronize(st);
+    if (e == cudaSuccess) e = cudaMemcpyFromSymbol(out, mla_fault, sizeof(*out));
+    const unsigned int zero = 0;
+    if (e == cudaSuccess && *out) e = cudaMemcpyToSymbol(mla_fault, &zero, sizeof(zero));
+    return e;
+}
+
+namespace tc {
+
+constexpr long long kWaitCycles = 4000000000ll;  // about two seconds
+
+// Instruction descriptor of kind::f16 with bf16 operands and float32 sums.
+__host__ __device__ constexpr uint32_t idesc(int M, int N, bool a_mn, bool b_mn) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | (uint32_t(a_mn) << 15) | (uint32_t(b_mn) << 16) |
+           (uint32_t(N >> 3) << 17) | (uint32_t(M >> 4) << 24);
+}
+
+// Waits for the phase of the given parity; gives up (and makes every other wait of the
+// block give up) after kWaitCycles.
+__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, volatile uint32_t *dead) {
+    if (ptx::mbar_try_wait(bar, parity)) return true;
+    const long long t0 = clock64();
+    while (!ptx::mbar_try_wait(bar, parity)) {
+        if (*dead) return false;
+        if (clock64() - t0 > kWaitCycles) {
+            *dead = 1;
+            atomicExch(&mla_fault, 1u);
+            return false;
+        }
+    }
+    return true;
+}
+
+__device__ __forceinline__ void tma_load_2d(uint32_t smem_dst, const void *tmap, uint64_t *bar, int c0, int c1) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(ptx::smem_u32(bar))
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_3d(uint32_t smem_dst, const void *tmap, uint64_t *bar, int c0, int c1, int c2) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(c2), "r"(ptx::smem_u32(bar))
+        : "memory");
+}
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+// Two floats as bf16, rounded to nearest even: `lo` in the low half.
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// Tensor map of a bf16 tensor with 128-byte-swizzled boxes; false when it cannot be described.
+// dims and box: `rank` numbers, innermost first; strides: rank - 1 numbers, in elements.
+bool make_map(CUtensorMap *m, const void *base, int rank, const int64_t *dims, const int64_t *strides, const int *box);
+
+}  // namespace tc
+}  // namespace kda

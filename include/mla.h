@@ -100,8 +100,9 @@ KDA_API size_t mla_decode_workspace_size(int B, int n, int H, int d_latent, int 
  * hold anything, NaN included.  Work is split over the keys by a fixed rule, so repeated
  * calls give identical results.
  * Supported: 1 <= d_latent <= 512, 0 <= d_rope <= 64, n * H <= 65536, B <= 65536;
- * q, cache and o 16-byte aligned.  bf16 with d_latent a multiple of 128 and d_rope 0 or
- * 64 runs on the tensor cores, everything else on the CUDA cores in float32.
+ * q, cache and o 16-byte aligned.  bf16 with d_latent a multiple of 128, d_rope 0 or 64,
+ * pages of a multiple of 8 rows and scale > 0 runs on the tensor cores (probabilities
+ * rounded to bf16, sums in float32), everything else on the CUDA cores in float32.
  */
 KDA_API kda_status_t mla_decode(const void *q, kda_dtype_t dtype, const void *cache, int num_pages, int page_size,
                         const int32_t *page_table, int max_pages, const int32_t *seq_lens, int B, int n, int H,
@@ -162,6 +163,14 @@ KDA_API kda_status_t mla_backward(const void *q, int64_t q_stride_t, int64_t q_s
                           float scale, int causal, const void *o, const float *lse, const void *dO, void *dq,
                           void *dk, void *dk_rope, void *dv, void *workspace, size_t workspace_bytes,
                           kda_stream_t stream);
+
+/*
+ * mla_status -- waits for `stream`, then reports whether a tensor-core kernel of an
+ * earlier mla_* call on the current device flagged an internal error (a bounded wait that
+ * ran out: KDA_ERR_DEVICE_FAULT, that call's outputs are not to be used) and clears the
+ * flag.  KDA_ERR_CUDA when the wait itself failed.  Not for use during a stream capture.
+ */
+KDA_API kda_status_t mla_status(kda_stream_t stream);
 
 #ifdef __cplusplus
 }

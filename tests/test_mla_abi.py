@@ -27,7 +27,7 @@ def test_exports(lib):
     text = open(os.path.join(ROOT, "include", "mla.h")).read()
     declared = set(re.findall(r"KDA_API\s+[\w\s\*]+?\b(mla_\w+)\s*\(", text))
     assert declared == {"mla_append", "mla_decode", "mla_decode_workspace_size", "mla_prefill", "mla_backward",
-                        "mla_backward_workspace_size"}
+                        "mla_backward_workspace_size", "mla_status"}
     out = os.popen(f"nm -D --defined-only {_binding.LIB_PATH}").read()
     assert {ln.split()[-1] for ln in out.splitlines() if " T " in ln and "mla" in ln} == declared
 
