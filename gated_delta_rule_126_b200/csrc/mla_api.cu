@@ -149,7 +149,8 @@ kda_status_t mla_prefill(const void *q, int64_t q_stride_t, int64_t q_stride_h, 
     if (!o || !aligned(o, elem(dtype))) return KDA_ERR_INVALID_ARG;
     a.o = o;
     a.lse = lse;
-    return from_cuda(kda::launch_mla_prefill_simt(a, reinterpret_cast<cudaStream_t>(stream)));
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    return from_cuda(kda::mla_tc_supported(a) ? kda::launch_mla_prefill_tc(a, st) : kda::launch_mla_prefill_simt(a, st));
 }
 
 size_t mla_backward_workspace_size(int64_t total_q, int64_t total_k, int H, int d_nope, int d_rope, int d_v,
@@ -195,9 +196,10 @@ kda_status_t mla_backward(const void *q, int64_t q_stride_t, int64_t q_stride_h,
 }
 
 kda_status_t mla_status(kda_stream_t stream) {
-    unsigned int f = 0;
-    if (kda::mla_decode_fault(reinterpret_cast<cudaStream_t>(stream), &f) != cudaSuccess) return KDA_ERR_CUDA;
-    return f ? KDA_ERR_DEVICE_FAULT : KDA_OK;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    unsigned int f = 0, g = 0;
+    if (kda::mla_decode_fault(st, &f) != cudaSuccess || kda::mla_prefill_fault(st, &g) != cudaSuccess) return KDA_ERR_CUDA;
+    return f || g ? KDA_ERR_DEVICE_FAULT : KDA_OK;
 }
 
 }  // extern "C"

@@ -79,6 +79,9 @@ inline int64_t count_tiles(const int32_t *cu, int n, int tile) {
 
 cudaError_t launch_mla_append(const MlaAppendArgs &a, cudaStream_t st);
 cudaError_t launch_mla_decode(const MlaDecodeArgs &a, cudaStream_t st);
+bool mla_tc_supported(const MlaArgs &a);
+cudaError_t launch_mla_prefill_tc(const MlaArgs &a, cudaStream_t st);
+cudaError_t mla_prefill_fault(cudaStream_t st, unsigned int *out);
 cudaError_t launch_mla_prefill_simt(const MlaArgs &a, cudaStream_t st);
 cudaError_t launch_mla_backward_simt(const MlaArgs &a, cudaStream_t st);
 cudaError_t launch_mla_delta(const MlaArgs &a, cudaStream_t st);

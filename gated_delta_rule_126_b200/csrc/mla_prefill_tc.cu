@@ -1,0 +1,360 @@
+// mla_prefill on the tensor cores (bf16, d_nope = d_v = 128, d_rope 0 or 64).
+//
+// A block holds 256 queries of one head as two tiles of 128 and streams the keys in blocks of
+// 128:  S_t = Q_t [K | Kr]^T,  P_t = exp(S_t - max),  O_t += P_t V.  S (float32), P (bf16, over S) and
+// O of both tiles fill TMEM's 512 columns; a row is a TMEM lane and a thread, so the softmax
+// needs no exchange between threads.  While one tile's softmax runs, the tensor cores work on
+// the other tile.  Bound by the tensor cores: (192 + 128) 128 128 products a tile and key block
+// take 1,280 cycles, its 16,384 exponentials 1,024 on the special-function units.
+//
+// Warps 0-3 and 4-7: softmax, rescaling and output of tiles 0 and 1; warp 8: matrix instructions; warp 9:
+// TMA loads (10 and 11 only give their registers to the softmax).  Keys and values pass through a ring of eight 16 KB slots (a 64-channel chunk of 128 keys,
+// or 64 keys of values), so the shared key part is loaded once a block and head sizes of 128 and
+// 192 use the same ring.
+#include <cmath>
+
+#include "mla_simt.cuh"
+#include "mla_tc.cuh"
+
+namespace kda {
+namespace {
+
+constexpr int kThreads = 384;
+// Registers a thread: launched with 168 x 384; the softmax warps take what the other four give back.
+constexpr int kRegsSoftmax = 208, kRegsOther = 88;
+static_assert(2 * kRegsSoftmax + kRegsOther <= 3 * 168, "register split");
+constexpr int kRows = 128;
+constexpr int kSlots = 8;
+constexpr uint32_t kSlotBytes = 16384;
+constexpr uint32_t kOffRing = 2 * 3 * kSlotBytes, kOffMisc = kOffRing + kSlots * kSlotBytes;
+constexpr uint32_t kSmem = kOffMisc + 1024 + 1024;  // misc, alignment
+constexpr uint32_t kTmemColumns = 512, kTmO = 256;
+constexpr float kLog2e = 1.4426950408889634f;
+// The maximum that scales P and O is raised only when the true one has outgrown it by 2^8:
+// sums stay exact enough in float32 (P <= 256), and rescaling O becomes rare.
+constexpr float kLazy = 8.f;
+
+struct Misc {
+    uint64_t full[kSlots], empty[kSlots], q_full[2], s_full[2], p_full[2], pv_done[2], drain;
+    int64_t find[kThreads / 32 + 2];
+    uint32_t tmem, dead;
+};
+static_assert(sizeof(Misc) <= 1024, "misc");
+
+struct Maps {
+    CUtensorMap q, k, kr, v;
+};
+
+__global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_constant__ Maps maps, const MlaArgs a) {
+    extern __shared__ uint8_t raw[];
+    const uint32_t base = (ptx::smem_u32(raw) + 1023u) & ~1023u;
+    Misc &mi = *reinterpret_cast<Misc *>(raw + (base - ptx::smem_u32(raw)) + kOffMisc);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int h = blockIdx.x % a.H, kc = a.dr ? 3 : 2;  // chunks of a key
+
+    if (tid == 0) {
+        for (int i = 0; i < kSlots; ++i) ptx::mbar_init(&mi.full[i], 1), ptx::mbar_init(&mi.empty[i], 1);
+        for (int t = 0; t < 2; ++t) {
+            ptx::mbar_init(&mi.q_full[t], 1);
+            ptx::mbar_init(&mi.s_full[t], 1);
+            ptx::mbar_init(&mi.p_full[t], 128);
+            ptx::mbar_init(&mi.pv_done[t], 1);
+        }
+        ptx::mbar_init(&mi.drain, 1);
+        mi.dead = 0;
+        ptx::fence_mbar_init();
+    }
+    if (warp == 9 && lane == 0) {
+        ptx::prefetch_tmap(&maps.q);
+        ptx::prefetch_tmap(&maps.k);
+        ptx::prefetch_tmap(&maps.v);
+        if (a.dr) ptx::prefetch_tmap(&maps.kr);
+    }
+    int seq = 0, tile = 0;  // long tiles (the last queries) first
+    if (!find_tile<kThreads>(a.cu_q, a.num_seqs, 2 * kRows, gridDim.x / a.H - 1 - blockIdx.x / a.H, mi.find, &seq, &tile)) return;
+    if (warp == 8) {
+        ptx::tmem_alloc(&mi.tmem, kTmemColumns);
+        ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = mi.tmem;
+    volatile uint32_t *dead = &mi.dead;
+
+    const int q0 = a.cu_q[seq], lq = a.cu_q[seq + 1] - q0, k0 = a.cu_k[seq], lk = a.cu_k[seq + 1] - k0, i0 = tile * 2 * kRows;
+    auto key_end = [&](int i) { return a.causal ? max(0, min(lk, i + 1 + lk - lq)) : lk; };  // keys that query i sees
+    // key blocks of each tile
+    int n[2];
+    for (int t = 0; t < 2; ++t) n[t] = i0 + t * kRows < lq ? (key_end(min(i0 + (t + 1) * kRows, lq) - 1) + 127) / 128 : 0;
+    const int blocks = max(n[0], n[1]);
+    const int per = kc + 2;  // slots of a key block: its chunks, then two halves of its values
+
+    if (warp >= 8) ptx::regs_dec<kRegsOther>();
+    else ptx::regs_inc<kRegsSoftmax>();
+    if (warp == 9) {
+        // -------------------------------------------------------------------- loads
+        if (lane == 0 && blocks > 0) {
+            auto load_q = [&](int t) {
+                if (n[t] == 0) return;
+                ptx::mbar_arrive_expect_tx(&mi.q_full[t], kc * kSlotBytes);
+                for (int c = 0; c < kc; ++c)
+                    tc::tma_load_3d(base + (3 * t + c) * kSlotBytes, &maps.q, &mi.q_full[t], 64 * c, h, q0 + i0 + t * kRows);
+            };
+            bool ok = true;
+            int idx = 0;
+            load_q(0);
+            for (int j = 0; ok && j < blocks; ++j)
+                for (int c = 0; c < per; ++c, ++idx) {
+                    const int slot = idx % kSlots;
+                    if (idx >= kSlots && !(ok = tc::wait(&mi.empty[slot], (idx / kSlots - 1) & 1, dead))) break;
+                    const uint32_t dst = base + kOffRing + slot * kSlotBytes;
+                    ptx::mbar_arrive_expect_tx(&mi.full[slot], kSlotBytes);
+                    if (c < 2) {
+                        tc::tma_load_3d(dst, &maps.k, &mi.full[slot], 64 * c, h, k0 + j * 128);
+                    } else if (c < kc) {
+                        tc::tma_load_2d(dst, &maps.kr, &mi.full[slot], 0, k0 + j * 128);
+                    } else {
+                        const int key = k0 + j * 128 + (c - kc) * 64;
+                        tc::tma_load_3d(dst, &maps.v, &mi.full[slot], 0, h, key);
+                        tc::tma_load_3d(dst + 8192, &maps.v, &mi.full[slot], 64, h, key);
+                    }
+                    if (idx == kc - 1) load_q(1);
+                }
+            if (!ok) {  // an error: the copies in flight land before the block ends
+                for (int i = max(0, idx - kSlots); i < idx; ++i)
+                    ptx::mbar_wait_bounded(&mi.full[i % kSlots], (i / kSlots) & 1, tc::kWaitCycles);
+                for (int t = 0; t < 2; ++t)
+                    if (n[t]) ptx::mbar_wait_bounded(&mi.q_full[t], 0, tc::kWaitCycles);
+            }
+        }
+    } else if (warp == 8) {
+        // -------------------------------------------------------------------- products
+        if (lane == 0 && blocks > 0) {
+            constexpr uint32_t kIdS = tc::idesc(128, 128, false, false), kIdO = tc::idesc(128, 128, false, true);
+            auto qk = [&](int t, int j) {
+                const uint32_t qa = base + 3 * t * kSlotBytes;
+                for (int c = 0; c < kc; ++c) {
+                    const int idx = j * per + c, slot = idx % kSlots;
+                    if (!tc::wait(&mi.full[slot], (idx / kSlots) & 1, dead)) return false;
+                    ptx::tc_fence_after();
+                    const uint32_t ka = base + kOffRing + slot * kSlotBytes;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        ptx::mma_ss(tmem + t * 128, ptx::sdesc_sw128(qa + c * kSlotBytes + 32 * k),
+                                    ptx::sdesc_sw128(ka + 32 * k), kIdS, c + k > 0);
+                }
+                ptx::mma_commit(&mi.s_full[t]);
+                return true;
+            };
+            auto pv = [&](int t, int j) {
+                if (!tc::wait(&mi.p_full[t], j & 1, dead)) return false;
+                for (int c = 0; c < 2; ++c) {
+                    const int idx = j * per + kc + c, slot = idx % kSlots;
+                    if (!tc::wait(&mi.full[slot], (idx / kSlots) & 1, dead)) return false;
+                    ptx::tc_fence_after();
+                    const uint32_t va = base + kOffRing + slot * kSlotBytes;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        ptx::mma_ts(tmem + kTmO + t * 128, tmem + t * 128 + (4 * c + k) * 8,
+                                    ptx::sdesc_sw128_mn(va + 2048 * k, 8192, 1024), kIdO, j > 0 || c + k > 0);
+                }
+                ptx::mma_commit(&mi.pv_done[t]);
+                return true;
+            };
+            auto release = [&](int first, int count) {
+                for (int i = first; i < first + count; ++i) ptx::mma_commit(&mi.empty[i % kSlots]);
+            };
+            bool ok = true;
+            for (int t = 0; ok && t < 2; ++t)
+                if (n[t]) ok = tc::wait(&mi.q_full[t], 0, dead) && qk(t, 0);
+            if (ok) release(0, kc);
+            for (int j = 0; ok && j < blocks; ++j) {
+                if (j < n[0]) ok = pv(0, j);
+                if (ok && j + 1 < n[0]) ok = qk(0, j + 1);
+                if (ok && j < n[1]) ok = pv(1, j);
+                if (!ok) break;
+                release(j * per + kc, 2);
+                if (j + 1 < n[1]) ok = qk(1, j + 1);
+                if (ok && j + 1 < blocks) release((j + 1) * per, kc);
+            }
+            if (!ok) {  // an error: the products in flight end before TMEM goes away
+                ptx::mma_commit(&mi.drain);
+                ptx::mbar_wait_bounded(&mi.drain, 0, tc::kWaitCycles);
+            }
+        }
+        __syncwarp();
+    } else if (warp < 8) {
+        // -------------------------------------------------------------------- softmax and output
+        const int t = warp >> 2, w = warp & 3, row = w * 32 + lane, r = i0 + t * kRows + row;
+        const uint32_t lanes = uint32_t(w) << 21, sa = tmem + lanes + t * 128, oa = tmem + lanes + kTmO + t * 128;
+        const float sl2 = a.scale * kLog2e;
+        const int end = r < lq ? key_end(r) : 0;
+        float top = -INFINITY, sum = 0.f;
+        bool ok = true;
+        for (int j = 0; j < n[t]; ++j) {
+            if (!(ok = tc::wait(&mi.s_full[t], j & 1, dead))) break;
+            ptx::tc_fence_after();
+            uint32_t s[4][32];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) ptx::tmem_ld32(sa + 32 * c, s[c]);
+            ptx::tmem_wait_ld();
+            const int seen = end - j * 128;
+            if (__any_sync(0xffffffffu, seen < 128)) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (32 * c + e >= seen) s[c][e] = 0xff800000u;
+                const int left = lk - j * 128;
+                if (left < 128) {
+                    // value rows behind the sequence may hold anything: they have to be zero
+                    for (int c = 0; ok && c < 2; ++c) {
+                        const int idx = j * per + kc + c, slot = idx % kSlots, rows0 = min(64, max(0, left - 64 * c));
+                        if (rows0 == 64) continue;
+                        if (!(ok = tc::wait(&mi.full[slot], (idx / kSlots) & 1, dead))) break;
+                        const uint32_t va = base + kOffRing + slot * kSlotBytes;
+                        for (int i = rows0 * 8 + row; i < 512; i += 128) {
+                            tc::st_shared_v4(va + 16 * i, 0, 0, 0, 0);
+                            tc::st_shared_v4(va + 8192 + 16 * i, 0, 0, 0, 0);
+                        }
+                    }
+                    if (!ok) break;
+                    ptx::fence_proxy_async_smem();
+                }
+            }
+            float m0 = top, m1 = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+                for (int e = 0; e < 32; e += 4) {
+                    m0 = fmaxf(m0, fmaxf(__uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1])));
+                    m1 = fmaxf(m1, fmaxf(__uint_as_float(s[c][e + 2]), __uint_as_float(s[c][e + 3])));
+                }
+            const float m = fmaxf(m0, m1);
+            bool raise = false;
+            float keep = 1.f;
+            if (top == -INFINITY) {
+                top = m;  // nothing summed yet
+            } else if ((m - top) * sl2 > kLazy) {
+                keep = ptx::ex2_approx((top - m) * sl2);
+                sum *= keep;
+                top = m;
+                raise = true;
+            }
+            if (__any_sync(0xffffffffu, raise)) {  // the last product has added to O
+                if (!(ok = tc::wait(&mi.pv_done[t], (j - 1) & 1, dead))) break;
+                ptx::tc_fence_after();
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t v[32];
+                    ptx::tmem_ld32(oa + 32 * c, v);
+                    ptx::tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * keep);
+                    ptx::tmem_st32(oa + 32 * c, v);
+                }
+            }
+            const float off = top == -INFINITY ? 0.f : top * sl2;
+            float add[4] = {};
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                uint32_t p[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const float x = ptx::ex2_approx(fmaf(__uint_as_float(s[c][2 * e]), sl2, -off));
+                    const float y = ptx::ex2_approx(fmaf(__uint_as_float(s[c][2 * e + 1]), sl2, -off));
+                    add[e & 3] += x + y;
+                    p[e] = tc::pack_bf16(x, y);
+                }
+                ptx::tmem_st16(sa + 16 * c, p);
+            }
+            sum += (add[0] + add[1]) + (add[2] + add[3]);
+            ptx::tmem_wait_st();
+            ptx::tc_fence_before();
+            ptx::mbar_arrive(&mi.p_full[t]);
+        }
+        if (ok && n[t]) ok = tc::wait(&mi.pv_done[t], (n[t] - 1) & 1, dead);
+        ptx::tc_fence_after();
+        if (ok) {
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            const int64_t at = int64_t(q0 + r) * a.H + h;
+            uint4 *out = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.o) + at * 128);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                uint32_t v[32];
+                if (n[t]) {
+                    ptx::tmem_ld32(oa + 32 * c, v);
+                    ptx::tmem_wait_ld();
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) v[e] = 0;
+                }
+                if (r < lq) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8) {
+                        uint4 x;
+                        x.x = tc::pack_bf16(__uint_as_float(v[e]) * inv, __uint_as_float(v[e + 1]) * inv);
+                        x.y = tc::pack_bf16(__uint_as_float(v[e + 2]) * inv, __uint_as_float(v[e + 3]) * inv);
+                        x.z = tc::pack_bf16(__uint_as_float(v[e + 4]) * inv, __uint_as_float(v[e + 5]) * inv);
+                        x.w = tc::pack_bf16(__uint_as_float(v[e + 6]) * inv, __uint_as_float(v[e + 7]) * inv);
+                        out[4 * c + e / 8] = x;
+                    }
+                }
+            }
+            if (a.lse && r < lq) a.lse[at] = sum == 0.f ? -INFINITY : top * a.scale + logf(sum);
+        }
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == 8) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, kTmemColumns);
+    }
+}
+
+}  // namespace
+
+namespace tc {
+
+bool rows_map(CUtensorMap *m, const void *p, int d, int H, int64_t T, int64_t st, int64_t sh, int rows) {
+    const int64_t dims[3] = {d, H, T}, strides[2] = {sh, st};
+    const int box[3] = {64, 1, rows};
+    return make_map(m, p, 3, dims, strides, box);
+}
+bool rope_map(CUtensorMap *m, const void *p, int64_t T, int64_t st, int rows) {
+    const int64_t dims[2] = {64, T};
+    const int box[2] = {64, rows};
+    return make_map(m, p, 2, dims, &st, box);
+}
+
+}  // namespace tc
+
+// Whole 64-channel chunks, TMA's alignment (bases 16 bytes, strides multiples of 8 elements
+// below 2^39) and a positive scale, since the maximum is taken before scaling.
+bool mla_tc_supported(const MlaArgs &a) {
+    auto p16 = [](const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; };
+    auto st = [](int64_t s) { return s > 0 && s % 8 == 0 && s < (int64_t(1) << 39); };
+    return a.dtype == KDA_DTYPE_BF16 && a.dn == 128 && a.dv == 128 && (a.dr == 0 || a.dr == 64) && a.scale > 0.f &&
+           a.Tq > 0 && a.Tk > 0 && p16(a.q) && p16(a.k) && p16(a.v) && p16(a.o) && st(a.q_st) && st(a.q_sh) &&
+           st(a.k_st) && st(a.k_sh) && st(a.v_st) && st(a.v_sh) && (a.dr == 0 || (p16(a.k_rope) && st(a.kr_st)));
+}
+
+cudaError_t launch_mla_prefill_tc(const MlaArgs &a, cudaStream_t st) {
+    const int64_t grid = count_tiles(a.cu_q_host, a.num_seqs, 2 * kRows) * a.H;
+    if (grid > INT32_MAX) return cudaErrorInvalidValue;
+    Maps maps{};
+    if (!tc::rows_map(&maps.q, a.q, 128 + a.dr, a.H, a.Tq, a.q_st, a.q_sh, kRows) ||
+        !tc::rows_map(&maps.k, a.k, 128, a.H, a.Tk, a.k_st, a.k_sh, 128) ||
+        !tc::rows_map(&maps.v, a.v, 128, a.H, a.Tk, a.v_st, a.v_sh, 64) ||
+        (a.dr && !tc::rope_map(&maps.kr, a.k_rope, a.Tk, a.kr_st, 128)))
+        return cudaErrorInvalidValue;
+    const cudaError_t e = cudaFuncSetAttribute(prefill_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmem));
+    if (e != cudaSuccess) return e;
+    prefill_tc_kernel<<<unsigned(grid), kThreads, kSmem, st>>>(maps, a);
+    return cudaGetLastError();
+}
+
+cudaError_t mla_prefill_fault(cudaStream_t st, unsigned int *out) { return mla_fault_read(st, out); }
+
+}  // namespace kda

@@ -74,6 +74,9 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 // Tensor map of a bf16 tensor with 128-byte-swizzled boxes; false when it cannot be described.
 // dims and box: `rank` numbers, innermost first; strides: rank - 1 numbers, in elements.
 bool make_map(CUtensorMap *m, const void *base, int rank, const int64_t *dims, const int64_t *strides, const int *box);
+// [T, H, d] rows with strides (st, sh), boxes of 64 channels of one head x `rows` tokens; and [T, 64].
+bool rows_map(CUtensorMap *m, const void *p, int d, int H, int64_t T, int64_t st, int64_t sh, int rows);
+bool rope_map(CUtensorMap *m, const void *p, int64_t T, int64_t st, int rows);
 
 }  // namespace tc
 }  // namespace kda
