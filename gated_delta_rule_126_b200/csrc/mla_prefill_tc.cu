@@ -90,9 +90,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
     const int blocks = max(n[0], n[1]);
     const int per = kc + 2;  // slots of a key block: its chunks, then two halves of its values
 
-    if (warp >= 8) ptx::regs_dec<kRegsOther>();
-    else ptx::regs_inc<kRegsSoftmax>();
-    if (warp == 9) {
+    if (warp >= 8) {
+        ptx::regs_dec<kRegsOther>();
+      if (warp == 9) {
         // -------------------------------------------------------------------- loads
         if (lane == 0 && blocks > 0) {
             auto load_q = [&](int t) {
@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
                     if (n[t]) ptx::mbar_wait_bounded(&mi.q_full[t], 0, tc::kWaitCycles);
             }
         }
-    } else if (warp == 8) {
+      } else if (warp == 8) {
         // -------------------------------------------------------------------- products
         if (lane == 0 && blocks > 0) {
             constexpr uint32_t kIdS = tc::idesc(128, 128, false, false), kIdO = tc::idesc(128, 128, false, true);
@@ -184,8 +184,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
             }
         }
         __syncwarp();
-    } else if (warp < 8) {
+      }
+    } else {
         // -------------------------------------------------------------------- softmax and output
+        ptx::regs_inc<kRegsSoftmax>();
         const int t = warp >> 2, w = warp & 3, row = w * 32 + lane, r = i0 + t * kRows + row;
         const uint32_t lanes = uint32_t(w) << 21, sa = tmem + lanes + t * 128, oa = tmem + lanes + kTmO + t * 128;
         const float sl2 = a.scale * kLog2e;
