@@ -20,7 +20,8 @@ LIB_PATH = os.path.join(LIB_DIR, "libkda_b200.so")
 SOURCES = ["kda_api.cu", "kda_decode.cu", "kda_prefill_simt.cu", "kda_prefill_tc.cu", "kda_noalloc.cu",
            "kda_epilogue.cu", "kda_prologue.cu", "kda_split.cu", "kda_selftest.cu",
            "kda_backward.cu", "mla_api.cu", "mla_append.cu", "mla_decode.cu", "mla_prefill_simt.cu",
-           "mla_tc.cu", "mla_decode_tc.cu", "mla_prefill_tc.cu"]
+           "mla_tc.cu", "mla_decode_tc.cu", "mla_prefill_tc.cu",
+           "mla_backward_tc.cu"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-fvisibility=hidden",

@@ -157,7 +157,7 @@ size_t mla_backward_workspace_size(int64_t total_q, int64_t total_k, int H, int 
                                    kda_dtype_t dtype) {
     if (check_head_sizes(H, d_nope, d_rope, d_v, dtype) != KDA_OK) return 0;
     if (total_q < 0 || total_k < 0 || total_q > INT32_MAX || total_k > INT32_MAX) return 0;
-    return 256 + align256(size_t(total_q) * H * sizeof(float)) + align256(size_t(total_k) * H * d_rope * sizeof(float));
+    return 256 + 2 * align256(size_t(total_q) * H * sizeof(float)) + align256(size_t(total_k) * H * d_rope * sizeof(float));
 }
 
 kda_status_t mla_backward(const void *q, int64_t q_stride_t, int64_t q_stride_h, const void *k, int64_t k_stride_t,
@@ -185,21 +185,28 @@ kda_status_t mla_backward(const void *q, int64_t q_stride_t, int64_t q_stride_h,
     a.o = const_cast<void *>(o);
     a.lse = const_cast<float *>(lse);
     a.dO = dO; a.dq = dq; a.dk = dk; a.dk_rope = d_rope ? dk_rope : nullptr; a.dv_out = dv;
-    a.delta = reinterpret_cast<float *>(static_cast<char *>(workspace) + 256);
-    a.dkr_partial = reinterpret_cast<float *>(static_cast<char *>(workspace) + 256 +
-                                              align256(size_t(a.Tq) * H * sizeof(float)));
+    char *ws = static_cast<char *>(workspace) + 256;
+    const size_t stats = align256(size_t(a.Tq) * H * sizeof(float));
+    a.delta = reinterpret_cast<float *>(ws);
+    a.lse2 = reinterpret_cast<float *>(ws + stats);
+    a.dkr_partial = reinterpret_cast<float *>(ws + 2 * stats);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e = kda::launch_mla_delta(a, st);
-    if (e == cudaSuccess) e = kda::launch_mla_backward_simt(a, st);
+    bool tensor = kda::mla_tc_supported(a);
+    for (const void *p : {dO, static_cast<const void *>(dq), static_cast<const void *>(dk), static_cast<const void *>(dv)})
+        tensor = tensor && aligned(p, 16);
+    if (e == cudaSuccess) e = tensor ? kda::launch_mla_backward_tc(a, st) : kda::launch_mla_backward_simt(a, st);
     if (e == cudaSuccess && d_rope > 0) e = kda::launch_mla_dkr_reduce(a, st);
     return from_cuda(e);
 }
 
 kda_status_t mla_status(kda_stream_t stream) {
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    unsigned int f = 0, g = 0;
-    if (kda::mla_decode_fault(st, &f) != cudaSuccess || kda::mla_prefill_fault(st, &g) != cudaSuccess) return KDA_ERR_CUDA;
-    return f || g ? KDA_ERR_DEVICE_FAULT : KDA_OK;
+    unsigned int f = 0, g = 0, h = 0;
+    if (kda::mla_decode_fault(st, &f) != cudaSuccess || kda::mla_prefill_fault(st, &g) != cudaSuccess ||
+        kda::mla_backward_fault(st, &h) != cudaSuccess)
+        return KDA_ERR_CUDA;
+    return f || g || h ? KDA_ERR_DEVICE_FAULT : KDA_OK;
 }
 
 }  // extern "C"

@@ -1,0 +1,558 @@
+// mla_backward on the tensor cores (bf16, d_nope = d_v = 128, d_rope 0 or 64): two kernels, so that
+// every gradient has one owner and no sum is made with atomics (a kernel with one pass over the scores
+// would add 128 x 192 float32 values of dq per tile pair through L2, about 30 bytes a cycle and
+// SM, more than L2 takes; the second pass costs 2 of 7 products instead).
+//
+// dkv_tc_kernel: a block owns 128 keys of one head and streams the queries in tiles of 64.
+//   S^T = K Q^T, dP^T = V dO^T  [128 x 64];  dV += P^T dO, dK += dS^T Q, with P^T and dS^T in TMEM
+//   as the left operands; Q and dO tiles serve as [q x d] K-major and as MN-major operand alike.
+//   TMEM: S^T twice 64 columns, dP^T 64, dV 128, dK 192: all 512.
+// dq_tc_kernel: a block owns 128 queries of one head and streams the keys in blocks of 128.
+//   S = Q K^T, dP = dO V^T  [128 x 128];  dQ += dS K, dS in TMEM.  TMEM: S 128, dP 128, dQ 192, dS 64.
+// P = exp2(scale log2(e) S - lse2) and dS = P (dP - delta) are rounded to bf16 for their products; the
+// factor `scale` of dq and dk is applied to the float32 sums at the end.
+// Bound by the tensor cores.  Warps 0-7: elementwise work and output, two warpgroups with half of the columns each;
+// warp 8: matrix instructions; warp 9: loads.
+#include <cmath>
+
+#include "mla_simt.cuh"
+#include "mla_tc.cuh"
+
+namespace kda {
+namespace {
+
+constexpr int kThreads = 320;
+constexpr uint32_t kTmemColumns = 512;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr uint32_t kChunk = 16384;  // 128 rows x 64 channels
+
+struct Place {  // one sequence's rows
+    int q0, lq, k0, lk, off;  // query i sees key j when j <= i + off (causal)
+};
+__device__ __forceinline__ Place place_of(const MlaArgs &a, int s) {
+    Place p;
+    p.q0 = a.cu_q[s];
+    p.lq = a.cu_q[s + 1] - p.q0;
+    p.k0 = a.cu_k[s];
+    p.lk = a.cu_k[s + 1] - p.k0;
+    p.off = a.causal ? p.lk - p.lq : INT32_MAX / 2;
+    return p;
+}
+
+// ------------------------------------------------------------------------------ dk, dv
+constexpr int kQt = 64;  // queries of a tile
+constexpr int kStages = 3;
+constexpr uint32_t kQChunk = kQt * 128;  // 64 rows x 64 channels
+constexpr uint32_t kStage = 5 * kQChunk;  // q (three chunks), dO (two)
+constexpr uint32_t kOffV = 3 * kChunk, kOffStages = 5 * kChunk, kOffMisc = kOffStages + kStages * kStage;
+constexpr uint32_t kDkvSmem = kOffMisc + 4096 + 1024;
+constexpr uint32_t kTmDp = 128, kTmDv = 192, kTmDk = 320;
+
+struct DkvMisc {
+    uint64_t full[kStages], empty[kStages], k_full, v_full, s_full[2], dp_full, p_full, ds_full, done;
+    int64_t find[kThreads / 32 + 2];
+    uint32_t tmem, dead;
+    alignas(16) float lse2[kStages][kQt], delta[kStages][kQt];
+};
+static_assert(sizeof(DkvMisc) <= 4096, "misc");
+
+struct DkvMaps {
+    CUtensorMap q, dO, k, kr, v;
+};
+
+__global__ void __launch_bounds__(kThreads, 1) dkv_tc_kernel(const __grid_constant__ DkvMaps maps, const MlaArgs a) {
+    extern __shared__ uint8_t raw[];
+    const uint32_t base = (ptx::smem_u32(raw) + 1023u) & ~1023u;
+    DkvMisc &mi = *reinterpret_cast<DkvMisc *>(raw + (base - ptx::smem_u32(raw)) + kOffMisc);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int h = blockIdx.x % a.H, kc = a.dr ? 3 : 2;
+    if (tid == 0) {
+        for (int i = 0; i < kStages; ++i) ptx::mbar_init(&mi.full[i], 1), ptx::mbar_init(&mi.empty[i], 1);
+        ptx::mbar_init(&mi.k_full, 1);
+        ptx::mbar_init(&mi.v_full, 1);
+        ptx::mbar_init(&mi.s_full[0], 1);
+        ptx::mbar_init(&mi.s_full[1], 1);
+        ptx::mbar_init(&mi.dp_full, 1);
+        ptx::mbar_init(&mi.p_full, 256);
+        ptx::mbar_init(&mi.ds_full, 256);
+        ptx::mbar_init(&mi.done, 1);
+        mi.dead = 0;
+        ptx::fence_mbar_init();
+    }
+    int seq = 0, tile = 0;  // the first keys, which most queries see, first
+    if (!find_tile<kThreads>(a.cu_k, a.num_seqs, 128, blockIdx.x / a.H, mi.find, &seq, &tile)) return;
+    if (warp == 8) {
+        ptx::tmem_alloc(&mi.tmem, kTmemColumns);
+        ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = mi.tmem;
+    volatile uint32_t *dead = &mi.dead;
+    const Place pl = place_of(a, seq);
+    const int j0 = tile * 128;
+    const int first = max(0, j0 - pl.off) / kQt;  // the first query tile that sees key j0
+    const int n = max(0, (pl.lq + kQt - 1) / kQt - first);
+
+    if (warp == 9) {
+        if (n > 0) {
+            if (lane == 0) {
+                ptx::mbar_arrive_expect_tx(&mi.k_full, kc * kChunk);
+                for (int c = 0; c < 2; ++c) tc::tma_load_3d(base + c * kChunk, &maps.k, &mi.k_full, 64 * c, h, pl.k0 + j0);
+                if (a.dr) tc::tma_load_2d(base + 2 * kChunk, &maps.kr, &mi.k_full, 0, pl.k0 + j0);
+            }
+            bool ok = true;
+            int i = 0;
+            for (; i < n; ++i) {
+                const int s = i % kStages, i0 = (first + i) * kQt;
+                if (i >= kStages && !(ok = tc::wait(&mi.empty[s], (i / kStages - 1) & 1, dead))) break;
+                for (int e = lane; e < kQt; e += 32) {
+                    const bool in = i0 + e < pl.lq;
+                    const int64_t at = int64_t(h) * a.Tq + pl.q0 + i0 + e;
+                    mi.lse2[s][e] = in ? a.lse2[at] : 0.f;
+                    mi.delta[s][e] = in ? a.delta[at] : 0.f;
+                }
+                __syncwarp();
+                if (lane == 0) {
+                    const uint32_t dst = base + kOffStages + s * kStage;
+                    ptx::mbar_arrive_expect_tx(&mi.full[s], (kc + 2) * kQChunk);
+                    for (int c = 0; c < kc; ++c)
+                        tc::tma_load_3d(dst + c * kQChunk, &maps.q, &mi.full[s], 64 * c, h, pl.q0 + i0);
+                    for (int c = 0; c < 2; ++c)
+                        tc::tma_load_3d(dst + (3 + c) * kQChunk, &maps.dO, &mi.full[s], 64 * c, h, pl.q0 + i0);
+                    if (i == 0) {
+                        ptx::mbar_arrive_expect_tx(&mi.v_full, 2 * kChunk);
+                        for (int c = 0; c < 2; ++c)
+                            tc::tma_load_3d(base + kOffV + c * kChunk, &maps.v, &mi.v_full, 64 * c, h, pl.k0 + j0);
+                    }
+                }
+            }
+            if (!ok && lane == 0) {  // an error: the copies in flight land before the block ends
+                for (int x = max(0, i - kStages); x < i; ++x)
+                    ptx::mbar_wait_bounded(&mi.full[x % kStages], (x / kStages) & 1, tc::kWaitCycles);
+                ptx::mbar_wait_bounded(&mi.k_full, 0, tc::kWaitCycles);
+                ptx::mbar_wait_bounded(&mi.v_full, 0, tc::kWaitCycles);
+            }
+        }
+    } else if (warp == 8) {
+        if (lane == 0 && n > 0) {
+            constexpr uint32_t kIdS = tc::idesc(128, kQt, false, false), kIdV = tc::idesc(128, 128, false, true);
+            const uint32_t id_k = kc == 3 ? tc::idesc(128, 192, false, true) : kIdV;
+            auto stage = [&](int i) { return base + kOffStages + (i % kStages) * kStage; };
+            auto scores = [&](int i) {
+                if (!tc::wait(&mi.full[i % kStages], (i / kStages) & 1, dead)) return false;
+                ptx::tc_fence_after();
+                for (int c = 0; c < kc; ++c)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        ptx::mma_ss(tmem + (i & 1) * 64, ptx::sdesc_sw128(base + c * kChunk + 32 * k),
+                                    ptx::sdesc_sw128(stage(i) + c * kQChunk + 32 * k), kIdS, c + k > 0);
+                ptx::mma_commit(&mi.s_full[i & 1]);
+                return true;
+            };
+            auto dprobs = [&](int i) {
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        ptx::mma_ss(tmem + kTmDp, ptx::sdesc_sw128(base + kOffV + c * kChunk + 32 * k),
+                                    ptx::sdesc_sw128(stage(i) + (3 + c) * kQChunk + 32 * k), kIdS, c + k > 0);
+                ptx::mma_commit(&mi.dp_full);
+            };
+            bool ok = tc::wait(&mi.k_full, 0, dead) && scores(0) && tc::wait(&mi.v_full, 0, dead);
+            if (ok) ptx::tc_fence_after(), dprobs(0);
+            for (int i = 0; ok && i < n; ++i) {
+                if (i + 1 < n) ok = scores(i + 1);
+                if (!ok || !(ok = tc::wait(&mi.p_full, i & 1, dead))) break;
+                ptx::tc_fence_after();
+#pragma unroll
+                for (int k = 0; k < 4; ++k)  // columns of P: 16 of each half lie at the start of its 32 of S
+                    ptx::mma_ts(tmem + kTmDv, tmem + (i & 1) * 64 + (k >> 1) * 32 + (k & 1) * 8,
+                                ptx::sdesc_sw128_mn(stage(i) + 3 * kQChunk + 2048 * k, kQChunk, 1024), kIdV, i + k > 0);
+                if (!(ok = tc::wait(&mi.ds_full, i & 1, dead))) break;
+                ptx::tc_fence_after();
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    ptx::mma_ts(tmem + kTmDk, tmem + kTmDp + (k >> 1) * 32 + (k & 1) * 8,
+                                ptx::sdesc_sw128_mn(stage(i) + 2048 * k, kQChunk, 1024), id_k, i + k > 0);
+                ptx::mma_commit(&mi.empty[i % kStages]);
+                if (i + 1 < n) dprobs(i + 1);
+            }
+            ptx::mma_commit(&mi.done);
+            if (!ok) ptx::mbar_wait_bounded(&mi.done, 0, tc::kWaitCycles);  // an error: nothing in flight at the end
+        }
+        __syncwarp();
+    } else {
+        const int half = warp >> 2, w = warp & 3, row = w * 32 + lane, j = j0 + row;
+        const uint32_t at = tmem + (uint32_t(w) << 21) + half * 32;
+        const float sl2 = a.scale * kLog2e;
+        bool ok = true;
+        for (int i = 0; i < n; ++i) {
+            const int s = i % kStages, i0 = (first + i) * kQt, c0 = i0 + half * 32;
+            if (!(ok = tc::wait(&mi.s_full[i & 1], (i >> 1) & 1, dead))) break;
+            if (!(ok = tc::wait(&mi.full[s], (i / kStages) & 1, dead))) break;  // complete: orders lse2 and delta
+            ptx::tc_fence_after();
+            uint32_t v[32];
+            ptx::tmem_ld32(at + (i & 1) * 64, v);
+            // columns [lo, hi) of this half are queries that see key j
+            const int lo = a.causal ? j - pl.off - c0 : 0, hi = pl.lq - c0;
+            const bool masked = __any_sync(0xffffffffu, lo > 0 || hi < 32);
+            if (i0 + kQt > pl.lq) {
+                // rows behind the sequence may hold anything: in dV += P^T dO and dK += dS^T Q they have to be zero
+                const int from = (pl.lq - i0) * 8, per = kQt * 8 - from;
+                for (int x = tid; x < per * 5; x += 256)
+                    tc::st_shared_v4(base + kOffStages + s * kStage + (x / per) * kQChunk + (from + x % per) * 16, 0, 0, 0, 0);
+                ptx::fence_proxy_async_smem();
+            }
+            ptx::tmem_wait_ld();
+            float p[32];
+            const float4 *l4 = reinterpret_cast<const float4 *>(&mi.lse2[s][half * 32]);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                const float4 l = l4[c];
+                p[4 * c] = ptx::ex2_approx(fmaf(__uint_as_float(v[4 * c]), sl2, -l.x));
+                p[4 * c + 1] = ptx::ex2_approx(fmaf(__uint_as_float(v[4 * c + 1]), sl2, -l.y));
+                p[4 * c + 2] = ptx::ex2_approx(fmaf(__uint_as_float(v[4 * c + 2]), sl2, -l.z));
+                p[4 * c + 3] = ptx::ex2_approx(fmaf(__uint_as_float(v[4 * c + 3]), sl2, -l.w));
+            }
+            if (masked) {
+#pragma unroll
+                for (int c = 0; c < 32; ++c)
+                    if (c < lo || c >= hi) p[c] = 0.f;
+            }
+            uint32_t x[16];
+#pragma unroll
+            for (int c = 0; c < 16; ++c) x[c] = tc::pack_bf16(p[2 * c], p[2 * c + 1]);
+            ptx::tmem_st16(at + (i & 1) * 64, x);
+            ptx::tmem_wait_st();
+            ptx::tc_fence_before();
+            ptx::mbar_arrive(&mi.p_full);
+            if (!(ok = tc::wait(&mi.dp_full, i & 1, dead))) break;
+            ptx::tc_fence_after();
+            ptx::tmem_ld32(at + kTmDp, v);
+            ptx::tmem_wait_ld();
+            const float4 *d4 = reinterpret_cast<const float4 *>(&mi.delta[s][half * 32]);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                const float4 d = d4[c];
+                p[4 * c] *= __uint_as_float(v[4 * c]) - d.x;
+                p[4 * c + 1] *= __uint_as_float(v[4 * c + 1]) - d.y;
+                p[4 * c + 2] *= __uint_as_float(v[4 * c + 2]) - d.z;
+                p[4 * c + 3] *= __uint_as_float(v[4 * c + 3]) - d.w;
+            }
+            if (masked) {
+#pragma unroll
+                for (int c = 0; c < 32; ++c)
+                    if (c < lo || c >= hi) p[c] = 0.f;
+            }
+#pragma unroll
+            for (int c = 0; c < 16; ++c) x[c] = tc::pack_bf16(p[2 * c], p[2 * c + 1]);
+            ptx::tmem_st16(at + kTmDp, x);
+            ptx::tmem_wait_st();
+            ptx::tc_fence_before();
+            ptx::mbar_arrive(&mi.ds_full);
+        }
+        if (ok && n > 0) ok = tc::wait(&mi.done, 0, dead);
+        ptx::tc_fence_after();
+        if (ok) {
+            // warpgroup 0 writes dv, warpgroup 1 dk; each half of the shared part's share
+            const uint32_t lanes = tmem + (uint32_t(w) << 21);
+            const int64_t row_at = int64_t(pl.k0 + j) * a.H + h;
+            __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(half ? a.dk : a.dv_out) + row_at * 128;
+            const float f = half ? a.scale : 1.f;
+            auto load = [&](uint32_t col, uint32_t (&v)[32]) {
+                if (n > 0) {
+                    ptx::tmem_ld32(lanes + col, v);
+                    ptx::tmem_wait_ld();
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) v[e] = 0;
+                }
+            };
+            uint32_t v[32];
+            for (int c = 0; c < 4; ++c) {
+                load((half ? kTmDk : kTmDv) + 32 * c, v);
+                if (j < pl.lk) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8) {
+                        uint4 x;
+                        x.x = tc::pack_bf16(__uint_as_float(v[e]) * f, __uint_as_float(v[e + 1]) * f);
+                        x.y = tc::pack_bf16(__uint_as_float(v[e + 2]) * f, __uint_as_float(v[e + 3]) * f);
+                        x.z = tc::pack_bf16(__uint_as_float(v[e + 4]) * f, __uint_as_float(v[e + 5]) * f);
+                        x.w = tc::pack_bf16(__uint_as_float(v[e + 6]) * f, __uint_as_float(v[e + 7]) * f);
+                        reinterpret_cast<uint4 *>(out)[4 * c + e / 8] = x;
+                    }
+                }
+            }
+            if (a.dr) {
+                load(kTmDk + 128 + 32 * half, v);
+                float4 *part = reinterpret_cast<float4 *>(a.dkr_partial + (int64_t(h) * a.Tk + pl.k0 + j) * 64 + 32 * half);
+                if (j < pl.lk) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4)
+                        part[e / 4] = make_float4(__uint_as_float(v[e]) * a.scale, __uint_as_float(v[e + 1]) * a.scale,
+                                                  __uint_as_float(v[e + 2]) * a.scale, __uint_as_float(v[e + 3]) * a.scale);
+                }
+            }
+        }
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == 8) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, kTmemColumns);
+    }
+}
+
+// ------------------------------------------------------------------------------ dq
+// Shared memory: Q (3 chunks), dO (2), keys twice 3, values 2.
+constexpr uint32_t kOffDo = 3 * kChunk, kOffK = 5 * kChunk, kOffVq = 11 * kChunk, kOffMiscQ = 13 * kChunk;
+constexpr uint32_t kDqSmem = kOffMiscQ + 1024 + 1024;
+constexpr uint32_t kTqDp = 128, kTqDq = 256, kTqDs = 448;
+
+struct DqMisc {
+    uint64_t q_full, do_full, k_full[2], k_empty[2], v_full, v_empty, s_full, s_read, dp_full, ds_full, done;
+    int64_t find[kThreads / 32 + 2];
+    uint32_t tmem, dead;
+};
+static_assert(sizeof(DqMisc) <= 1024, "misc");
+
+__global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constant__ DkvMaps maps, const MlaArgs a) {
+    extern __shared__ uint8_t raw[];
+    const uint32_t base = (ptx::smem_u32(raw) + 1023u) & ~1023u;
+    DqMisc &mi = *reinterpret_cast<DqMisc *>(raw + (base - ptx::smem_u32(raw)) + kOffMiscQ);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int h = blockIdx.x % a.H, kc = a.dr ? 3 : 2;
+    if (tid == 0) {
+        for (uint64_t *b : {&mi.q_full, &mi.do_full, &mi.k_full[0], &mi.k_full[1], &mi.k_empty[0], &mi.k_empty[1],
+                            &mi.v_full, &mi.v_empty, &mi.s_full, &mi.dp_full, &mi.done})
+            ptx::mbar_init(b, 1);
+        ptx::mbar_init(&mi.s_read, 256);
+        ptx::mbar_init(&mi.ds_full, 256);
+        mi.dead = 0;
+        ptx::fence_mbar_init();
+    }
+    int seq = 0, tile = 0;  // the last queries, which see most keys, first
+    if (!find_tile<kThreads>(a.cu_q, a.num_seqs, 128, gridDim.x / a.H - 1 - blockIdx.x / a.H, mi.find, &seq, &tile)) return;
+    if (warp == 8) {
+        ptx::tmem_alloc(&mi.tmem, kTmemColumns);
+        ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = mi.tmem;
+    volatile uint32_t *dead = &mi.dead;
+    const Place pl = place_of(a, seq);
+    const int i0 = tile * 128;
+    auto key_end = [&](int i) { return a.causal ? max(0, min(pl.lk, i + 1 + pl.off)) : pl.lk; };
+    const int n = (key_end(min(i0 + 128, pl.lq) - 1) + 127) / 128;
+
+    if (warp == 9) {
+        if (lane == 0 && n > 0) {
+            auto load_k = [&](int j) {
+                if (j >= 2 && !tc::wait(&mi.k_empty[j & 1], (j / 2 - 1) & 1, dead)) return false;
+                const uint32_t dst = base + kOffK + (j & 1) * 3 * kChunk;
+                ptx::mbar_arrive_expect_tx(&mi.k_full[j & 1], kc * kChunk);
+                for (int c = 0; c < 2; ++c)
+                    tc::tma_load_3d(dst + c * kChunk, &maps.k, &mi.k_full[j & 1], 64 * c, h, pl.k0 + j * 128);
+                if (a.dr) tc::tma_load_2d(dst + 2 * kChunk, &maps.kr, &mi.k_full[j & 1], 0, pl.k0 + j * 128);
+                return true;
+            };
+            ptx::mbar_arrive_expect_tx(&mi.q_full, kc * kChunk);
+            for (int c = 0; c < kc; ++c) tc::tma_load_3d(base + c * kChunk, &maps.q, &mi.q_full, 64 * c, h, pl.q0 + i0);
+            int ks = 0, vs = 0;  // loads begun
+            bool ok = load_k(ks++);
+            ptx::mbar_arrive_expect_tx(&mi.do_full, 2 * kChunk);
+            for (int c = 0; c < 2; ++c)
+                tc::tma_load_3d(base + kOffDo + c * kChunk, &maps.dO, &mi.do_full, 64 * c, h, pl.q0 + i0);
+            for (int j = 0; ok && j < n; ++j) {
+                if (j && !(ok = tc::wait(&mi.v_empty, (j - 1) & 1, dead))) break;
+                ptx::mbar_arrive_expect_tx(&mi.v_full, 2 * kChunk);
+                for (int c = 0; c < 2; ++c)
+                    tc::tma_load_3d(base + kOffVq + c * kChunk, &maps.v, &mi.v_full, 64 * c, h, pl.k0 + j * 128);
+                ++vs;
+                if (j + 1 < n && (ok = load_k(j + 1))) ++ks;
+            }
+            if (!ok) {  // an error: the copies in flight land before the block ends
+                ptx::mbar_wait_bounded(&mi.q_full, 0, tc::kWaitCycles);
+                ptx::mbar_wait_bounded(&mi.do_full, 0, tc::kWaitCycles);
+                for (int j = max(0, ks - 2); j < ks; ++j)
+                    ptx::mbar_wait_bounded(&mi.k_full[j & 1], (j / 2) & 1, tc::kWaitCycles);
+                if (vs) ptx::mbar_wait_bounded(&mi.v_full, (vs - 1) & 1, tc::kWaitCycles);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 8) {
+        if (lane == 0 && n > 0) {
+            constexpr uint32_t kIdS = tc::idesc(128, 128, false, false);
+            const uint32_t id_q = tc::idesc(128, 64 * kc, false, true);
+            auto keys = [&](int j) { return base + kOffK + (j & 1) * 3 * kChunk; };
+            auto scores = [&](int j) {
+                if (!tc::wait(&mi.k_full[j & 1], (j >> 1) & 1, dead)) return false;
+                ptx::tc_fence_after();
+                for (int c = 0; c < kc; ++c)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        ptx::mma_ss(tmem, ptx::sdesc_sw128(base + c * kChunk + 32 * k),
+                                    ptx::sdesc_sw128(keys(j) + c * kChunk + 32 * k), kIdS, c + k > 0);
+                ptx::mma_commit(&mi.s_full);
+                return true;
+            };
+            auto dprobs = [&](int j) {
+                if (!tc::wait(&mi.v_full, j & 1, dead)) return false;
+                ptx::tc_fence_after();
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        ptx::mma_ss(tmem + kTqDp, ptx::sdesc_sw128(base + kOffDo + c * kChunk + 32 * k),
+                                    ptx::sdesc_sw128(base + kOffVq + c * kChunk + 32 * k), kIdS, c + k > 0);
+                ptx::mma_commit(&mi.dp_full);
+                ptx::mma_commit(&mi.v_empty);
+                return true;
+            };
+            bool ok = tc::wait(&mi.q_full, 0, dead) && scores(0) && tc::wait(&mi.do_full, 0, dead) && dprobs(0);
+            for (int j = 0; ok && j < n; ++j) {
+                if (j + 1 < n) {
+                    ok = tc::wait(&mi.s_read, j & 1, dead);
+                    ptx::tc_fence_after();
+                    ok = ok && scores(j + 1);
+                }
+                if (!ok || !(ok = tc::wait(&mi.ds_full, j & 1, dead))) break;
+                ptx::tc_fence_after();
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    ptx::mma_ts(tmem + kTqDq, tmem + kTqDs + 8 * k, ptx::sdesc_sw128_mn(keys(j) + 2048 * k, kChunk, 1024), id_q,
+                                j + k > 0);
+                ptx::mma_commit(&mi.k_empty[j & 1]);
+                if (j + 1 < n) ok = dprobs(j + 1);
+            }
+            ptx::mma_commit(&mi.done);
+            if (!ok) ptx::mbar_wait_bounded(&mi.done, 0, tc::kWaitCycles);  // an error: nothing in flight at the end
+        }
+        __syncwarp();
+    } else {
+        const int half = warp >> 2, w = warp & 3, row = w * 32 + lane, r = i0 + row;
+        const uint32_t lanes = tmem + (uint32_t(w) << 21);
+        const float sl2 = a.scale * kLog2e;
+        const int end = r < pl.lq ? key_end(r) : 0;
+        const int64_t stat = int64_t(h) * a.Tq + pl.q0 + r;
+        const float lse2 = r < pl.lq ? a.lse2[stat] : 0.f, delta = r < pl.lq ? a.delta[stat] : 0.f;
+        bool ok = true;
+        for (int j = 0; j < n; ++j) {
+            if (!(ok = tc::wait(&mi.s_full, j & 1, dead))) break;
+            ptx::tc_fence_after();
+            uint32_t v[2][32];
+            ptx::tmem_ld32(lanes + 64 * half, v[0]);
+            ptx::tmem_ld32(lanes + 64 * half + 32, v[1]);
+            ptx::tmem_wait_ld();
+            ptx::tc_fence_before();
+            ptx::mbar_arrive(&mi.s_read);
+            const int seen = end - j * 128 - 64 * half;  // columns of this half that the row sees
+            const bool masked = __any_sync(0xffffffffu, seen < 64);
+            float p[64];
+#pragma unroll
+            for (int c = 0; c < 64; ++c) {
+                p[c] = ptx::ex2_approx(fmaf(__uint_as_float(v[c >> 5][c & 31]), sl2, -lse2));
+            }
+            if (pl.lk - j * 128 < 128) {
+                // key rows behind the sequence may hold anything: in dQ += dS K they have to be zero
+                const int from = max(0, pl.lk - j * 128) * 8, per = 1024 - from;
+                for (int x = tid; x < per * kc; x += 256)
+                    tc::st_shared_v4(base + kOffK + ((j & 1) * 3 + x / per) * kChunk + (from + x % per) * 16, 0, 0, 0, 0);
+                ptx::fence_proxy_async_smem();
+            }
+            if (!(ok = tc::wait(&mi.dp_full, j & 1, dead))) break;  // the last dQ has read dS, too
+            ptx::tc_fence_after();
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                ptx::tmem_ld32(lanes + kTqDp + 64 * half + 32 * g, v[0]);
+                ptx::tmem_wait_ld();
+                uint32_t x[16];
+#pragma unroll
+                for (int c = 0; c < 16; ++c) {
+                    float y = p[32 * g + 2 * c] * (__uint_as_float(v[0][2 * c]) - delta);
+                    float z = p[32 * g + 2 * c + 1] * (__uint_as_float(v[0][2 * c + 1]) - delta);
+                    if (masked) {
+                        if (32 * g + 2 * c >= seen) y = 0.f;
+                        if (32 * g + 2 * c + 1 >= seen) z = 0.f;
+                    }
+                    x[c] = tc::pack_bf16(y, z);
+                }
+                ptx::tmem_st16(lanes + kTqDs + 32 * half + 16 * g, x);
+            }
+            ptx::tmem_wait_st();
+            ptx::tc_fence_before();
+            ptx::mbar_arrive(&mi.ds_full);
+        }
+        if (ok && n > 0) ok = tc::wait(&mi.done, 0, dead);
+        ptx::tc_fence_after();
+        if (ok) {
+            const int width = 64 * kc;
+            uint4 *out = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.dq) + (int64_t(pl.q0 + r) * a.H + h) * width);
+            for (int c = half; c < 2 * kc; c += 2) {  // 32-column groups, in turn
+                uint32_t v[32];
+                if (n > 0) {
+                    ptx::tmem_ld32(lanes + kTqDq + 32 * c, v);
+                    ptx::tmem_wait_ld();
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) v[e] = 0;
+                }
+                if (r < pl.lq) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8) {
+                        const float f = a.scale;
+                        uint4 x;
+                        x.x = tc::pack_bf16(__uint_as_float(v[e]) * f, __uint_as_float(v[e + 1]) * f);
+                        x.y = tc::pack_bf16(__uint_as_float(v[e + 2]) * f, __uint_as_float(v[e + 3]) * f);
+                        x.z = tc::pack_bf16(__uint_as_float(v[e + 4]) * f, __uint_as_float(v[e + 5]) * f);
+                        x.w = tc::pack_bf16(__uint_as_float(v[e + 6]) * f, __uint_as_float(v[e + 7]) * f);
+                        out[4 * c + e / 8] = x;
+                    }
+                }
+            }
+        }
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == 8) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, kTmemColumns);
+    }
+}
+
+template <typename K> cudaError_t launch(K *kernel, const DkvMaps &maps, int64_t tiles, uint32_t smem, const MlaArgs &a, cudaStream_t st) {
+    if (tiles == 0) return cudaSuccess;
+    if (tiles * a.H > INT32_MAX) return cudaErrorInvalidValue;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    if (e != cudaSuccess) return e;
+    kernel<<<unsigned(tiles * a.H), kThreads, smem, st>>>(maps, a);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+// After launch_mla_delta (delta and lse2), before launch_mla_dkr_reduce.
+cudaError_t launch_mla_backward_tc(const MlaArgs &a, cudaStream_t st) {
+    const int64_t dO_st = int64_t(a.H) * 128;
+    DkvMaps kv{}, qs{};
+    bool ok = tc::rows_map(&kv.q, a.q, 128 + a.dr, a.H, a.Tq, a.q_st, a.q_sh, kQt) &&
+              tc::rows_map(&kv.dO, a.dO, 128, a.H, a.Tq, dO_st, 128, kQt) &&
+              tc::rows_map(&qs.q, a.q, 128 + a.dr, a.H, a.Tq, a.q_st, a.q_sh, 128) &&
+              tc::rows_map(&qs.dO, a.dO, 128, a.H, a.Tq, dO_st, 128, 128) &&
+              tc::rows_map(&kv.k, a.k, 128, a.H, a.Tk, a.k_st, a.k_sh, 128) &&
+              tc::rows_map(&kv.v, a.v, 128, a.H, a.Tk, a.v_st, a.v_sh, 128) &&
+              (a.dr == 0 || tc::rope_map(&kv.kr, a.k_rope, a.Tk, a.kr_st, 128));
+    if (!ok) return cudaErrorInvalidValue;
+    qs.k = kv.k;
+    qs.v = kv.v;
+    qs.kr = kv.kr;
+    const cudaError_t e = launch(dkv_tc_kernel, kv, count_tiles(a.cu_k_host, a.num_seqs, 128), kDkvSmem, a, st);
+    if (e != cudaSuccess) return e;
+    return launch(dq_tc_kernel, qs, count_tiles(a.cu_q_host, a.num_seqs, 128), kDqSmem, a, st);
+}
+
+cudaError_t mla_backward_fault(cudaStream_t st, unsigned int *out) { return mla_fault_read(st, out); }
+
+}  // namespace kda

@@ -50,7 +50,8 @@ struct MlaArgs {  // mla_prefill and mla_backward
     // backward
     const void *dO;
     void *dq, *dk, *dk_rope, *dv_out;
-    float *delta;       // [Tq, H]: sum_c dO * o
+    float *delta;       // [H, Tq]: sum_c dO * o
+    float *lse2;        // [H, Tq]: lse log2(e)
     float *dkr_partial; // [H, Tk, dr]: each head's share of dk_rope
 };
 
@@ -82,6 +83,8 @@ cudaError_t launch_mla_decode(const MlaDecodeArgs &a, cudaStream_t st);
 bool mla_tc_supported(const MlaArgs &a);
 cudaError_t launch_mla_prefill_tc(const MlaArgs &a, cudaStream_t st);
 cudaError_t mla_prefill_fault(cudaStream_t st, unsigned int *out);
+cudaError_t launch_mla_backward_tc(const MlaArgs &a, cudaStream_t st);
+cudaError_t mla_backward_fault(cudaStream_t st, unsigned int *out);
 cudaError_t launch_mla_prefill_simt(const MlaArgs &a, cudaStream_t st);
 cudaError_t launch_mla_backward_simt(const MlaArgs &a, cudaStream_t st);
 cudaError_t launch_mla_delta(const MlaArgs &a, cudaStream_t st);

@@ -141,8 +141,7 @@ __device__ __forceinline__ void tile_grads(const MlaArgs &a, const Rows &w, int 
         const int r = i0 + 4 * ty + i;
         const bool in = r < w.lq;
         const int end = in ? key_end(a, w, r) - j0 : 0;
-        const int64_t at = int64_t(w.q0 + r) * a.H + h;
-        const float lse = in ? a.lse[at] : 0.f, delta = in ? a.delta[at] : 0.f;
+        const float lse = in ? a.lse[int64_t(w.q0 + r) * a.H + h] : 0.f, delta = in ? a.delta[int64_t(h) * a.Tq + w.q0 + r] : 0.f;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const bool seen = tx + 16 * j < end;
@@ -249,7 +248,7 @@ template <typename T> __global__ void __launch_bounds__(kThreads) dq_kernel(cons
     }
 }
 
-// delta[t][h] = sum_c dO o, one warp per (token, head) of the sequences' rows.
+// delta[h][t] = sum_c dO o and lse2[h][t] = lse log2(e), one warp per (token, head) of the sequences' rows.
 template <typename T> __global__ void delta_kernel(const MlaArgs a) {
     const int64_t row = int64_t(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
     if (row >= a.Tq * a.H) return;
@@ -258,7 +257,11 @@ template <typename T> __global__ void delta_kernel(const MlaArgs a) {
     for (int c = threadIdx.x & 31; c < a.dv; c += 32) s = fmaf(to_f32(x[c]), to_f32(y[c]), s);
 #pragma unroll
     for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if ((threadIdx.x & 31) == 0) a.delta[row] = s;
+    if ((threadIdx.x & 31) == 0) {
+        const int64_t at = row % a.H * a.Tq + row / a.H;
+        a.delta[at] = s;
+        a.lse2[at] = a.lse[row] * 1.4426950408889634f;
+    }
 }
 
 // dk_rope[t][c] = sum_h partial[h][t][c], in the order of the heads.
