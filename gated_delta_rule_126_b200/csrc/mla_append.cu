@@ -1,8 +1,7 @@
 // mla_append: RMSNorm of the latent, position rotation of the shared key part and of the
 // queries' part, and the write into the paged cache, in one pass over the new tokens.
 //
-// One block per token: the block finds its sequence by a binary search over cu_seqlens,
-// forms the token's d_rope/2 angles once (float64 product and reduction: a float32 product
+// One block per token: the block finds its sequence from cu_seqlens, forms the token's d_rope/2 angles once (float64 product and reduction: a float32 product
 // at position 10^6 is off by 0.03 rad) and shares them between the key part and all heads.
 // Bound by memory: each input element is read once and each output written once.
 #include <algorithm>
@@ -50,64 +49,94 @@ template <typename T, int V> __device__ __forceinline__ void store_vec(T *p, con
 }
 
 // One item of rotation work: V channels of the first half and their partners (half-split
-// pairs), or 2V neighbouring channels (interleaved pairs).  dst and dst2 may be NULL.
-template <typename T, int V>
-__device__ __forceinline__ void rotate_item(const T *src, T *dst, T *dst2, int item, int half, bool interleaved,
-                                            const float2 *cs, bool turn) {
-    float a[V], b[V], x[V], y[V];
-    const int o0 = interleaved ? 2 * V * item : V * item;
-    const int o1 = interleaved ? o0 + V : o0 + half;
-    load_vec<T, V>(src + o0, a);
-    load_vec<T, V>(src + o1, b);
-    if (!turn) {
+// pairs), or 2V neighbouring channels (interleaved pairs).
+template <typename T, int V> struct Item {
+    float a[V], b[V];
+    static __device__ __forceinline__ int first(int item, bool interleaved) { return interleaved ? 2 * V * item : V * item; }
+    static __device__ __forceinline__ int second(int item, int half, bool interleaved) {
+        return interleaved ? 2 * V * item + V : V * item + half;
+    }
+    __device__ __forceinline__ void load(const T *src, int item, int half, bool interleaved) {
+        load_vec<T, V>(src + first(item, interleaved), a);
+        load_vec<T, V>(src + second(item, half, interleaved), b);
+    }
+    __device__ __forceinline__ void turn(int item, bool interleaved, const float2 *cs) {
+        if (!interleaved || V == 1) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) x[i] = a[i], y[i] = b[i];
-    } else if (!interleaved) {
+            for (int i = 0; i < V; ++i) {
+                const float2 w = cs[V * item + i];
+                const float x = a[i], y = b[i];
+                a[i] = x * w.x - y * w.y;
+                b[i] = x * w.y + y * w.x;
+            }
+        } else {
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const float2 w = cs[V * item + i];
-            x[i] = a[i] * w.x - b[i] * w.y;
-            y[i] = a[i] * w.y + b[i] * w.x;
-        }
-    } else if constexpr (V == 1) {
-        const float2 w = cs[item];
-        x[0] = a[0] * w.x - b[0] * w.y;
-        y[0] = a[0] * w.y + b[0] * w.x;
-    } else {
-#pragma unroll
-        for (int i = 0; i < V / 2; ++i) {
-            const float2 w = cs[V * item + i], u = cs[V * item + V / 2 + i];
-            x[2 * i] = a[2 * i] * w.x - a[2 * i + 1] * w.y;
-            x[2 * i + 1] = a[2 * i] * w.y + a[2 * i + 1] * w.x;
-            y[2 * i] = b[2 * i] * u.x - b[2 * i + 1] * u.y;
-            y[2 * i + 1] = b[2 * i] * u.y + b[2 * i + 1] * u.x;
+            for (int i = 0; i < V / 2; ++i) {
+                const float2 w = cs[V * item + i], u = cs[V * item + V / 2 + i];
+                float x = a[2 * i], y = a[2 * i + 1];
+                a[2 * i] = x * w.x - y * w.y;
+                a[2 * i + 1] = x * w.y + y * w.x;
+                x = b[2 * i], y = b[2 * i + 1];
+                b[2 * i] = x * u.x - y * u.y;
+                b[2 * i + 1] = x * u.y + y * u.x;
+            }
         }
     }
-    if (dst) store_vec<T, V>(dst + o0, x), store_vec<T, V>(dst + o1, y);
-    if (dst2) store_vec<T, V>(dst2 + o0, x), store_vec<T, V>(dst2 + o1, y);
+    __device__ __forceinline__ void store(T *dst, int item, int half, bool interleaved) const {
+        store_vec<T, V>(dst + first(item, interleaved), a);
+        store_vec<T, V>(dst + second(item, half, interleaved), b);
+    }
+};
+
+// The last b with cu[b] <= t, by one warp: 32 offsets a step, the steps' loads independent.
+__device__ __forceinline__ int find_sequence(const int32_t *cu, int num_seqs, int64_t t) {
+    int lo = 0, hi = num_seqs;
+    while (hi - lo > 256) {
+        const int mid = (lo + hi) >> 1;
+        if (cu[mid] <= t) lo = mid;
+        else hi = mid;
+    }
+    int count = 0;
+#pragma unroll 4
+    for (int i = lo + 1 + int(threadIdx.x & 31); i - int(threadIdx.x & 31) < hi; i += 32)
+        count += __popc(__ballot_sync(0xffffffffu, i < hi && cu[i] <= t));
+    return lo + count;
 }
 
+// The inputs' loads come first: they need only t, and the way to the cache row (offsets, past,
+// page) takes several dependent loads.
 template <typename T, int V> __global__ void __launch_bounds__(kThreads) append_kernel(const MlaAppendArgs a) {
     __shared__ float2 cs[kMaxRope / 2];
     __shared__ float warp_sum[kThreads / 32];
     const int64_t t = blockIdx.x;
-    const int tid = threadIdx.x;
-    // the sequence of row t: the last b with cu[b] <= t
-    int lo = 0, hi = a.num_seqs;
-    while (lo + 1 < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (a.cu[mid] <= t) lo = mid;
-        else hi = mid;
+    const int tid = threadIdx.x, half = a.dr / 2, items = half / V;
+    const int q_items = a.q_rope ? items * a.H : 0;
+    // latent: kept in registers between the sum of squares and the store
+    constexpr int kChunks = (kMaxLatent + kThreads * V - 1) / (kThreads * V);
+    float x[kChunks][V];
+    const T *c_row = static_cast<const T *>(a.c) + t * a.c_stride;
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) {
+        const int j = (i * kThreads + tid) * V;
+        if (j < a.dc) load_vec<T, V>(c_row + j, x[i]);
     }
-    if (t < a.cu[lo] || t >= a.cu[lo + 1]) return;  // behind the last sequence
-    const int64_t pos = int64_t(a.past[lo]) + (t - a.cu[lo]);
+    // the first queries' item of this thread; the last threads take the key part's
+    Item<T, V> q, k;
+    const T *q_row = static_cast<const T *>(a.q_rope) + t * a.q_st;
+    T *q_to = static_cast<T *>(a.q_out) + t * a.qo_st;
+    const int k_item = kThreads - 1 - tid;
+    if (tid < q_items) q.load(q_row + tid / items * a.q_sh, tid % items, half, a.interleaved);
+    if (k_item < items) k.load(static_cast<const T *>(a.k_rope) + t * a.k_rope_stride, k_item, half, a.interleaved);
+
+    const int b = find_sequence(a.cu, a.num_seqs, t);
+    if (t < a.cu[b] || t >= a.cu[b + 1]) return;  // behind the last sequence
+    const int64_t pos = int64_t(a.past[b]) + (t - a.cu[b]);
     T *row = nullptr;
     if (pos >= 0 && pos / a.page_size < a.max_pages) {
-        const int32_t page = a.page_table[int64_t(lo) * a.max_pages + pos / a.page_size];
+        const int32_t page = a.page_table[int64_t(b) * a.max_pages + pos / a.page_size];
         if (page >= 0 && page < a.num_pages)
             row = static_cast<T *>(a.cache) + (int64_t(page) * a.page_size + pos % a.page_size) * (a.dc + a.dr);
     }
-    const int half = a.dr / 2;
     const bool turn = a.inv_freq != nullptr;
     if (turn && tid < half) {
         const double ang = double(pos) * double(a.inv_freq[tid]);
@@ -116,20 +145,12 @@ template <typename T, int V> __global__ void __launch_bounds__(kThreads) append_
         sincosf(float(ang - two_pi * rint(ang / two_pi)), &s, &c);
         cs[tid] = make_float2(c, s);
     }
-    // latent: kept in registers between the sum of squares and the store
-    constexpr int kChunks = (kMaxLatent + kThreads * V - 1) / (kThreads * V);
-    float x[kChunks][V];
-    const T *c_row = static_cast<const T *>(a.c) + t * a.c_stride;
     float ss = 0.f;
 #pragma unroll
-    for (int i = 0; i < kChunks; ++i) {
-        const int j = (i * kThreads + tid) * V;
-        if (j < a.dc) {
-            load_vec<T, V>(c_row + j, x[i]);
+    for (int i = 0; i < kChunks; ++i)
 #pragma unroll
-            for (int e = 0; e < V; ++e) ss = fmaf(x[i][e], x[i][e], ss);
-        }
-    }
+        for (int e = 0; e < V; ++e)
+            if ((i * kThreads + tid) * V < a.dc) ss = fmaf(x[i][e], x[i][e], ss);
 #pragma unroll
     for (int d = 16; d; d >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, d);
     if ((tid & 31) == 0) warp_sum[tid >> 5] = ss;
@@ -154,21 +175,16 @@ template <typename T, int V> __global__ void __launch_bounds__(kThreads) append_
             if (c_out) store_vec<T, V>(c_out + j, x[i]);
         }
     }
-    if (a.dr == 0) return;
-    // rotation: the key part and the queries of every head, `items` pieces each
-    const int items = half / V;
-    const int heads = a.q_rope ? a.H : 0;
-    for (int w = tid; w < items * (heads + 1); w += kThreads) {
-        const int h = w / items - 1, item = w % items;
-        if (h < 0) {
-            const T *src = static_cast<const T *>(a.k_rope) + t * a.k_rope_stride;
-            T *dst2 = a.k_rope_out ? static_cast<T *>(a.k_rope_out) + t * a.dr : nullptr;
-            rotate_item<T, V>(src, row ? row + a.dc : nullptr, dst2, item, half, a.interleaved, cs, turn);
-        } else {
-            const T *src = static_cast<const T *>(a.q_rope) + t * a.q_st + h * a.q_sh;
-            T *dst = static_cast<T *>(a.q_out) + t * a.qo_st + h * a.qo_sh;
-            rotate_item<T, V>(src, dst, nullptr, item, half, a.interleaved, cs, turn);
-        }
+    if (k_item < items) {
+        if (turn) k.turn(k_item, a.interleaved, cs);
+        if (row) k.store(row + a.dc, k_item, half, a.interleaved);
+        if (a.k_rope_out) k.store(static_cast<T *>(a.k_rope_out) + t * a.dr, k_item, half, a.interleaved);
+    }
+    for (int w = tid; w < q_items; w += kThreads) {
+        const int h = w / items, item = w % items;
+        if (w != tid) q.load(q_row + h * a.q_sh, item, half, a.interleaved);
+        if (turn) q.turn(item, a.interleaved, cs);
+        q.store(q_to + h * a.qo_sh, item, half, a.interleaved);
     }
 }
 

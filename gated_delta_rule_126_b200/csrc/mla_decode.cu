@@ -151,19 +151,20 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(const MlaDecodeArgs a,
     }
 }
 
-// Joins the parts of the items that are split over blocks: o = sum_i e^(m_i - m) o_i / sum_i e^(m_i - m) l_i.
-// One block per (block of the main kernel, query row); four groups of 128 threads take the
-// parts in turn, group sums are added in a fixed order.
-constexpr int kJoinThreads = 512;
+// Joins the parts of the sequences that are split over groups: o = sum_i e^(m_i - m) o_i / sum_i e^(m_i - m) l_i,
+// the parts in order.  One small block per (block of the main kernel, query row), four channels a
+// thread, so that a call's thousands of short rows are all resident at once.  It is launched while the main
+// kernel still runs and waits for its end on the device.
+constexpr int kJoinThreads = 128;
 template <typename T>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const MlaDecodeArgs a, const MlaDecodeShape shape) {
-    __shared__ float acc[4][512];
-    __shared__ float top[kJoinThreads / 32], sums[kJoinThreads / 32];
+    __shared__ float stat[kJoinThreads / 32];
     const int x = blockIdx.x, row = blockIdx.y, tid = threadIdx.x;
-    const MlaJoin j = static_cast<const MlaJoin *>(a.workspace)[x];
-    if (j.parts == 0) return;
     const int R = a.n * a.H, r0 = (x % shape.row_tiles) * shape.row_tile;
     if (r0 + row >= R) return;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const MlaJoin j = static_cast<const MlaJoin *>(a.workspace)[x];
+    if (j.parts == 0) return;
     const float *slots = reinterpret_cast<const float *>(static_cast<const char *>(a.workspace) + mla_meta_bytes(gridDim.x));
     const size_t slot_floats = mla_slot_floats(shape.row_tile, a.dc);
     auto part = [&](int i) { return slots + size_t(i == 0 ? j.first_slot : 2 * (x + i * shape.row_tiles)) * slot_floats; };
@@ -172,35 +173,25 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const MlaDecodeArgs 
     for (int i = tid; i < j.parts; i += kJoinThreads) m = fmaxf(m, part(i)[ml]);
 #pragma unroll
     for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-    if ((tid & 31) == 0) top[tid >> 5] = m;
+    if ((tid & 31) == 0) stat[tid >> 5] = m;
     __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kJoinThreads / 32; ++w) m = fmaxf(m, top[w]);
+    m = fmaxf(fmaxf(stat[0], stat[1]), fmaxf(stat[2], stat[3]));
     const float base = m == -INFINITY ? 0.f : m;
-    float l = 0.f;
-    for (int i = tid; i < j.parts; i += kJoinThreads) l += expf(part(i)[ml] - base) * part(i)[ml + 1];
-#pragma unroll
-    for (int d = 16; d; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
-    if ((tid & 31) == 0) sums[tid >> 5] = l;
-    const int group = tid >> 7, lane = tid & 127;
-    float o[4] = {};  // columns lane + 128 e
-    for (int i = group; i < j.parts; i += 4) {
+    float l = 0.f, o[4] = {};  // channels tid + 128 e
+#pragma unroll 4
+    for (int i = 0; i < j.parts; ++i) {
         const float *p = part(i);
         const float f = expf(p[ml] - base);
+        l = fmaf(f, p[ml + 1], l);
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            if (lane + 128 * e < a.dc) o[e] = fmaf(f, p[row * a.dc + lane + 128 * e], o[e]);
+            if (tid + 128 * e < a.dc) o[e] = fmaf(f, p[row * a.dc + tid + 128 * e], o[e]);
     }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) acc[group][lane + 128 * e] = o[e];
-    __syncthreads();
-    l = 0.f;
-#pragma unroll
-    for (int w = 0; w < kJoinThreads / 32; ++w) l += sums[w];
     const int64_t at = int64_t(j.b) * R + r0 + row;
     const float inv = l == 0.f ? 0.f : 1.f / l;
-    if (tid < a.dc)
-        static_cast<T *>(a.o)[at * a.dc + tid] = from_f32<T>((acc[0][tid] + acc[1][tid] + acc[2][tid] + acc[3][tid]) * inv);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        if (tid + 128 * e < a.dc) static_cast<T *>(a.o)[at * a.dc + tid + 128 * e] = from_f32<T>(o[e] * inv);
     if (a.lse && tid == 0) a.lse[at] = l == 0.f ? -INFINITY : m + logf(l);
 }
 
@@ -237,9 +228,17 @@ cudaError_t launch_mla_decode(const MlaDecodeArgs &a, cudaStream_t st) {
                                                      : launch_simt<__nv_bfloat16>(a, s, st);
     if (e != cudaSuccess) return e;
     const dim3 grid(s.grid(), s.row_tile < a.n * a.H ? s.row_tile : a.n * a.H);
-    if (a.dtype == KDA_DTYPE_F32) join_kernel<float><<<grid, kJoinThreads, 0, st>>>(a, s);
-    else join_kernel<__nv_bfloat16><<<grid, kJoinThreads, 0, st>>>(a, s);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute early{};
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &early;
+    cfg.numAttrs = 1;
+    return a.dtype == KDA_DTYPE_F32 ? cudaLaunchKernelEx(&cfg, join_kernel<float>, a, s)
+                                    : cudaLaunchKernelEx(&cfg, join_kernel<__nv_bfloat16>, a, s);
 }
 
 }  // namespace kda

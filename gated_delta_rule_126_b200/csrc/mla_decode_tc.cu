@@ -30,7 +30,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLazy = 8.f;
 
 struct Misc {
-    uint64_t full[kMaxStages], empty[kMaxStages], s_full[2], p_full, pv_done, q_full, q_empty;
+    uint64_t full[kMaxStages], empty[kMaxStages], s_full[2], p_full, pv_done, q_full, q_empty, drain;
     uint64_t mask[kMaxStages];  // which keys of the stage lie on a page of the pool
     float factor[64];
     uint32_t tmem, dead;
@@ -87,6 +87,7 @@ decode_tc_kernel(const __grid_constant__ Maps maps, const MlaDecodeArgs a, const
         ptx::mbar_init(&mi.pv_done, 1);
         ptx::mbar_init(&mi.q_full, 1);
         ptx::mbar_init(&mi.q_empty, 1);
+        ptx::mbar_init(&mi.drain, 1);
         mi.dead = 0;
         ptx::fence_mbar_init();
     }
@@ -166,56 +167,71 @@ decode_tc_kernel(const __grid_constant__ Maps maps, const MlaDecodeArgs a, const
             // ---------------------------------------------------------------- products
             constexpr uint32_t kIdS = tc::idesc(64, kKeys, false, false), kIdO = tc::idesc(128, RB, true, false);
             const uint32_t qa = base + L.q, pa = base + L.p;
-            int s_stage = 0, pv_stage = 0;
-            uint32_t s_round = 0, n_s = 0, n_pv = 0, items = 0;
-            auto scores = [&]() {  // S of the next loaded tile
-                if (!tc::wait(&mi.full[s_stage], s_round & 1, dead)) return false;
-                ptx::tc_fence_after();
-                if (lane == 0) {
-                    const uint32_t ka = base + s_stage * L.stage_bytes;
-                    for (int c = 0; c < L.chunks; ++c)
+            if (lane == 0) {
+                // Scores run up to two tiles ahead of O's products (two S buffers), as tiles arrive;
+                // whichever of the two can go next goes, so neither waits for the other's input.
+                MlaWalk ws(run), wp(run);
+                bool more = ws.next(a, kKeys, run), ok = true;
+                wp.next(a, kKeys, run);
+                int s_tile = ws.t0, p_tile = wp.t0, s_stage = 0, p_stage = 0;
+                uint32_t s_round = 0, s_item = 0, n_s = 0, n_pv = 0;
+                const uint32_t n_all = uint32_t(run.end - run.start);
+                long long since = clock64();
+                while (n_pv < n_all) {
+                    bool idle = true;
+                    if (more && n_s - n_pv < 2 && (s_tile != ws.t0 || ptx::mbar_try_wait(&mi.q_full, s_item & 1)) &&
+                        ptx::mbar_try_wait(&mi.full[s_stage], s_round & 1)) {
+                        ptx::tc_fence_after();
+                        const uint32_t ka = base + s_stage * L.stage_bytes;
+                        for (int c = 0; c < L.chunks; ++c)
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            ptx::mma_ss(tmem + Tm<RB>::kS + (n_s & 1) * 64, ptx::sdesc_sw128(qa + c * RB * 128 + 32 * k),
-                                        ptx::sdesc_sw128(ka + c * 8192 + 32 * k), kIdS, c + k > 0);
-                    ptx::mma_commit(&mi.s_full[n_s & 1]);
-                }
-                __syncwarp();
-                ++n_s;
-                if (++s_stage == L.stages) s_stage = 0, ++s_round;
-                return true;
-            };
-            bool ok = true;
-            MlaWalk w(run);
-            while (ok && w.next(a, kKeys, run)) {
-                ok = tc::wait(&mi.q_full, items & 1, dead) && scores();
-                ++items;
-                for (int t = w.t0; ok && t < w.t1; ++t) {
-                    if (t + 1 < w.t1) ok = scores();
-                    if (!ok) break;
-                    if (t + 1 >= w.t1 && lane == 0) ptx::mma_commit(&mi.q_empty);
-                    __syncwarp();
-                    if (!(ok = tc::wait(&mi.p_full, n_pv & 1, dead))) break;
-                    ptx::tc_fence_after();
-                    if (lane == 0) {
-                        const uint32_t va = base + pv_stage * L.stage_bytes;
+                            for (int k = 0; k < 4; ++k)
+                                ptx::mma_ss(tmem + Tm<RB>::kS + (n_s & 1) * 64, ptx::sdesc_sw128(qa + c * RB * 128 + 32 * k),
+                                            ptx::sdesc_sw128(ka + c * 8192 + 32 * k), kIdS, c + k > 0);
+                        ptx::mma_commit(&mi.s_full[n_s & 1]);
+                        ++n_s;
+                        if (++s_stage == L.stages) s_stage = 0, ++s_round;
+                        if (++s_tile == ws.t1) {
+                            ptx::mma_commit(&mi.q_empty);
+                            more = ws.next(a, kKeys, run);
+                            s_tile = ws.t0;
+                            ++s_item;
+                        }
+                        idle = false;
+                    }
+                    if (n_s > n_pv && ptx::mbar_try_wait(&mi.p_full, n_pv & 1)) {
+                        ptx::tc_fence_after();
+                        const uint32_t va = base + p_stage * L.stage_bytes;
                         for (int i = 0; i < blocks; ++i)
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
                                 ptx::mma_ss(tmem + i * RB, ptx::sdesc_sw128_mn(va + i * 16384 + 2048 * k, 8192, 1024),
-                                            ptx::sdesc_sw128(pa + 32 * k), kIdO, t > w.t0 || k > 0);
-                        ptx::mma_commit(&mi.empty[pv_stage]);
+                                            ptx::sdesc_sw128(pa + 32 * k), kIdO, p_tile > wp.t0 || k > 0);
+                        ptx::mma_commit(&mi.empty[p_stage]);
                         ptx::mma_commit(&mi.pv_done);
+                        ++n_pv;
+                        if (++p_stage == L.stages) p_stage = 0;
+                        if (++p_tile == wp.t1) {
+                            wp.next(a, kKeys, run);
+                            p_tile = wp.t0;
+                        }
+                        idle = false;
                     }
-                    __syncwarp();
-                    ++n_pv;
-                    if (++pv_stage == L.stages) pv_stage = 0;
+                    if (!idle) {
+                        since = clock64();
+                    } else if (*dead || clock64() - since > tc::kWaitCycles) {
+                        if (!*dead) atomicExch(&mla_fault, 1u);
+                        *dead = 1;
+                        ok = false;
+                        break;
+                    }
+                }
+                if (!ok) {  // an error: the products in flight end before TMEM goes away
+                    ptx::mma_commit(&mi.drain);
+                    ptx::mbar_wait_bounded(&mi.drain, 0, tc::kWaitCycles);
                 }
             }
-            if (!ok && lane == 0) {  // an error: the products in flight end before TMEM goes away
-                ptx::mma_commit(&mi.pv_done);
-                ptx::mbar_wait_bounded(&mi.pv_done, n_pv & 1, tc::kWaitCycles);
-            }
+            __syncwarp();
         } else {
             // ---------------------------------------------------------------- softmax, rescaling, output
             const uint32_t lanes = uint32_t(warp) << 21;  // TMEM lane 32 warp
