@@ -25,66 +25,59 @@ template <> struct Io<__nv_bfloat16> {
     static __device__ void put(__nv_bfloat16 *p, float x) { *p = __float2bfloat16_rn(x); }
 };
 
-// V elements at p as floats (V * sizeof(T) is 16 bytes, or V = 1).
-template <typename T, int V> __device__ __forceinline__ void load_vec(const T *p, float (&x)[V]) {
-    if constexpr (V == 1) {
-        x[0] = Io<T>::get(p);
-    } else {
-        const uint4 w = *reinterpret_cast<const uint4 *>(p);
-        const T *e = reinterpret_cast<const T *>(&w);
-#pragma unroll
-        for (int i = 0; i < V; ++i) x[i] = Io<T>::get(e + i);
-    }
-}
-template <typename T, int V> __device__ __forceinline__ void store_vec(T *p, const float (&x)[V]) {
-    if constexpr (V == 1) {
-        Io<T>::put(p, x[0]);
-    } else {
-        uint4 w;
-        T *e = reinterpret_cast<T *>(&w);
-#pragma unroll
-        for (int i = 0; i < V; ++i) Io<T>::put(e + i, x[i]);
-        *reinterpret_cast<uint4 *>(p) = w;
-    }
-}
+// V elements as they lie in memory: 16 bytes, or one element.
+template <typename T, int V> struct Vec {
+    uint4 w;
+    __device__ __forceinline__ void load(const T *p) { w = *reinterpret_cast<const uint4 *>(p); }
+    __device__ __forceinline__ void store(T *p) const { *reinterpret_cast<uint4 *>(p) = w; }
+    __device__ __forceinline__ float get(int i) const { return Io<T>::get(reinterpret_cast<const T *>(&w) + i); }
+    __device__ __forceinline__ void put(int i, float x) { Io<T>::put(reinterpret_cast<T *>(&w) + i, x); }
+};
+template <typename T> struct Vec<T, 1> {
+    T w;
+    __device__ __forceinline__ void load(const T *p) { w = *p; }
+    __device__ __forceinline__ void store(T *p) const { *p = w; }
+    __device__ __forceinline__ float get(int) const { return Io<T>::get(&w); }
+    __device__ __forceinline__ void put(int, float x) { Io<T>::put(&w, x); }
+};
 
 // One item of rotation work: V channels of the first half and their partners (half-split
 // pairs), or 2V neighbouring channels (interleaved pairs).
 template <typename T, int V> struct Item {
-    float a[V], b[V];
+    Vec<T, V> a, b;
     static __device__ __forceinline__ int first(int item, bool interleaved) { return interleaved ? 2 * V * item : V * item; }
     static __device__ __forceinline__ int second(int item, int half, bool interleaved) {
         return interleaved ? 2 * V * item + V : V * item + half;
     }
     __device__ __forceinline__ void load(const T *src, int item, int half, bool interleaved) {
-        load_vec<T, V>(src + first(item, interleaved), a);
-        load_vec<T, V>(src + second(item, half, interleaved), b);
+        a.load(src + first(item, interleaved));
+        b.load(src + second(item, half, interleaved));
     }
     __device__ __forceinline__ void turn(int item, bool interleaved, const float2 *cs) {
         if (!interleaved || V == 1) {
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 const float2 w = cs[V * item + i];
-                const float x = a[i], y = b[i];
-                a[i] = x * w.x - y * w.y;
-                b[i] = x * w.y + y * w.x;
+                const float x = a.get(i), y = b.get(i);
+                a.put(i, x * w.x - y * w.y);
+                b.put(i, x * w.y + y * w.x);
             }
         } else {
 #pragma unroll
             for (int i = 0; i < V / 2; ++i) {
                 const float2 w = cs[V * item + i], u = cs[V * item + V / 2 + i];
-                float x = a[2 * i], y = a[2 * i + 1];
-                a[2 * i] = x * w.x - y * w.y;
-                a[2 * i + 1] = x * w.y + y * w.x;
-                x = b[2 * i], y = b[2 * i + 1];
-                b[2 * i] = x * u.x - y * u.y;
-                b[2 * i + 1] = x * u.y + y * u.x;
+                float x = a.get(2 * i), y = a.get(2 * i + 1);
+                a.put(2 * i, x * w.x - y * w.y);
+                a.put(2 * i + 1, x * w.y + y * w.x);
+                x = b.get(2 * i), y = b.get(2 * i + 1);
+                b.put(2 * i, x * u.x - y * u.y);
+                b.put(2 * i + 1, x * u.y + y * u.x);
             }
         }
     }
     __device__ __forceinline__ void store(T *dst, int item, int half, bool interleaved) const {
-        store_vec<T, V>(dst + first(item, interleaved), a);
-        store_vec<T, V>(dst + second(item, half, interleaved), b);
+        a.store(dst + first(item, interleaved));
+        b.store(dst + second(item, half, interleaved));
     }
 };
 
@@ -105,20 +98,21 @@ __device__ __forceinline__ int find_sequence(const int32_t *cu, int num_seqs, in
 
 // The inputs' loads come first: they need only t, and the way to the cache row (offsets, past,
 // page) takes several dependent loads.
-template <typename T, int V> __global__ void __launch_bounds__(kThreads) append_kernel(const MlaAppendArgs a) {
+template <typename T, int V> __global__ void __launch_bounds__(kThreads, 12) append_kernel(const MlaAppendArgs a) {
     __shared__ float2 cs[kMaxRope / 2];
     __shared__ float warp_sum[kThreads / 32];
+    __shared__ int64_t place;  // of the cache row, in elements; -1: none, -2: no token
     const int64_t t = blockIdx.x;
     const int tid = threadIdx.x, half = a.dr / 2, items = half / V;
     const int q_items = a.q_rope ? items * a.H : 0;
     // latent: kept in registers between the sum of squares and the store
     constexpr int kChunks = (kMaxLatent + kThreads * V - 1) / (kThreads * V);
-    float x[kChunks][V];
+    Vec<T, V> x[kChunks];
     const T *c_row = static_cast<const T *>(a.c) + t * a.c_stride;
 #pragma unroll
     for (int i = 0; i < kChunks; ++i) {
         const int j = (i * kThreads + tid) * V;
-        if (j < a.dc) load_vec<T, V>(c_row + j, x[i]);
+        if (j < a.dc) x[i].load(c_row + j);
     }
     // the first queries' item of this thread; the last threads take the key part's
     Item<T, V> q, k;
@@ -128,42 +122,59 @@ template <typename T, int V> __global__ void __launch_bounds__(kThreads) append_
     if (tid < q_items) q.load(q_row + tid / items * a.q_sh, tid % items, half, a.interleaved);
     if (k_item < items) k.load(static_cast<const T *>(a.k_rope) + t * a.k_rope_stride, k_item, half, a.interleaved);
 
-    const int b = find_sequence(a.cu, a.num_seqs, t);
-    if (t < a.cu[b] || t >= a.cu[b + 1]) return;  // behind the last sequence
-    const int64_t pos = int64_t(a.past[b]) + (t - a.cu[b]);
-    T *row = nullptr;
-    if (pos >= 0 && pos / a.page_size < a.max_pages) {
-        const int32_t page = a.page_table[int64_t(b) * a.max_pages + pos / a.page_size];
-        if (page >= 0 && page < a.num_pages)
-            row = static_cast<T *>(a.cache) + (int64_t(page) * a.page_size + pos % a.page_size) * (a.dc + a.dr);
+    if (tid < 32) {  // the walk to the cache row and the angles, by the first warp for all
+        const int b = find_sequence(a.cu, a.num_seqs, t);
+        const int64_t at = t - a.cu[b];
+        int64_t to = t < a.cu[b + 1] && at >= 0 ? -1 : -2;
+        const int64_t pos = int64_t(a.past[b]) + at;
+        if (to == -1 && pos >= 0 && pos <= INT32_MAX) {  // a table of pages ends before 2^31 rows
+            const int p = int(pos), entry = p / a.page_size;
+            if (entry < a.max_pages) {
+                const int32_t page = a.page_table[int64_t(b) * a.max_pages + entry];
+                if (page >= 0 && page < a.num_pages)
+                    to = (int64_t(page) * a.page_size + (p - entry * a.page_size)) * (a.dc + a.dr);
+            }
+        }
+        if (tid == 0) place = to;
+        if (a.inv_freq != nullptr && tid < half) {
+            const double ang = double(pos) * double(a.inv_freq[tid]);
+            const double two_pi = 6.283185307179586476925, turns = rint(ang * (1.0 / two_pi));
+            float s, c;
+            sincosf(float(fma(-turns, two_pi, ang)), &s, &c);
+            cs[tid] = make_float2(c, s);
+        }
     }
     const bool turn = a.inv_freq != nullptr;
-    if (turn && tid < half) {
-        const double ang = double(pos) * double(a.inv_freq[tid]);
-        const double two_pi = 6.283185307179586476925;
-        float s, c;
-        sincosf(float(ang - two_pi * rint(ang / two_pi)), &s, &c);
-        cs[tid] = make_float2(c, s);
-    }
     float ss = 0.f;
 #pragma unroll
     for (int i = 0; i < kChunks; ++i)
 #pragma unroll
         for (int e = 0; e < V; ++e)
-            if ((i * kThreads + tid) * V < a.dc) ss = fmaf(x[i][e], x[i][e], ss);
+            if ((i * kThreads + tid) * V < a.dc) ss = fmaf(x[i].get(e), x[i].get(e), ss);
 #pragma unroll
     for (int d = 16; d; d >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, d);
     if ((tid & 31) == 0) warp_sum[tid >> 5] = ss;
     __syncthreads();
+    if (place == -2) return;  // behind the last sequence
+    T *row = place >= 0 ? static_cast<T *>(a.cache) + place : nullptr;
     ss = warp_sum[0] + warp_sum[1] + warp_sum[2] + warp_sum[3];
     if (a.norm_weight) {
         const float r = 1.f / sqrtf(ss / float(a.dc) + a.eps);
 #pragma unroll
         for (int i = 0; i < kChunks; ++i)
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
+            for (int e = 0; e < V; e += 4) {
                 const int j = (i * kThreads + tid) * V + e;
-                if (j < a.dc) x[i][e] *= r * a.norm_weight[j];
+                if (j >= a.dc) continue;
+                if constexpr (V == 1) {
+                    x[i].put(e, x[i].get(e) * (r * a.norm_weight[j]));
+                } else {
+                    const float4 w = *reinterpret_cast<const float4 *>(a.norm_weight + j);
+                    x[i].put(e, x[i].get(e) * (r * w.x));
+                    x[i].put(e + 1, x[i].get(e + 1) * (r * w.y));
+                    x[i].put(e + 2, x[i].get(e + 2) * (r * w.z));
+                    x[i].put(e + 3, x[i].get(e + 3) * (r * w.w));
+                }
             }
     }
     T *c_out = a.c_out ? static_cast<T *>(a.c_out) + t * a.dc : nullptr;
@@ -171,8 +182,8 @@ template <typename T, int V> __global__ void __launch_bounds__(kThreads) append_
     for (int i = 0; i < kChunks; ++i) {
         const int j = (i * kThreads + tid) * V;
         if (j < a.dc) {
-            if (row) store_vec<T, V>(row + j, x[i]);
-            if (c_out) store_vec<T, V>(c_out + j, x[i]);
+            if (row) x[i].store(row + j);
+            if (c_out) x[i].store(c_out + j);
         }
     }
     if (k_item < items) {
@@ -192,7 +203,7 @@ template <typename T, int V> __global__ void __launch_bounds__(kThreads) append_
 template <typename T> bool vector_ok(const MlaAppendArgs &a) {
     constexpr int V = 16 / sizeof(T);
     auto p16 = [](const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; };
-    const void *ptrs[] = {a.c, a.k_rope, a.cache, a.q_rope, a.q_out, a.c_out, a.k_rope_out};
+    const void *ptrs[] = {a.c, a.k_rope, a.cache, a.q_rope, a.q_out, a.c_out, a.k_rope_out, a.norm_weight};
     for (const void *p : ptrs)
         if (!p16(p)) return false;
     if (a.dc % V || (a.dr / 2) % V || a.c_stride % V) return false;
