@@ -139,24 +139,29 @@ __global__ void __launch_bounds__(kThreads, 1) dkv_tc_kernel(const __grid_consta
         if (lane == 0 && n > 0) {
             constexpr uint32_t kIdS = tc::idesc(128, kQt, false, false), kIdV = tc::idesc(128, 128, false, true);
             const uint32_t id_k = kc == 3 ? tc::idesc(128, 192, false, true) : kIdV;
-            auto stage = [&](int i) { return base + kOffStages + (i % kStages) * kStage; };
+            const uint64_t desc = ptx::sdesc_sw128(base), desc_mn = ptx::sdesc_sw128_mn(base, kQChunk, 1024);
+            auto stage = [&](int i) { return kOffStages + (i % kStages) * kStage; };
             auto scores = [&](int i) {
                 if (!tc::wait(&mi.full[i % kStages], (i / kStages) & 1, dead)) return false;
                 ptx::tc_fence_after();
-                for (int c = 0; c < kc; ++c)
+                for (int c = 0; c < kc; ++c) {
+                    const uint64_t kd = tc::moved(desc, c * kChunk), qd = tc::moved(desc, stage(i) + c * kQChunk);
+                    ptx::mma_ss(tmem + (i & 1) * 64, kd, qd, kIdS, c > 0);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        ptx::mma_ss(tmem + (i & 1) * 64, ptx::sdesc_sw128(base + c * kChunk + 32 * k),
-                                    ptx::sdesc_sw128(stage(i) + c * kQChunk + 32 * k), kIdS, c + k > 0);
+                    for (int k = 1; k < 4; ++k)
+                        ptx::mma_ss(tmem + (i & 1) * 64, tc::moved(kd, 32 * k), tc::moved(qd, 32 * k), kIdS, 1);
+                }
                 ptx::mma_commit(&mi.s_full[i & 1]);
                 return true;
             };
             auto dprobs = [&](int i) {
-                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const uint64_t vd = tc::moved(desc, kOffV + c * kChunk), od = tc::moved(desc, stage(i) + (3 + c) * kQChunk);
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        ptx::mma_ss(tmem + kTmDp, ptx::sdesc_sw128(base + kOffV + c * kChunk + 32 * k),
-                                    ptx::sdesc_sw128(stage(i) + (3 + c) * kQChunk + 32 * k), kIdS, c + k > 0);
+                        ptx::mma_ss(tmem + kTmDp, tc::moved(vd, 32 * k), tc::moved(od, 32 * k), kIdS, c + k > 0);
+                }
                 ptx::mma_commit(&mi.dp_full);
             };
             bool ok = tc::wait(&mi.k_full, 0, dead) && scores(0) && tc::wait(&mi.v_full, 0, dead);
@@ -165,16 +170,17 @@ __global__ void __launch_bounds__(kThreads, 1) dkv_tc_kernel(const __grid_consta
                 if (i + 1 < n) ok = scores(i + 1);
                 if (!ok || !(ok = tc::wait(&mi.p_full, i & 1, dead))) break;
                 ptx::tc_fence_after();
+                const uint64_t q_desc = tc::moved(desc_mn, stage(i)), dO_desc = tc::moved(q_desc, 3 * kQChunk);
 #pragma unroll
                 for (int k = 0; k < 4; ++k)  // columns of P: 16 of each half lie at the start of its 32 of S
                     ptx::mma_ts(tmem + kTmDv, tmem + (i & 1) * 64 + (k >> 1) * 32 + (k & 1) * 8,
-                                ptx::sdesc_sw128_mn(stage(i) + 3 * kQChunk + 2048 * k, kQChunk, 1024), kIdV, i + k > 0);
+                                tc::moved(dO_desc, 2048 * k), kIdV, i + k > 0);
                 if (!(ok = tc::wait(&mi.ds_full, i & 1, dead))) break;
                 ptx::tc_fence_after();
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     ptx::mma_ts(tmem + kTmDk, tmem + kTmDp + (k >> 1) * 32 + (k & 1) * 8,
-                                ptx::sdesc_sw128_mn(stage(i) + 2048 * k, kQChunk, 1024), id_k, i + k > 0);
+                                tc::moved(q_desc, 2048 * k), id_k, i + k > 0);
                 ptx::mma_commit(&mi.empty[i % kStages]);
                 if (i + 1 < n) dprobs(i + 1);
             }
@@ -387,26 +393,29 @@ __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constan
         if (lane == 0 && n > 0) {
             constexpr uint32_t kIdS = tc::idesc(128, 128, false, false);
             const uint32_t id_q = tc::idesc(128, 64 * kc, false, true);
-            auto keys = [&](int j) { return base + kOffK + (j & 1) * 3 * kChunk; };
+            const uint64_t desc = ptx::sdesc_sw128(base), desc_mn = ptx::sdesc_sw128_mn(base, kChunk, 1024);
+            auto keys = [&](int j) { return kOffK + (j & 1) * 3 * kChunk; };
             auto scores = [&](int j) {
                 if (!tc::wait(&mi.k_full[j & 1], (j >> 1) & 1, dead)) return false;
                 ptx::tc_fence_after();
-                for (int c = 0; c < kc; ++c)
+                for (int c = 0; c < kc; ++c) {
+                    const uint64_t qd = tc::moved(desc, c * kChunk), kd = tc::moved(qd, keys(j));
+                    ptx::mma_ss(tmem, qd, kd, kIdS, c > 0);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        ptx::mma_ss(tmem, ptx::sdesc_sw128(base + c * kChunk + 32 * k),
-                                    ptx::sdesc_sw128(keys(j) + c * kChunk + 32 * k), kIdS, c + k > 0);
+                    for (int k = 1; k < 4; ++k) ptx::mma_ss(tmem, tc::moved(qd, 32 * k), tc::moved(kd, 32 * k), kIdS, 1);
+                }
                 ptx::mma_commit(&mi.s_full);
                 return true;
             };
             auto dprobs = [&](int j) {
                 if (!tc::wait(&mi.v_full, j & 1, dead)) return false;
                 ptx::tc_fence_after();
+#pragma unroll
                 for (int c = 0; c < 2; ++c)
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        ptx::mma_ss(tmem + kTqDp, ptx::sdesc_sw128(base + kOffDo + c * kChunk + 32 * k),
-                                    ptx::sdesc_sw128(base + kOffVq + c * kChunk + 32 * k), kIdS, c + k > 0);
+                        ptx::mma_ss(tmem + kTqDp, tc::moved(desc, kOffDo + c * kChunk + 32 * k),
+                                    tc::moved(desc, kOffVq + c * kChunk + 32 * k), kIdS, c + k > 0);
                 ptx::mma_commit(&mi.dp_full);
                 ptx::mma_commit(&mi.v_empty);
                 return true;
@@ -422,8 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constan
                 ptx::tc_fence_after();
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
-                    ptx::mma_ts(tmem + kTqDq, tmem + kTqDs + 8 * k, ptx::sdesc_sw128_mn(keys(j) + 2048 * k, kChunk, 1024), id_q,
-                                j + k > 0);
+                    ptx::mma_ts(tmem + kTqDq, tmem + kTqDs + 8 * k, tc::moved(desc_mn, keys(j) + 2048 * k), id_q, j + k > 0);
                 ptx::mma_commit(&mi.k_empty[j & 1]);
                 if (j + 1 < n) ok = dprobs(j + 1);
             }

@@ -166,7 +166,8 @@ decode_tc_kernel(const __grid_constant__ Maps maps, const MlaDecodeArgs a, const
         } else if (warp == 4) {
             // ---------------------------------------------------------------- products
             constexpr uint32_t kIdS = tc::idesc(64, kKeys, false, false), kIdO = tc::idesc(128, RB, true, false);
-            const uint32_t qa = base + L.q, pa = base + L.p;
+            const uint64_t q_desc = ptx::sdesc_sw128(base + L.q), p_desc = ptx::sdesc_sw128(base + L.p),
+                           k_desc = ptx::sdesc_sw128(base), v_desc = ptx::sdesc_sw128_mn(base, 8192, 1024);
             if (lane == 0) {
                 // Scores run up to two tiles ahead of O's products (two S buffers), as tiles arrive;
                 // whichever of the two can go next goes, so neither waits for the other's input.
@@ -182,12 +183,18 @@ decode_tc_kernel(const __grid_constant__ Maps maps, const MlaDecodeArgs a, const
                     if (more && n_s - n_pv < 2 && (s_tile != ws.t0 || ptx::mbar_try_wait(&mi.q_full, s_item & 1)) &&
                         ptx::mbar_try_wait(&mi.full[s_stage], s_round & 1)) {
                         ptx::tc_fence_after();
-                        const uint32_t ka = base + s_stage * L.stage_bytes;
-                        for (int c = 0; c < L.chunks; ++c)
+                        uint64_t qd = q_desc, kd = tc::moved(k_desc, s_stage * L.stage_bytes);
+                        const uint32_t to = tmem + Tm<RB>::kS + (n_s & 1) * 64;
+                        ptx::mma_ss(to, qd, kd, kIdS, 0);
+#pragma unroll
+                        for (int k = 1; k < 4; ++k) ptx::mma_ss(to, tc::moved(qd, 32 * k), tc::moved(kd, 32 * k), kIdS, 1);
+                        for (int c = 1; c < L.chunks; ++c) {
+                            qd = tc::moved(qd, RB * 128);
+                            kd = tc::moved(kd, 8192);
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
-                                ptx::mma_ss(tmem + Tm<RB>::kS + (n_s & 1) * 64, ptx::sdesc_sw128(qa + c * RB * 128 + 32 * k),
-                                            ptx::sdesc_sw128(ka + c * 8192 + 32 * k), kIdS, c + k > 0);
+                                ptx::mma_ss(to, tc::moved(qd, 32 * k), tc::moved(kd, 32 * k), kIdS, 1);
+                        }
                         ptx::mma_commit(&mi.s_full[n_s & 1]);
                         ++n_s;
                         if (++s_stage == L.stages) s_stage = 0, ++s_round;
@@ -201,12 +208,14 @@ decode_tc_kernel(const __grid_constant__ Maps maps, const MlaDecodeArgs a, const
                     }
                     if (n_s > n_pv && ptx::mbar_try_wait(&mi.p_full, n_pv & 1)) {
                         ptx::tc_fence_after();
-                        const uint32_t va = base + p_stage * L.stage_bytes;
-                        for (int i = 0; i < blocks; ++i)
+                        uint64_t vd = tc::moved(v_desc, p_stage * L.stage_bytes);
+                        const uint32_t more_o = p_tile > wp.t0;
+                        for (int i = 0; i < blocks; ++i, vd = tc::moved(vd, 16384)) {
+                            ptx::mma_ss(tmem + i * RB, vd, p_desc, kIdO, more_o);
 #pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                ptx::mma_ss(tmem + i * RB, ptx::sdesc_sw128_mn(va + i * 16384 + 2048 * k, 8192, 1024),
-                                            ptx::sdesc_sw128(pa + 32 * k), kIdO, p_tile > wp.t0 || k > 0);
+                            for (int k = 1; k < 4; ++k)
+                                ptx::mma_ss(tmem + i * RB, tc::moved(vd, 2048 * k), tc::moved(p_desc, 32 * k), kIdO, 1);
+                        }
                         ptx::mma_commit(&mi.empty[p_stage]);
                         ptx::mma_commit(&mi.pv_done);
                         ++n_pv;

@@ -132,17 +132,18 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
         // -------------------------------------------------------------------- products
         if (lane == 0 && blocks > 0) {
             constexpr uint32_t kIdS = tc::idesc(128, 128, false, false), kIdO = tc::idesc(128, 128, false, true);
+            const uint64_t k_desc = ptx::sdesc_sw128(base), v_desc = ptx::sdesc_sw128_mn(base + kOffRing, 8192, 1024);
             auto qk = [&](int t, int j) {
-                const uint32_t qa = base + 3 * t * kSlotBytes;
-                for (int c = 0; c < kc; ++c) {
+                uint64_t qd = tc::moved(k_desc, 3 * t * kSlotBytes);
+                for (int c = 0; c < kc; ++c, qd = tc::moved(qd, kSlotBytes)) {
                     const int idx = j * per + c, slot = idx % kSlots;
                     if (!tc::wait(&mi.full[slot], (idx / kSlots) & 1, dead)) return false;
                     ptx::tc_fence_after();
-                    const uint32_t ka = base + kOffRing + slot * kSlotBytes;
+                    const uint64_t kd = tc::moved(k_desc, kOffRing + slot * kSlotBytes);
+                    ptx::mma_ss(tmem + t * 128, qd, kd, kIdS, c > 0);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        ptx::mma_ss(tmem + t * 128, ptx::sdesc_sw128(qa + c * kSlotBytes + 32 * k),
-                                    ptx::sdesc_sw128(ka + 32 * k), kIdS, c + k > 0);
+                    for (int k = 1; k < 4; ++k)
+                        ptx::mma_ss(tmem + t * 128, tc::moved(qd, 32 * k), tc::moved(kd, 32 * k), kIdS, 1);
                 }
                 ptx::mma_commit(&mi.s_full[t]);
                 return true;
@@ -153,11 +154,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
                     const int idx = j * per + kc + c, slot = idx % kSlots;
                     if (!tc::wait(&mi.full[slot], (idx / kSlots) & 1, dead)) return false;
                     ptx::tc_fence_after();
-                    const uint32_t va = base + kOffRing + slot * kSlotBytes;
+                    const uint64_t vd = tc::moved(v_desc, slot * kSlotBytes);
+                    const uint32_t pt = tmem + t * 128 + c * 32;
+                    ptx::mma_ts(tmem + kTmO + t * 128, pt, vd, kIdO, j + c > 0);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        ptx::mma_ts(tmem + kTmO + t * 128, tmem + t * 128 + (4 * c + k) * 8,
-                                    ptx::sdesc_sw128_mn(va + 2048 * k, 8192, 1024), kIdO, j > 0 || c + k > 0);
+                    for (int k = 1; k < 4; ++k)
+                        ptx::mma_ts(tmem + kTmO + t * 128, pt + 8 * k, tc::moved(vd, 2048 * k), kIdO, 1);
                 }
                 ptx::mma_commit(&mi.pv_done[t]);
                 return true;

@@ -61,6 +61,10 @@ __device__ __forceinline__ void tma_load_3d(uint32_t smem_dst, const void *tmap,
         "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(c2), "r"(ptx::smem_u32(bar))
         : "memory");
 }
+// A descriptor moved by `bytes` (the address field is the low one and does not overflow within
+// shared memory): products are issued by one thread, and building a descriptor for each
+// costs more of its time than the product takes.
+__device__ __forceinline__ constexpr uint64_t moved(uint64_t desc, uint32_t bytes) { return desc + (bytes >> 4); }
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
