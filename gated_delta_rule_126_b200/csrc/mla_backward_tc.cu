@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(kThreads, 1) dkv_tc_kernel(const __grid_consta
             }
         }
     } else if (warp == 8) {
-        if (lane == 0 && n > 0) {
+        if (tc::elect() && n > 0) {
             constexpr uint32_t kIdS = tc::idesc(128, kQt, false, false), kIdV = tc::idesc(128, 128, false, true);
             const uint32_t id_k = kc == 3 ? tc::idesc(128, 192, false, true) : kIdV;
             const uint64_t desc = ptx::sdesc_sw128(base), desc_mn = ptx::sdesc_sw128_mn(base, kQChunk, 1024);
@@ -390,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constan
         }
         __syncwarp();
     } else if (warp == 8) {
-        if (lane == 0 && n > 0) {
+        if (tc::elect() && n > 0) {
             constexpr uint32_t kIdS = tc::idesc(128, 128, false, false);
             const uint32_t id_q = tc::idesc(128, 64 * kc, false, true);
             const uint64_t desc = ptx::sdesc_sw128(base), desc_mn = ptx::sdesc_sw128_mn(base, kChunk, 1024);

@@ -168,7 +168,7 @@ decode_tc_kernel(const __grid_constant__ Maps maps, const MlaDecodeArgs a, const
             constexpr uint32_t kIdS = tc::idesc(64, kKeys, false, false), kIdO = tc::idesc(128, RB, true, false);
             const uint64_t q_desc = ptx::sdesc_sw128(base + L.q), p_desc = ptx::sdesc_sw128(base + L.p),
                            k_desc = ptx::sdesc_sw128(base), v_desc = ptx::sdesc_sw128_mn(base, 8192, 1024);
-            if (lane == 0) {
+            if (tc::elect()) {
                 // Scores run up to two tiles ahead of O's products (two S buffers), as tiles arrive;
                 // whichever of the two can go next goes, so neither waits for the other's input.
                 MlaWalk ws(run), wp(run);

@@ -130,7 +130,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
         }
       } else if (warp == 8) {
         // -------------------------------------------------------------------- products
-        if (lane == 0 && blocks > 0) {
+        if (tc::elect() && blocks > 0) {
             constexpr uint32_t kIdS = tc::idesc(128, 128, false, false), kIdO = tc::idesc(128, 128, false, true);
             const uint64_t k_desc = ptx::sdesc_sw128(base), v_desc = ptx::sdesc_sw128_mn(base + kOffRing, 8192, 1024);
             auto qk = [&](int t, int j) {

@@ -61,6 +61,13 @@ __device__ __forceinline__ void tma_load_3d(uint32_t smem_dst, const void *tmap,
         "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(c2), "r"(ptx::smem_u32(bar))
         : "memory");
 }
+// True in one lane of a converged warp.  Products issued behind this test cost their issuer about a third less
+// time than behind `lane == 0` (33 against 46 cycles each, measured with 64 x 64 x 16 products).
+__device__ __forceinline__ bool elect() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
 // A descriptor moved by `bytes` (the address field is the low one and does not overflow within
 // shared memory): products are issued by one thread, and building a descriptor for each
 // costs more of its time than the product takes.
