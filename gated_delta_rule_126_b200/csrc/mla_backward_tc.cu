@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(kThreads, 1) dkv_tc_kernel(const __grid_consta
 
     if (warp == 9) {
         if (n > 0) {
-            if (lane == 0) {
+            if (tc::elect()) {
                 ptx::mbar_arrive_expect_tx(&mi.k_full, kc * kChunk);
                 for (int c = 0; c < 2; ++c) tc::tma_load_3d(base + c * kChunk, &maps.k, &mi.k_full, 64 * c, h, pl.k0 + j0);
                 if (a.dr) tc::tma_load_2d(base + 2 * kChunk, &maps.kr, &mi.k_full, 0, pl.k0 + j0);
@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(kThreads, 1) dkv_tc_kernel(const __grid_consta
                     mi.delta[s][e] = in ? a.delta[at] : 0.f;
                 }
                 __syncwarp();
-                if (lane == 0) {
+                if (tc::elect()) {
                     const uint32_t dst = base + kOffStages + s * kStage;
                     ptx::mbar_arrive_expect_tx(&mi.full[s], (kc + 2) * kQChunk);
                     for (int c = 0; c < kc; ++c)
@@ -355,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constan
     const int n = (key_end(min(i0 + 128, pl.lq) - 1) + 127) / 128;
 
     if (warp == 9) {
-        if (lane == 0 && n > 0) {
+        if (tc::elect() && n > 0) {
             auto load_k = [&](int j) {
                 if (j >= 2 && !tc::wait(&mi.k_empty[j & 1], (j / 2 - 1) & 1, dead)) return false;
                 const uint32_t dst = base + kOffK + (j & 1) * 3 * kChunk;

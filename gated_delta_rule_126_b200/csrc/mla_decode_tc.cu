@@ -6,12 +6,17 @@
 //   O^T [d_latent x RB] += K[:, :d_latent]^T P^T   (the tile again, MN-major; P K-major)
 // The output is kept transposed because RB rows of 512 float32 channels would fill all of TMEM
 // as [RB x 512] with M = 128, while as d_latent / 128 blocks of [128 x RB] they take 4 RB columns.
-// Bound by memory: a tile is 73,728 bytes and an SM's share of the bandwidth brings it in about
-// 3,000 cycles; two tiles are in flight.
+// Bound by memory: a tile is 73,728 bytes, and an SM's share of the bandwidth brings it in in about
+// 3,000 cycles, while its products take 1,900 (both read shared memory 128 bytes a cycle: 33 cycles for a
+// 64 x 64 x 16 product, 41 or 49 for one of 128 x RB x 16) and its softmax 1,100.  So loads have to be under way all
+// the time: the tile passes through a ring of 16 KB slots (128 channels of its 64 rows), S takes each as it arrives and
+// O^T's product frees each as it ends; 10 slots (2.5 tiles) with RB = 32, 8 with RB = 64.
 //
-// Warps 0-3: softmax (row i of S lies in lane i % 16 of warp i / 16, the M = 64 layout), rescaling
-// and output; warp 4: matrix instructions; warp 5: TMA loads through the page table.  S is double buffered, so the next tile's
-// scores are formed while this one's softmax runs.
+// Warps 0-3: softmax, rescaling and output (row i of S lies in lane i % 16 of warp i / 16, the M = 64 layout);
+// warp 4: matrix instructions; warps 5-7: TMA loads through the page table.  S is double buffered, so the
+// next tile's scores are formed while this one's softmax runs.  One thread takes about 650 cycles from one slot's
+// loads to the next (wait, expected bytes, two boxes), which for the five pieces of a tile is more than memory
+// takes for it: warps 5 and 6 fill the ring's slots in turn, warp 7 the shared part and Q.
 #include <cmath>
 
 #include "mla_decode_plan.cuh"
@@ -20,9 +25,11 @@
 namespace kda {
 namespace {
 
-constexpr int kThreads = 192;
+constexpr int kThreads = 256;
 constexpr int kKeys = 64;
-constexpr int kMaxStages = 8;
+constexpr int kMaxSlots = 12, kMaxRope = 4;
+constexpr int kMasks = 16;  // tiles whose key mask is kept: more than are ever in flight
+constexpr uint32_t kSlotBytes = 16384, kRopeBytes = 8192;
 constexpr uint32_t kTmemColumns = 512;
 constexpr float kLog2e = 1.4426950408889634f;
 // The running maximum that scales P and O is raised only when the true one has outgrown it by
@@ -30,32 +37,48 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLazy = 8.f;
 
 struct Misc {
-    uint64_t full[kMaxStages], empty[kMaxStages], s_full[2], p_full, pv_done, q_full, q_empty, drain;
-    uint64_t mask[kMaxStages];  // which keys of the stage lie on a page of the pool
+    uint64_t full[kMaxSlots], empty[kMaxSlots], rope_full[kMaxRope], rope_empty[kMaxRope];
+    uint64_t s_full[2], p_full, pv_done, q_full, q_empty, drain;
+    uint64_t mask[kMasks];  // which keys of a tile lie on a page of the pool
     float factor[64];
     uint32_t tmem, dead;
 };
 constexpr size_t kMiscBytes = 1024;
 static_assert(sizeof(Misc) <= kMiscBytes, "misc");
+static_assert(kMasks > kMaxSlots, "a tile holds at least one slot");
 
 struct Layout {
-    int chunks, stages;  // 64-channel chunks of a row; tiles in flight
-    uint32_t stage_bytes, q, p, misc, total;
+    int chunks;       // 64-channel chunks of a row
+    int slots, rope;  // ring slots; slots of the shared part (0 without one)
+    uint32_t rope_at, q, p, misc, total;
 };
-__host__ __device__ inline Layout layout(int W, int rb) {
+__host__ __device__ inline Layout layout(int dc, int dr, int rb) {
     Layout L;
-    L.chunks = W / 64;
-    L.stage_bytes = uint32_t(L.chunks) * 8192u;
-    const uint32_t fixed = uint32_t(L.chunks) * rb * 128u + 8192u + uint32_t(kMiscBytes);  // Q, P (read to 64 rows), misc
-    const uint32_t room = 232448u - 1024u - fixed;
-    L.stages = int(room / L.stage_bytes);
-    if (L.stages > kMaxStages) L.stages = kMaxStages;
-    L.q = L.stages * L.stage_bytes;
+    L.chunks = (dc + dr) / 64;
+    // Q, P, misc; with rb = 32 the 64-row reads of Q's last chunk end inside P
+    const uint32_t fixed = uint32_t(L.chunks) * rb * 128u + rb * 128u + uint32_t(kMiscBytes);
+    const int tile = dc / 128;
+    uint32_t room = 232448u - 1024u - fixed;
+    L.rope = dr == 0 ? 0 : tile == 4 ? (rb == 32 ? 3 : 2) : kMaxRope;  // as many tiles as the ring holds, at least in part
+    room -= L.rope * kRopeBytes;
+    L.slots = int(room / kSlotBytes);
+    L.slots = (L.slots > kMaxSlots ? kMaxSlots : L.slots) & ~1;  // even: a slot is always filled by the same warp
+    L.rope_at = L.slots * kSlotBytes;
+    L.q = L.rope_at + L.rope * kRopeBytes;
     L.p = L.q + uint32_t(L.chunks) * rb * 128u;
-    L.misc = L.p + 8192u;
+    L.misc = L.p + rb * 128u;
     L.total = L.misc + uint32_t(kMiscBytes) + 1024u;
     return L;
 }
+
+// A place in a ring of n slots and the parity of its current round.
+struct Ring {
+    int slot = 0;
+    uint32_t round = 0;
+    __device__ void next(int n) {
+        if (++slot == n) slot = 0, ++round;
+    }
+};
 
 struct Maps {
     CUtensorMap cache, q;
@@ -73,14 +96,15 @@ decode_tc_kernel(const __grid_constant__ Maps maps, const MlaDecodeArgs a, const
     __shared__ int64_t buf[kThreads / 32 + 4];
     const uint32_t base = (ptx::smem_u32(raw) + 1023u) & ~1023u;
     uint8_t *sm = raw + (base - ptx::smem_u32(raw));
-    const int W = a.dc + a.dr, R = a.n * a.H, blocks = a.dc / 128;
-    const Layout L = layout(W, RB);
+    const int R = a.n * a.H, blocks = a.dc / 128;
+    const Layout L = layout(a.dc, a.dr, RB);
     Misc &mi = *reinterpret_cast<Misc *>(sm + L.misc);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int group = blockIdx.x / shape.row_tiles, rt = blockIdx.x % shape.row_tiles, r0 = rt * RB, rows = min(RB, R - r0);
 
     if (tid == 0) {
-        for (int i = 0; i < L.stages; ++i) ptx::mbar_init(&mi.full[i], 1), ptx::mbar_init(&mi.empty[i], 1);
+        for (int i = 0; i < kMaxSlots; ++i) ptx::mbar_init(&mi.full[i], 1), ptx::mbar_init(&mi.empty[i], 1);
+        for (int i = 0; i < kMaxRope; ++i) ptx::mbar_init(&mi.rope_full[i], 1), ptx::mbar_init(&mi.rope_empty[i], 1);
         ptx::mbar_init(&mi.s_full[0], 1);
         ptx::mbar_init(&mi.s_full[1], 1);
         ptx::mbar_init(&mi.p_full, 128);
@@ -106,98 +130,132 @@ decode_tc_kernel(const __grid_constant__ Maps maps, const MlaDecodeArgs a, const
     volatile uint32_t *dead = &mi.dead;
 
     if (group < run.groups) {
-        if (warp == 5) {
+        if (warp >= 5) {
             // ---------------------------------------------------------------- loads
-            const int boxes = kKeys / box;  // of one tile, each inside a page
-            const int rows_total = a.num_pages * a.page_size;
-            const uint64_t bits = box == 64 ? ~0ull : (1ull << box) - 1;
-            int stage = 0, issued = 0;
-            uint32_t round = 0, items = 0;
-            bool ok = true;
-            MlaWalk w(run);
-            while (ok && w.next(a, kKeys, run)) {
-                // the row of this lane's box of tile t, or one behind the pool (read as zeros)
-                auto lookup = [&](int t) {
-                    int row = rows_total;
-                    const int key = t * kKeys + lane * box;
-                    if (lane < boxes && t < w.t1 && key < w.len) {
-                        const int page = a.page_table[int64_t(w.b) * a.max_pages + key / a.page_size];
-                        if (page >= 0 && page < a.num_pages) row = page * a.page_size + key % a.page_size;
+            if (tc::elect()) {
+                const int role = warp - 5;        // 0, 1: even and odd pieces of 128 channels; 2: shared part and Q
+                const int boxes = kKeys / box;    // of one tile, each inside a page
+                const int rows_total = a.num_pages * a.page_size;
+                const uint64_t bits = box == 64 ? ~0ull : (1ull << box) - 1;
+                Ring ring, rope;
+                uint32_t tile = 0, items = 0;
+                bool ok = true;
+                MlaWalk w(run);
+                while (ok && w.next(a, kKeys, run)) {
+                    const int32_t *table = a.page_table + int64_t(w.b) * a.max_pages;
+                    int entry = w.t0 * kKeys / a.page_size, off = w.t0 * kKeys - entry * a.page_size;
+                    int page[kKeys / 8], at[kKeys / 8];  // of the coming tile's boxes: page number, row in it
+                    auto look = [&](int t) {             // loaded a tile ahead, used when the tile's turn comes
+#pragma unroll
+                        for (int x = 0; x < kKeys / 8; ++x)
+                            if (x < boxes) {
+                                page[x] = t < w.t1 && t * kKeys + x * box < w.len ? table[entry] : -1;
+                                at[x] = off;
+                                if ((off += box) == a.page_size) off = 0, ++entry;
+                            }
+                    };
+                    look(w.t0);
+                    if (role == 2) {
+                        if (items) ok = tc::wait(&mi.q_empty, (items - 1) & 1, dead);
+                        if (!ok) break;
+                        ptx::mbar_arrive_expect_tx(&mi.q_full, uint32_t(L.chunks) * RB * 128u);
+                        for (int c = 0; c < L.chunks; ++c)
+                            tc::tma_load_2d(base + L.q + c * RB * 128, &maps.q, &mi.q_full, 64 * c, w.b * R + r0);
+                        ++items;
+                        if (L.rope == 0) continue;
                     }
-                    return row;
-                };
-                int row = lookup(w.t0);
-                if (items) ok = tc::wait(&mi.q_empty, (items - 1) & 1, dead);
-                if (!ok) break;
-                if (lane == 0) {
-                    ptx::mbar_arrive_expect_tx(&mi.q_full, uint32_t(L.chunks) * RB * 128u);
-                    for (int c = 0; c < L.chunks; ++c)
-                        tc::tma_load_2d(base + L.q + c * RB * 128, &maps.q, &mi.q_full, 64 * c, w.b * R + r0);
-                }
-                ++items;
-                for (int t = w.t0; t < w.t1; ++t) {
-                    const int next = lookup(t + 1);
-                    if (round && !(ok = tc::wait(&mi.empty[stage], (round - 1) & 1, dead))) break;
-                    const uint32_t good = __ballot_sync(0xffffffffu, row != rows_total);
-                    if (lane == 0) {
+                    for (int t = w.t0; ok && t < w.t1; ++t, ++tile) {
+                        int row[kKeys / 8];  // in the pool, or behind it (read as zeros)
                         uint64_t m = 0;
-                        for (int i = 0; i < boxes; ++i)
-                            if (good >> i & 1) m |= bits << (i * box);
-                        mi.mask[stage] = m;
-                        ptx::mbar_arrive_expect_tx(&mi.full[stage], L.stage_bytes);
+#pragma unroll
+                        for (int x = 0; x < kKeys / 8; ++x)
+                            if (x < boxes) {
+                                const bool good = page[x] >= 0 && page[x] < a.num_pages;
+                                row[x] = good ? page[x] * a.page_size + at[x] : rows_total;
+                                if (good) m |= bits << (x * box);
+                            }
+                        look(t + 1);
+                        auto load = [&](uint32_t dst, uint64_t *bar, int c) {  // 64 keys x 64 channels from c on
+                            tc::tma_load_2d(dst, &maps.cache, bar, c, row[0]);
+                            if (boxes == 1) return;
+#pragma unroll
+                            for (int x = 1; x < kKeys / 8; ++x)
+                                if (x < boxes) tc::tma_load_2d(dst + x * box * 128, &maps.cache, bar, c, row[x]);
+                        };
+                        if (role == 2) {
+                            if (rope.round && !(ok = tc::wait(&mi.rope_empty[rope.slot], (rope.round - 1) & 1, dead))) break;
+                            ptx::mbar_arrive_expect_tx(&mi.rope_full[rope.slot], kRopeBytes);
+                            load(base + L.rope_at + rope.slot * kRopeBytes, &mi.rope_full[rope.slot], a.dc);
+                            rope.next(L.rope);
+                            continue;
+                        }
+                        for (int i = 0; i < blocks; ++i, ring.next(L.slots)) {
+                            if ((ring.slot & 1) != role) continue;
+                            if (ring.round && !(ok = tc::wait(&mi.empty[ring.slot], (ring.round - 1) & 1, dead))) break;
+                            if (i == 0) mi.mask[tile % kMasks] = m;
+                            ptx::mbar_arrive_expect_tx(&mi.full[ring.slot], kSlotBytes);
+                            load(base + ring.slot * kSlotBytes, &mi.full[ring.slot], 128 * i);
+                            load(base + ring.slot * kSlotBytes + 8192, &mi.full[ring.slot], 128 * i + 64);
+                        }
                     }
-                    __syncwarp();
-                    for (int i = lane; i < ((boxes * L.chunks + 31) & ~31); i += 32) {
-                        const int at = __shfl_sync(0xffffffffu, row, i % boxes);
-                        if (i < boxes * L.chunks)
-                            tc::tma_load_2d(base + stage * L.stage_bytes + (i / boxes) * 8192 + (i % boxes) * box * 128,
-                                            &maps.cache, &mi.full[stage], 64 * (i / boxes), at);
-                    }
-                    row = next;
-                    ++issued;
-                    if (++stage == L.stages) stage = 0, ++round;
+                }
+                if (!ok) {  // an error: the copies in flight land before the block ends
+                    auto drain = [&](const Ring &r, int n, uint64_t *bars, int first, int step) {
+                        for (int i = first; i < n; i += step) {
+                            const uint32_t uses = r.round + (i < r.slot ? 1 : 0);  // of slot i so far
+                            if (uses) ptx::mbar_wait_bounded(&bars[i], (uses - 1) & 1, tc::kWaitCycles);
+                        }
+                    };
+                    if (role < 2) drain(ring, L.slots, mi.full, role, 2);
+                    else drain(rope, L.rope, mi.rope_full, 0, 1);
+                    if (items) ptx::mbar_wait_bounded(&mi.q_full, (items - 1) & 1, tc::kWaitCycles);
                 }
             }
-            if (!ok && lane == 0) {  // an error: the copies in flight land before the block ends
-                for (int i = max(0, issued - L.stages); i < issued; ++i)
-                    ptx::mbar_wait_bounded(&mi.full[i % L.stages], (i / L.stages) & 1, tc::kWaitCycles);
-                if (items) ptx::mbar_wait_bounded(&mi.q_full, (items - 1) & 1, tc::kWaitCycles);
-            }
+            __syncwarp();
         } else if (warp == 4) {
             // ---------------------------------------------------------------- products
             constexpr uint32_t kIdS = tc::idesc(64, kKeys, false, false), kIdO = tc::idesc(128, RB, true, false);
             const uint64_t q_desc = ptx::sdesc_sw128(base + L.q), p_desc = ptx::sdesc_sw128(base + L.p),
                            k_desc = ptx::sdesc_sw128(base), v_desc = ptx::sdesc_sw128_mn(base, 8192, 1024);
             if (tc::elect()) {
-                // Scores run up to two tiles ahead of O's products (two S buffers), as tiles arrive;
-                // whichever of the two can go next goes, so neither waits for the other's input.
+                // Scores run up to two tiles ahead of O's products (two S buffers).  Whichever of the two has its
+                // input goes; a tile's scores, once begun, take its slots as they arrive.
                 MlaWalk ws(run), wp(run);
                 bool more = ws.next(a, kKeys, run), ok = true;
                 wp.next(a, kKeys, run);
-                int s_tile = ws.t0, p_tile = wp.t0, s_stage = 0, p_stage = 0;
-                uint32_t s_round = 0, s_item = 0, n_s = 0, n_pv = 0;
+                Ring s_ring, s_rope, p_ring;
+                int s_tile = ws.t0, p_tile = wp.t0;
+                uint32_t s_item = 0, n_s = 0, n_pv = 0;
                 const uint32_t n_all = uint32_t(run.end - run.start);
                 long long since = clock64();
                 while (n_pv < n_all) {
                     bool idle = true;
-                    if (more && n_s - n_pv < 2 && (s_tile != ws.t0 || ptx::mbar_try_wait(&mi.q_full, s_item & 1)) &&
-                        ptx::mbar_try_wait(&mi.full[s_stage], s_round & 1)) {
-                        ptx::tc_fence_after();
-                        uint64_t qd = q_desc, kd = tc::moved(k_desc, s_stage * L.stage_bytes);
+                    if (more && n_s - n_pv < 2 && (s_tile != ws.t0 || tc::ready(&mi.q_full, s_item & 1)) &&
+                        tc::ready(&mi.full[s_ring.slot], s_ring.round & 1)) {
                         const uint32_t to = tmem + Tm<RB>::kS + (n_s & 1) * 64;
-                        ptx::mma_ss(to, qd, kd, kIdS, 0);
+                        uint64_t qd = q_desc;
+                        for (int i = 0; i < blocks; ++i, s_ring.next(L.slots), qd = tc::moved(qd, RB * 256)) {
+                            if (!(ok = tc::wait(&mi.full[s_ring.slot], s_ring.round & 1, dead))) break;
+                            ptx::tc_fence_after();
+                            const uint64_t kd = tc::moved(k_desc, s_ring.slot * kSlotBytes);
+                            ptx::mma_ss(to, qd, kd, kIdS, i > 0);
 #pragma unroll
-                        for (int k = 1; k < 4; ++k) ptx::mma_ss(to, tc::moved(qd, 32 * k), tc::moved(kd, 32 * k), kIdS, 1);
-                        for (int c = 1; c < L.chunks; ++c) {
-                            qd = tc::moved(qd, RB * 128);
-                            kd = tc::moved(kd, 8192);
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                ptx::mma_ss(to, tc::moved(qd, 32 * k), tc::moved(kd, 32 * k), kIdS, 1);
+                            for (int k = 1; k < 8; ++k)
+                                ptx::mma_ss(to, tc::moved(qd, (k >> 2) * (RB * 128) + 32 * (k & 3)),
+                                            tc::moved(kd, (k >> 2) * 8192 + 32 * (k & 3)), kIdS, 1);
                         }
+                        if (ok && L.rope) {
+                            ok = tc::wait(&mi.rope_full[s_rope.slot], s_rope.round & 1, dead);
+                            ptx::tc_fence_after();
+                            const uint64_t kd = tc::moved(k_desc, L.rope_at + s_rope.slot * kRopeBytes);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) ptx::mma_ss(to, tc::moved(qd, 32 * k), tc::moved(kd, 32 * k), kIdS, 1);
+                            ptx::mma_commit(&mi.rope_empty[s_rope.slot]);
+                            s_rope.next(L.rope);
+                        }
+                        if (!ok) break;
                         ptx::mma_commit(&mi.s_full[n_s & 1]);
                         ++n_s;
-                        if (++s_stage == L.stages) s_stage = 0, ++s_round;
                         if (++s_tile == ws.t1) {
                             ptx::mma_commit(&mi.q_empty);
                             more = ws.next(a, kKeys, run);
@@ -206,20 +264,19 @@ decode_tc_kernel(const __grid_constant__ Maps maps, const MlaDecodeArgs a, const
                         }
                         idle = false;
                     }
-                    if (n_s > n_pv && ptx::mbar_try_wait(&mi.p_full, n_pv & 1)) {
+                    if (n_s > n_pv && tc::ready(&mi.p_full, n_pv & 1)) {
                         ptx::tc_fence_after();
-                        uint64_t vd = tc::moved(v_desc, p_stage * L.stage_bytes);
                         const uint32_t more_o = p_tile > wp.t0;
-                        for (int i = 0; i < blocks; ++i, vd = tc::moved(vd, 16384)) {
+                        for (int i = 0; i < blocks; ++i, p_ring.next(L.slots)) {
+                            const uint64_t vd = tc::moved(v_desc, p_ring.slot * kSlotBytes);
                             ptx::mma_ss(tmem + i * RB, vd, p_desc, kIdO, more_o);
 #pragma unroll
                             for (int k = 1; k < 4; ++k)
                                 ptx::mma_ss(tmem + i * RB, tc::moved(vd, 2048 * k), tc::moved(p_desc, 32 * k), kIdO, 1);
+                            ptx::mma_commit(&mi.empty[p_ring.slot]);
                         }
-                        ptx::mma_commit(&mi.empty[p_stage]);
                         ptx::mma_commit(&mi.pv_done);
                         ++n_pv;
-                        if (++p_stage == L.stages) p_stage = 0;
                         if (++p_tile == wp.t1) {
                             wp.next(a, kKeys, run);
                             p_tile = wp.t0;
@@ -244,77 +301,84 @@ decode_tc_kernel(const __grid_constant__ Maps maps, const MlaDecodeArgs a, const
         } else {
             // ---------------------------------------------------------------- softmax, rescaling, output
             const uint32_t lanes = uint32_t(warp) << 21;  // TMEM lane 32 warp
-            const int row = warp * 16 + lane;             // query row of this thread when lane < 16
-            const bool mine = lane < 16 && row < rows;
-            const int hidden = mine ? a.n - 1 - (r0 + row) / a.H : 0;  // last keys that this row's token does not see
+            // this thread's rows, each shared with the three other threads of its group of four
+            const int r1 = warp * 16 + (lane >> 2), r2 = r1 + 8, pair = 2 * (lane & 3);
+            const int hidden1 = a.n - 1 - (r0 + r1) / a.H, hidden2 = a.n - 1 - (r0 + r2) / a.H;  // last keys that a row does not see
             const float sl2 = a.scale * kLog2e;
             float *slots = reinterpret_cast<float *>(static_cast<char *>(a.workspace) + mla_meta_bytes(gridDim.x));
-            int stage = 0;
-            uint32_t round = 0, n_s = 0, n_pv = 0;
+            Ring ring;
+            uint32_t tile = 0;
             bool ok = true;
             MlaWalk w(run);
             while (ok && w.next(a, kKeys, run)) {
-                float top = -INFINITY, sum = 0.f;  // the scale's maximum (raw scores) and the row's sum
+                float top[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};  // the scale's maximum (raw scores); this thread's share
                 for (int t = w.t0; t < w.t1; ++t) {
                     // a wait that fails is voted on below: no warp leaves the others at a barrier
-                    ok = tc::wait(&mi.s_full[n_s & 1], (n_s >> 1) & 1, dead) && ok;
-                    ok = tc::wait(&mi.full[stage], round & 1, dead) && ok;  // complete: orders mask and rows
+                    ok = tc::wait(&mi.s_full[tile & 1], (tile >> 1) & 1, dead) && ok;
+                    ok = tc::wait(&mi.full[ring.slot], ring.round & 1, dead) && ok;  // complete: orders the mask
                     ptx::tc_fence_after();
-                    uint32_t s0[32], s1[32];
-                    const uint32_t sa = tmem + lanes + Tm<RB>::kS + (n_s & 1) * 64;
-                    ptx::tmem_ld32(sa, s0);
-                    ptx::tmem_ld32(sa + 32, s1);
-                    const int left = w.len - t * kKeys, seen = mine ? left - hidden : 0;
-                    uint64_t mask = mi.mask[stage];
-                    mask &= seen >= 64 ? ~0ull : seen <= 0 ? 0ull : (1ull << seen) - 1;
-                    if (left < kKeys) {
+                    uint32_t s[32];
+                    tc::tmem_ld_16x64(tmem + lanes + Tm<RB>::kS + (tile & 1) * 64, s);
+                    const int left = w.len - t * kKeys;
+                    const uint64_t mask = mi.mask[tile % kMasks];
+                    auto seen = [&](int r, int hidden) {
+                        const int n = r < rows ? left - hidden : 0;
+                        return mask & (n >= 64 ? ~0ull : n <= 0 ? 0ull : (1ull << n) - 1);
+                    };
+                    const uint64_t see1 = seen(r1, hidden1), see2 = seen(r2, hidden2);
+                    Ring z = ring;
+                    for (int i = 0; i < blocks; ++i, z.next(L.slots)) {
+                        if (left >= kKeys) continue;
                         // rows behind the sequence may hold anything: as values they have to be zero
-                        const int rows0 = max(left, 0), per = (kKeys - rows0) * 8;
-                        for (int i = tid; i < per * (a.dc / 64); i += 128) {
-                            const int c = i / per, at = rows0 * 8 + i % per;
-                            tc::st_shared_v4(base + stage * L.stage_bytes + c * 8192 + at * 16, 0, 0, 0, 0);
-                        }
+                        ok = tc::wait(&mi.full[z.slot], z.round & 1, dead) && ok;
+                        const int from = left * 8, per = kKeys * 8 - from;
+                        for (int x = tid; x < 2 * per; x += 128)
+                            tc::st_shared_v4(base + z.slot * kSlotBytes + (x / per) * 8192 + (from + x % per) * 16, 0, 0, 0, 0);
                     }
+                    ring = z;
                     ptx::tmem_wait_ld();
-                    if (mask != ~0ull) {
+                    if ((see1 & see2) != ~0ull) {
+                        const uint64_t m1 = see1 >> pair, m2 = see2 >> pair;
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            if (!(mask >> i & 1)) s0[i] = 0xff800000u;
-                            if (!(mask >> (i + 32) & 1)) s1[i] = 0xff800000u;
+                        for (int i = 0; i < 8; ++i) {
+                            if (!(m1 >> (8 * i) & 1)) s[4 * i] = 0xff800000u;
+                            if (!(m1 >> (8 * i + 1) & 1)) s[4 * i + 1] = 0xff800000u;
+                            if (!(m2 >> (8 * i) & 1)) s[4 * i + 2] = 0xff800000u;
+                            if (!(m2 >> (8 * i + 1) & 1)) s[4 * i + 3] = 0xff800000u;
                         }
                     }
-                    float m = -INFINITY;
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) m = fmaxf(m, fmaxf(__uint_as_float(s0[i]), __uint_as_float(s1[i])));
-                    m = fmaxf(m, top);
                     bool raise = false;
-                    float keep = 1.f;
-                    if (top == -INFINITY) {
-                        top = m;  // nothing summed yet
-                    } else if ((m - top) * sl2 > kLazy) {
-                        keep = ptx::ex2_approx((top - m) * sl2);
-                        sum *= keep;
-                        top = m;
-                        raise = true;
+                    float keep[2], off[2];
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        float m = top[r];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            m = fmaxf(m, fmaxf(__uint_as_float(s[4 * i + 2 * r]), __uint_as_float(s[4 * i + 2 * r + 1])));
+                        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+                        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+                        const bool fresh = top[r] == -INFINITY, up = !fresh && (m - top[r]) * sl2 > kLazy;
+                        keep[r] = up ? ptx::ex2_approx((top[r] - m) * sl2) : 1.f;
+                        sum[r] *= keep[r];
+                        top[r] = fresh || up ? m : top[r];
+                        raise = raise || up;
+                        off[r] = top[r] == -INFINITY ? 0.f : top[r] * sl2;
                     }
-                    const float off = top == -INFINITY ? 0.f : top * sl2;
-                    uint32_t p[32];
-                    float add = 0.f;
+                    uint32_t p[16];
+                    float add[4] = {};
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
-                        const float x = ptx::ex2_approx(fmaf(__uint_as_float(s0[2 * i]), sl2, -off));
-                        const float y = ptx::ex2_approx(fmaf(__uint_as_float(s0[2 * i + 1]), sl2, -off));
-                        const float z = ptx::ex2_approx(fmaf(__uint_as_float(s1[2 * i]), sl2, -off));
-                        const float u = ptx::ex2_approx(fmaf(__uint_as_float(s1[2 * i + 1]), sl2, -off));
+                        const float x = ptx::ex2_approx(fmaf(__uint_as_float(s[2 * i]), sl2, -off[i & 1]));
+                        const float y = ptx::ex2_approx(fmaf(__uint_as_float(s[2 * i + 1]), sl2, -off[i & 1]));
                         p[i] = tc::pack_bf16(x, y);
-                        p[i + 16] = tc::pack_bf16(z, u);
-                        add += (x + y) + (z + u);
+                        add[i & 3] += x + y;
                     }
-                    sum += add;
+                    sum[0] += add[0] + add[2];
+                    sum[1] += add[1] + add[3];
                     // the last product has read P and added to O
-                    if (n_pv) ok = tc::wait(&mi.pv_done, (n_pv - 1) & 1, dead) && ok;
+                    if (tile) ok = tc::wait(&mi.pv_done, (tile - 1) & 1, dead) && ok;
                     if (ptx::named_barrier_or(1, 128, raise || !ok)) {
-                        if (lane < 16) mi.factor[row] = keep;
+                        if (pair == 0) mi.factor[r1] = keep[0], mi.factor[r2] = keep[1];
                         if (ptx::named_barrier_or(1, 128, !ok)) {
                             ok = false;
                             break;
@@ -333,30 +397,36 @@ decode_tc_kernel(const __grid_constant__ Maps maps, const MlaDecodeArgs a, const
                             }
                         ptx::tmem_wait_st();
                     }
-                    if (lane < 16 && row < RB) {
+                    if (r1 < RB) {
+                        const uint32_t to = base + L.p + r1 * 128 + pair * 2;  // r2 is 8 rows on, its swizzle the same
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            tc::st_shared_v4(base + L.p + row * 128 + ((i ^ (row & 7)) << 4), p[4 * i], p[4 * i + 1],
-                                             p[4 * i + 2], p[4 * i + 3]);
+                        for (int i = 0; i < 8; ++i) {
+                            tc::st_shared_b32(to + ((i ^ (r1 & 7)) << 4), p[2 * i]);
+                            tc::st_shared_b32(to + 1024 + ((i ^ (r1 & 7)) << 4), p[2 * i + 1]);
+                        }
                     }
                     ptx::fence_proxy_async_smem();
                     ptx::tc_fence_before();
                     ptx::mbar_arrive(&mi.p_full);
-                    ++n_s;
-                    ++n_pv;
-                    if (++stage == L.stages) stage = 0, ++round;
+                    ++tile;
                 }
-                if (ok) ok = tc::wait(&mi.pv_done, (n_pv - 1) & 1, dead);
+                if (ok) ok = tc::wait(&mi.pv_done, (tile - 1) & 1, dead);
                 if (ptx::named_barrier_or(1, 128, !ok)) break;  // and factor is free
                 const bool whole = w.whole();
                 float *slot = slots + mla_slot(w) * mla_slot_floats(RB, a.dc);
-                if (lane < 16 && row < RB) {
-                    mi.factor[row] = !whole ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    float l = sum[r];
+                    l += __shfl_xor_sync(0xffffffffu, l, 1);
+                    l += __shfl_xor_sync(0xffffffffu, l, 2);
+                    const int row = r ? r2 : r1;
+                    if (pair != 0 || row >= RB) continue;
+                    mi.factor[row] = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
                     if (!whole) {
-                        slot[RB * a.dc + 2 * row] = top == -INFINITY ? top : top * a.scale;
-                        slot[RB * a.dc + 2 * row + 1] = sum;
-                    } else if (a.lse && mine) {
-                        a.lse[int64_t(w.b) * R + r0 + row] = sum == 0.f ? -INFINITY : top * a.scale + logf(sum);
+                        slot[RB * a.dc + 2 * row] = top[r] == -INFINITY ? top[r] : top[r] * a.scale;
+                        slot[RB * a.dc + 2 * row + 1] = l;
+                    } else if (a.lse && row < rows) {
+                        a.lse[int64_t(w.b) * R + r0 + row] = l == 0.f ? -INFINITY : top[r] * a.scale + logf(l);
                     }
                 }
                 if (tid == 0 && !whole && w.t0 == 0)
@@ -399,7 +469,7 @@ int box_rows(int page_size) {
 
 template <int RB>
 cudaError_t launch(const Maps &maps, const MlaDecodeArgs &a, const MlaDecodeShape &s, int box, cudaStream_t st) {
-    const Layout L = layout(a.dc + a.dr, RB);
+    const Layout L = layout(a.dc, a.dr, RB);
     const cudaError_t e = cudaFuncSetAttribute(decode_tc_kernel<RB>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(L.total));
     if (e != cudaSuccess) return e;
     decode_tc_kernel<RB><<<s.grid(), kThreads, L.total, st>>>(maps, a, s, box);

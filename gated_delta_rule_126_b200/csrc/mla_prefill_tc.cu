@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
         ptx::regs_dec<kRegsOther>();
       if (warp == 9) {
         // -------------------------------------------------------------------- loads
-        if (lane == 0 && blocks > 0) {
+        if (tc::elect() && blocks > 0) {
             auto load_q = [&](int t) {
                 if (n[t] == 0) return;
                 ptx::mbar_arrive_expect_tx(&mi.q_full[t], kc * kSlotBytes);
