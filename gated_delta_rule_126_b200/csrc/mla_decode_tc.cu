@@ -40,7 +40,7 @@ struct Misc {
     uint64_t full[kMaxSlots], empty[kMaxSlots], rope_full[kMaxRope], rope_empty[kMaxRope];
     uint64_t s_full[2], p_full, pv_done, q_full, q_empty, drain;
     uint64_t mask[kMasks];  // which keys of a tile lie on a page of the pool
-    float factor[64];
+    alignas(16) float factor[64];
     uint32_t tmem, dead;
 };
 constexpr size_t kMiscBytes = 1024;
@@ -154,7 +154,7 @@ decode_tc_kernel(const __grid_constant__ Maps maps, const MlaDecodeArgs a, const
                                 if ((off += box) == a.page_size) off = 0, ++entry;
                             }
                     };
-                    look(w.t0);
+                    if (role != 2 || L.rope) look(w.t0);
                     if (role == 2) {
                         if (items) ok = tc::wait(&mi.q_empty, (items - 1) & 1, dead);
                         if (!ok) break;
@@ -301,7 +301,8 @@ decode_tc_kernel(const __grid_constant__ Maps maps, const MlaDecodeArgs a, const
         } else {
             // ---------------------------------------------------------------- softmax, rescaling, output
             const uint32_t lanes = uint32_t(warp) << 21;  // TMEM lane 32 warp
-            // this thread's rows, each shared with the three other threads of its group of four
+            // this thread's rows, each shared with the three other threads of its group of four; rows behind the
+            // call's last hold anything, and what they give is not stored
             const int r1 = warp * 16 + (lane >> 2), r2 = r1 + 8, pair = 2 * (lane & 3);
             const int hidden1 = a.n - 1 - (r0 + r1) / a.H, hidden2 = a.n - 1 - (r0 + r2) / a.H;  // last keys that a row does not see
             const float sl2 = a.scale * kLog2e;
@@ -321,24 +322,24 @@ decode_tc_kernel(const __grid_constant__ Maps maps, const MlaDecodeArgs a, const
                     tc::tmem_ld_16x64(tmem + lanes + Tm<RB>::kS + (tile & 1) * 64, s);
                     const int left = w.len - t * kKeys;
                     const uint64_t mask = mi.mask[tile % kMasks];
-                    auto seen = [&](int r, int hidden) {
-                        const int n = r < rows ? left - hidden : 0;
-                        return mask & (n >= 64 ? ~0ull : n <= 0 ? 0ull : (1ull << n) - 1);
-                    };
-                    const uint64_t see1 = seen(r1, hidden1), see2 = seen(r2, hidden2);
-                    Ring z = ring;
-                    for (int i = 0; i < blocks; ++i, z.next(L.slots)) {
-                        if (left >= kKeys) continue;
+                    if (left < kKeys) {
                         // rows behind the sequence may hold anything: as values they have to be zero
-                        ok = tc::wait(&mi.full[z.slot], z.round & 1, dead) && ok;
-                        const int from = left * 8, per = kKeys * 8 - from;
-                        for (int x = tid; x < 2 * per; x += 128)
-                            tc::st_shared_v4(base + z.slot * kSlotBytes + (x / per) * 8192 + (from + x % per) * 16, 0, 0, 0, 0);
+                        Ring z = ring;
+                        for (int i = 0; i < blocks; ++i, z.next(L.slots)) {
+                            ok = tc::wait(&mi.full[z.slot], z.round & 1, dead) && ok;
+                            const int from = left * 8, per = kKeys * 8 - from;
+                            for (int x = tid; x < 2 * per; x += 128)
+                                tc::st_shared_v4(base + z.slot * kSlotBytes + (x / per) * 8192 + (from + x % per) * 16, 0, 0, 0, 0);
+                        }
                     }
-                    ring = z;
+                    if ((ring.slot += blocks) >= L.slots) ring.slot -= L.slots, ++ring.round;
                     ptx::tmem_wait_ld();
-                    if ((see1 & see2) != ~0ull) {
-                        const uint64_t m1 = see1 >> pair, m2 = see2 >> pair;
+                    if (left < kKeys + a.n - 1 || mask != ~0ull) {  // else every row sees every key
+                        auto seen = [&](int hidden) {
+                            const int n = left - hidden;
+                            return (mask & (n >= 64 ? ~0ull : n <= 0 ? 0ull : (1ull << n) - 1)) >> pair;
+                        };
+                        const uint64_t m1 = seen(hidden1), m2 = seen(hidden2);
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
                             if (!(m1 >> (8 * i) & 1)) s[4 * i] = 0xff800000u;
@@ -391,8 +392,13 @@ decode_tc_kernel(const __grid_constant__ Maps maps, const MlaDecodeArgs a, const
                                 ptx::tmem_ld32(tmem + lanes + i * RB + c, v);
                                 ptx::tmem_wait_ld();
 #pragma unroll
-                                for (int e = 0; e < 32; ++e)
-                                    v[e] = __float_as_uint(__uint_as_float(v[e]) * mi.factor[c + e]);
+                                for (int e = 0; e < 32; e += 4) {
+                                    const float4 f = *reinterpret_cast<const float4 *>(&mi.factor[c + e]);
+                                    v[e] = __float_as_uint(__uint_as_float(v[e]) * f.x);
+                                    v[e + 1] = __float_as_uint(__uint_as_float(v[e + 1]) * f.y);
+                                    v[e + 2] = __float_as_uint(__uint_as_float(v[e + 2]) * f.z);
+                                    v[e + 3] = __float_as_uint(__uint_as_float(v[e + 3]) * f.w);
+                                }
                                 ptx::tmem_st32(tmem + lanes + i * RB + c, v);
                             }
                         ptx::tmem_wait_st();
@@ -421,7 +427,7 @@ decode_tc_kernel(const __grid_constant__ Maps maps, const MlaDecodeArgs a, const
                     l += __shfl_xor_sync(0xffffffffu, l, 2);
                     const int row = r ? r2 : r1;
                     if (pair != 0 || row >= RB) continue;
-                    mi.factor[row] = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
+                    mi.factor[row] = l == 0.f ? 0.f : 1.f / l;
                     if (!whole) {
                         slot[RB * a.dc + 2 * row] = top[r] == -INFINITY ? top[r] : top[r] * a.scale;
                         slot[RB * a.dc + 2 * row + 1] = l;
@@ -434,20 +440,32 @@ decode_tc_kernel(const __grid_constant__ Maps maps, const MlaDecodeArgs a, const
                 ptx::named_barrier(1, 128);
                 ptx::tc_fence_after();
                 __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.o) + (int64_t(w.b) * R + r0) * a.dc;
-                for (int i = 0; i < blocks; ++i)
 #pragma unroll
-                    for (int c = 0; c < RB; c += 32) {
+                for (int c = 0; c < RB; c += 32) {
+                    // factors first: the compiler cannot move their loads over the stores below
+                    float f[32];
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4) {
+                        const float4 x = *reinterpret_cast<const float4 *>(&mi.factor[c + e]);
+                        f[e] = x.x, f[e + 1] = x.y, f[e + 2] = x.z, f[e + 3] = x.w;
+                    }
+                    for (int i = 0; i < blocks; ++i) {
                         uint32_t v[32];
                         ptx::tmem_ld32(tmem + lanes + i * RB + c, v);
                         ptx::tmem_wait_ld();
                         const int ch = i * 128 + warp * 32 + lane;  // lane of TMEM: the channel
+                        if (!whole) {
+                            float *to = slot + size_t(c) * a.dc + ch;
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            const float x = __uint_as_float(v[e]) * mi.factor[c + e];
-                            if (!whole) slot[size_t(c + e) * a.dc + ch] = x;
-                            else if (c + e < rows) out[size_t(c + e) * a.dc + ch] = __float2bfloat16_rn(x);
+                            for (int e = 0; e < 32; ++e, to += a.dc) *to = __uint_as_float(v[e]);
+                        } else {
+                            __nv_bfloat16 *to = out + size_t(c) * a.dc + ch;
+#pragma unroll
+                            for (int e = 0; e < 32; ++e, to += a.dc)
+                                if (c + e < rows) *to = __float2bfloat16_rn(__uint_as_float(v[e]) * f[e]);
                         }
                     }
+                }
                 ptx::tc_fence_before();
             }
         }
