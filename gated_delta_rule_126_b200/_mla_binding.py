@@ -8,46 +8,59 @@ import math
 import torch
 
 from . import _binding
-from ._binding import DTYPE_CODE, _check, _dims, _need, _offsets, _ptr, _shapes, _stream_handle
+from ._binding import DTYPE_CODE, _check, _dims, _offsets
 
 _declared = None
+_PACKED, _LAST = True, False  # what a tensor has to be contiguous in: all of it, or its last dimension
 
 
 def _lib():
     global _declared
+    if _declared is not None and _declared is _binding._lib:
+        return _declared
     lib = _binding.load()
-    if _declared is not lib:
-        c = ctypes
-        vp, i32, i64, sz, f32 = c.c_void_p, c.c_int, c.c_int64, c.c_size_t, c.c_float
-        lib.mla_append.restype = i32
-        lib.mla_append.argtypes = [vp, i64, vp, i64, i32, vp, f32, vp, i32, vp, vp, i32, i64, vp, i32, vp, i32, i32,
-                                   i32, i32, vp, i64, i64, i32, vp, i64, i64, vp, vp, vp]
-        lib.mla_decode_workspace_size.restype = sz
-        lib.mla_decode_workspace_size.argtypes = [i32] * 6
-        lib.mla_decode.restype = i32
-        lib.mla_decode.argtypes = [vp, i32, vp, i32, i32, vp, i32, vp, i32, i32, i32, i32, i32, f32, vp, vp, vp, sz, vp]
-        packed = [vp, i64, i64, vp, i64, i64, vp, i64, vp, i64, i64, i32, vp, vp, vp, vp, i32, i32, i32, i32, i32, f32, i32]
-        lib.mla_prefill.restype = i32
-        lib.mla_prefill.argtypes = packed + [vp, vp, vp]
-        lib.mla_backward_workspace_size.restype = sz
-        lib.mla_backward_workspace_size.argtypes = [i64, i64] + [i32] * 5
-        lib.mla_backward.restype = i32
-        lib.mla_backward.argtypes = packed + [vp] * 8 + [sz, vp]
-        lib.mla_status.restype = i32
-        lib.mla_status.argtypes = [vp]
-        _declared = lib
+    c = ctypes
+    vp, i32, i64, sz, f32 = c.c_void_p, c.c_int, c.c_int64, c.c_size_t, c.c_float
+    lib.mla_append.restype = i32
+    lib.mla_append.argtypes = [vp, i64, vp, i64, i32, vp, f32, vp, i32, vp, vp, i32, i64, vp, i32, vp, i32, i32,
+                               i32, i32, vp, i64, i64, i32, vp, i64, i64, vp, vp, vp]
+    lib.mla_decode_workspace_size.restype = sz
+    lib.mla_decode_workspace_size.argtypes = [i32] * 6
+    lib.mla_decode.restype = i32
+    lib.mla_decode.argtypes = [vp, i32, vp, i32, i32, vp, i32, vp, i32, i32, i32, i32, i32, f32, vp, vp, vp, sz, vp]
+    packed = [vp, i64, i64, vp, i64, i64, vp, i64, vp, i64, i64, i32, vp, vp, vp, vp, i32, i32, i32, i32, i32, f32, i32]
+    lib.mla_prefill.restype = i32
+    lib.mla_prefill.argtypes = packed + [vp, vp, vp]
+    lib.mla_backward_workspace_size.restype = sz
+    lib.mla_backward_workspace_size.argtypes = [i64, i64] + [i32] * 5
+    lib.mla_backward.restype = i32
+    lib.mla_backward.argtypes = packed + [vp] * 8 + [sz, vp]
+    lib.mla_status.restype = i32
+    lib.mla_status.argtypes = [vp]
+    _declared = lib
     return lib
 
 
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
 @contextlib.contextmanager
-def _on(stream, dev):
-    """The device and stream a call runs on: what it allocates belongs to that stream."""
-    with torch.cuda.device(dev):
-        if stream is None:
-            yield torch.cuda.current_stream()
-        else:
-            with torch.cuda.stream(stream):
-                yield stream
+def _switched(stream, index):
+    with torch.cuda.device(index), torch.cuda.stream(stream):
+        yield
+
+
+def _on(stream, index):
+    """Context and raw handle of the device and stream a call runs on: what it allocates belongs to that stream.
+    These calls are made once a token, so the usual case (current device and stream) switches nothing."""
+    if stream is not None:
+        return _switched(stream, index), stream.cuda_stream
+    raw = torch._C._cuda_getCurrentRawStream(index)
+    return (_NOTHING if torch.cuda.current_device() == index else torch.cuda.device(index)), raw
+
+
+_NOTHING = contextlib.nullcontext()
 
 
 def _rows(rows, used, *shape, dtype, device):
@@ -58,20 +71,37 @@ def _rows(rows, used, *shape, dtype, device):
     return t
 
 
-def _strided(t, name, dtype, device):
-    """A CUDA tensor whose last dimension is contiguous; the others may have any non-negative stride."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must have dtype {dtype}, got {t.dtype}")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
-        raise ValueError(f"{name} must be contiguous in its last dimension")
+def _verify(specs, index):
+    """Checks (name, tensor or None, shape, dtype, contiguous in what) of every tensor before a pointer reaches the
+    library: the kernels trust the sizes they are given.  Shapes come first, then the device of the first
+    tensor, whose index ``index`` is."""
+    for name, t, shape, _, _ in specs:
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.shape != shape:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    for name, t, _, dtype, packed in specs:
+        if t is None:
+            continue
+        if t.get_device() != index or index < 0:
+            if not t.is_cuda:
+                raise ValueError(f"{name} must be a CUDA tensor")
+            raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
+        if dtype is not None and t.dtype is not dtype:
+            raise ValueError(f"{name} must have dtype {dtype}, got {t.dtype}")
+        if packed:
+            if not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous")
+        elif t.stride(-1) != 1 and t.shape[-1] > 1:
+            raise ValueError(f"{name} must be contiguous in its last dimension")
 
 
 def _written(t, name):
     """An output's rows must be apart from one another: every stride covers what lies inside it."""
+    if t.is_contiguous():
+        return t
     inside = 1
     for size, stride in sorted(zip(t.shape, t.stride()), key=lambda p: p[1]):
         if size > 1 and stride < inside:
@@ -107,50 +137,42 @@ def mla_append(c, k_rope, cache, page_table, past_lens, cu_seqlens, norm_weight=
     pages, page, _ = _dims(cache, "cache", 3)
     N, width = _dims(page_table, "page_table", 2)
     H = 0 if q_rope is None else _dims(q_rope, "q_rope", 3)[1]
-    given = dict(out or {})
-    for name in given:
-        if name not in ("q_rope", "c", "k_rope") or (name == "q_rope" and q_rope is None) or (
-                name != "q_rope" and not packed) or (name == "k_rope" and not dr):
-            raise ValueError(f"out[{name!r}] is not an output of this call")
-    _shapes(k_rope=(k_rope, (T, dr)), cache=(cache, (pages, page, dc + dr)), past_lens=(past_lens, (N,)),
-            cu_seqlens=(cu_seqlens, (N + 1,)), norm_weight=(norm_weight, (dc,)), inv_freq=(inv_freq, (dr // 2,)),
-            q_rope=(q_rope, (T, H, dr)))
-    for name, shape in (("q_rope", (T, H, dr)), ("c", (T, dc)), ("k_rope", (T, dr))):
-        _shapes(**{f"out[{name!r}]": (given.get(name), shape)})
-    dev, dt = c.device, _type(c, "c")
-    _strided(c, "c", dt, None)
-    if dr:
-        _strided(k_rope, "k_rope", dt, dev)
-    _need(cache, "cache", dt, dev)
-    for name, t in (("page_table", page_table), ("past_lens", past_lens), ("cu_seqlens", cu_seqlens)):
-        _need(t, name, torch.int32, dev)
-    for name, t in (("norm_weight", norm_weight), ("inv_freq", inv_freq)):
-        if t is not None:
-            _need(t, name, torch.float32, dev)
-    if q_rope is not None:
-        _strided(q_rope, "q_rope", dt, dev)
-    if "q_rope" in given:
-        _strided(given["q_rope"], "out['q_rope']", dt, dev)
-        _written(given["q_rope"], "out['q_rope']")
-    for name in ("c", "k_rope"):
-        if name in given:
-            _need(given[name], f"out[{name!r}]", dt, dev)
-    st = lambda t, i: 0 if t is None else t.stride(i)
-    with _on(stream, dev) as use:
-        res = {"cache": cache}
-        if q_rope is not None:
-            res["q_rope"] = given["q_rope"] if "q_rope" in given else torch.empty(T, H, dr, dtype=dt, device=dev)
+    dt, index = _type(c, "c"), c.get_device()
+    i32, f32 = torch.int32, torch.float32
+    specs = [("c", c, (T, dc), dt, _LAST), ("k_rope", k_rope, (T, dr), dt, _LAST),
+             ("cache", cache, (pages, page, dc + dr), dt, _PACKED), ("page_table", page_table, (N, width), i32, _PACKED),
+             ("past_lens", past_lens, (N,), i32, _PACKED), ("cu_seqlens", cu_seqlens, (N + 1,), i32, _PACKED),
+             ("norm_weight", norm_weight, (dc,), f32, _PACKED), ("inv_freq", inv_freq, (dr // 2,), f32, _PACKED),
+             ("q_rope", q_rope, (T, H, dr), dt, _LAST)]
+    qo = co = ko = None
+    if out:
+        for name in out:
+            if name not in ("q_rope", "c", "k_rope") or (name == "q_rope" and q_rope is None) or (
+                    name != "q_rope" and not packed) or (name == "k_rope" and not dr):
+                raise ValueError(f"out[{name!r}] is not an output of this call")
+        qo, co, ko = out.get("q_rope"), out.get("c"), out.get("k_rope")
+        specs += [("out['q_rope']", qo, (T, H, dr), dt, _LAST), ("out['c']", co, (T, dc), dt, _PACKED),
+                  ("out['k_rope']", ko, (T, dr), dt, _PACKED)]
+    _verify(specs, index)
+    if qo is not None:
+        _written(qo, "out['q_rope']")
+    context, raw = _on(stream, index)
+    with context:
+        if q_rope is not None and qo is None:
+            qo = torch.empty(T, H, dr, dtype=dt, device=c.device)
         if packed:
-            res["c"] = given["c"] if "c" in given else torch.empty(T, dc, dtype=dt, device=dev)
-            if dr:
-                res["k_rope"] = given["k_rope"] if "k_rope" in given else torch.empty(T, dr, dtype=dt, device=dev)
-        qo = res.get("q_rope")
-        status = lib.mla_append(_ptr(c), st(c, 0), _ptr(k_rope), st(k_rope, 0), DTYPE_CODE[dt], _ptr(norm_weight),
-                                float(eps), _ptr(inv_freq), int(bool(interleaved)), _ptr(cu_seqlens),
-                                _ptr(past_lens), N, T, _ptr(page_table), width, _ptr(cache), pages, page, dc, dr,
-                                _ptr(q_rope), st(q_rope, 0), st(q_rope, 1), H, _ptr(qo), st(qo, 0), st(qo, 1),
-                                _ptr(res.get("c")), _ptr(res.get("k_rope")), _stream_handle(use))
+            co = torch.empty(T, dc, dtype=dt, device=c.device) if co is None else co
+            ko = torch.empty(T, dr, dtype=dt, device=c.device) if ko is None and dr else ko
+        qs, qos = (q_rope.stride(), qo.stride()) if H else ((0, 0), (0, 0))
+        status = lib.mla_append(c.data_ptr(), c.stride(0), _ptr(k_rope), k_rope.stride(0) if dr else 0, DTYPE_CODE[dt],
+                                _ptr(norm_weight), eps, _ptr(inv_freq), 1 if interleaved else 0, cu_seqlens.data_ptr(),
+                                past_lens.data_ptr(), N, T, page_table.data_ptr(), width, cache.data_ptr(), pages, page,
+                                dc, dr, _ptr(q_rope), qs[0], qs[1], H, _ptr(qo), qos[0], qos[1], _ptr(co), _ptr(ko), raw)
     _check(status, "mla_append")
+    res = {"cache": cache}
+    for name, t in (("q_rope", qo), ("c", co), ("k_rope", ko)):
+        if t is not None:
+            res[name] = t
     return res
 
 
@@ -174,27 +196,23 @@ def mla_decode(q, cache, page_table, seq_lens, d_latent, scale, o=None, lse=None
     dc = int(d_latent)
     if not 1 <= dc <= W:
         raise ValueError(f"d_latent must lie in 1..{W}, got {dc}")
-    _shapes(cache=(cache, (pages, page, W)), page_table=(page_table, (B, width)), seq_lens=(seq_lens, (B,)),
-            o=(o, (B, n, H, dc)), lse=(lse, (B, n, H)))
-    dev, dt = q.device, _type(q, "q")
-    _need(q, "q", dt)
-    _need(cache, "cache", dt, dev)
-    _need(page_table, "page_table", torch.int32, dev)
-    _need(seq_lens, "seq_lens", torch.int32, dev)
-    for name, t, want in (("o", o, dt), ("lse", lse, torch.float32), ("workspace", workspace, None)):
-        if t is not None:
-            _need(t, name, want, dev)
-    with _on(stream, dev) as use:
+    dt, index = _type(q, "q"), q.get_device()
+    _verify([("q", q, (B, n, H, W), dt, _PACKED), ("cache", cache, (pages, page, W), dt, _PACKED),
+             ("page_table", page_table, (B, width), torch.int32, _PACKED), ("seq_lens", seq_lens, (B,), torch.int32, _PACKED),
+             ("o", o, (B, n, H, dc), dt, _PACKED), ("lse", lse, (B, n, H), torch.float32, _PACKED),
+             ("workspace", workspace, workspace.shape if isinstance(workspace, torch.Tensor) else (), None, _PACKED)], index)
+    context, raw = _on(stream, index)
+    with context:
         if o is None:
-            o = torch.empty(B, n, H, dc, dtype=dt, device=dev)
+            o = torch.empty(B, n, H, dc, dtype=dt, device=q.device)
         if lse is None and want_lse:
-            lse = torch.empty(B, n, H, dtype=torch.float32, device=dev)
+            lse = torch.empty(B, n, H, dtype=torch.float32, device=q.device)
         if workspace is None:
-            workspace = torch.empty(max(mla_decode_workspace_size(B, n, H, dc, W - dc, dt), 256), dtype=torch.uint8,
-                                    device=dev)
-        st = lib.mla_decode(_ptr(q), DTYPE_CODE[dt], _ptr(cache), pages, page, _ptr(page_table), width,
-                            _ptr(seq_lens), B, n, H, dc, W - dc, float(scale), _ptr(o), _ptr(lse), _ptr(workspace),
-                            workspace.numel() * workspace.element_size(), _stream_handle(use))
+            size = lib.mla_decode_workspace_size(B, n, H, dc, W - dc, DTYPE_CODE[dt])
+            workspace = torch.empty(max(size, 256), dtype=torch.uint8, device=q.device)
+        st = lib.mla_decode(q.data_ptr(), DTYPE_CODE[dt], cache.data_ptr(), pages, page, page_table.data_ptr(), width,
+                            seq_lens.data_ptr(), B, n, H, dc, W - dc, scale, o.data_ptr(), _ptr(lse),
+                            workspace.data_ptr(), workspace.numel() * workspace.element_size(), raw)
     _check(st, "mla_decode")
     return o, lse
 
@@ -205,25 +223,26 @@ def _packed(q, k, v, cu_q, cu_k, k_rope, scale, cu_q_host, cu_k_host, o, lse, dO
     Tk, _, dn = _dims(k, "k", 3)
     dv = _dims(v, "v", 3)[2]
     dr = 0 if k_rope is None else _dims(k_rope, "k_rope", 2)[1]
-    _shapes(q=(q, (Tq, H, dn + dr)), k=(k, (Tk, H, dn)), v=(v, (Tk, H, dv)), k_rope=(k_rope, (Tk, dr)),
-            o=(o, (Tq, H, dv)), lse=(lse, (Tq, H)), dO=(dO, (Tq, H, dv)))
+    dt, index = _type(q, "q"), q.get_device()
+    i32 = torch.int32
+    specs = [("q", q, (Tq, H, dn + dr), dt, _LAST), ("k", k, (Tk, H, dn), dt, _LAST), ("v", v, (Tk, H, dv), dt, _LAST),
+             ("k_rope", k_rope, (Tk, dr), dt, _LAST), ("o", o, (Tq, H, dv), dt, _PACKED),
+             ("lse", lse, (Tq, H), torch.float32, _PACKED), ("dO", dO, (Tq, H, dv), dt, _PACKED)]
+    for name, t, shape, _, _ in specs:  # before the offsets, which may have to come from the device
+        if isinstance(t, torch.Tensor) and t.shape != shape:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     N, cq = _offsets(cu_q, cu_q_host, Tq)
     M, ck = _offsets(cu_k, cu_k_host, Tk)
     if N != M:
         raise ValueError(f"cu_q holds {N} sequences, cu_k {M}")
-    dev, dt = q.device, _type(q, "q")
-    _strided(q, "q", dt, None)
-    _strided(k, "k", dt, dev)
-    _strided(v, "v", dt, dev)
-    if dr:
-        _strided(k_rope, "k_rope", dt, dev)
-    _need(cu_q, "cu_q", torch.int32, dev)
-    _need(cu_k, "cu_k", torch.int32, dev)
+    specs += [("cu_q", cu_q, (N + 1,), i32, _PACKED), ("cu_k", cu_k, (N + 1,), i32, _PACKED)]
+    _verify(specs, index)
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
-    lead = [_ptr(q), q.stride(0), q.stride(1), _ptr(k), k.stride(0), k.stride(1), _ptr(k_rope),
-            k_rope.stride(0) if dr else 0, _ptr(v), v.stride(0), v.stride(1), DTYPE_CODE[dt], _ptr(cu_q),
-            ctypes.c_void_p(cq.data_ptr()), _ptr(cu_k), ctypes.c_void_p(ck.data_ptr()), N, H, dn, dr, dv, scale]
-    return (Tq, Tk, H, dn, dr, dv, dev, dt, cq, ck), lead
+    qs, ks, vs = q.stride(), k.stride(), v.stride()
+    lead = (q.data_ptr(), qs[0], qs[1], k.data_ptr(), ks[0], ks[1], _ptr(k_rope), k_rope.stride(0) if dr else 0,
+            v.data_ptr(), vs[0], vs[1], DTYPE_CODE[dt], cu_q.data_ptr(), cq.data_ptr(), cu_k.data_ptr(), ck.data_ptr(),
+            N, H, dn, dr, dv, scale)
+    return (Tq, Tk, H, dn, dr, dv, index, dt, cq, ck), lead
 
 
 def mla_prefill(q, k, v, cu_q, cu_k, k_rope=None, scale=None, causal=True, cu_q_host=None, cu_k_host=None, o=None,
@@ -237,17 +256,16 @@ def mla_prefill(q, k, v, cu_q, cu_k, k_rope=None, scale=None, causal=True, cu_q_
     rows that belong to no sequence are zero, or left as they were in a given o or lse.
     """
     lib = _lib()
-    (Tq, Tk, H, dn, dr, dv, dev, dt, cq, ck), lead = _packed(q, k, v, cu_q, cu_k, k_rope, scale, cu_q_host, cu_k_host,
+    (Tq, Tk, H, dn, dr, dv, index, dt, cq, ck), lead = _packed(q, k, v, cu_q, cu_k, k_rope, scale, cu_q_host, cu_k_host,
                                                              o, lse)
-    for name, t, want in (("o", o, dt), ("lse", lse, torch.float32)):
-        if t is not None:
-            _need(t, name, want, dev)
-    with _on(stream, dev) as use:
+    context, raw = _on(stream, index)
+    with context:
+        used = int(cq[-1]) if o is None or (lse is None and want_lse) else Tq
         if o is None:
-            o = _rows(Tq, int(cq[-1]), H, dv, dtype=dt, device=dev)
+            o = _rows(Tq, used, H, dv, dtype=dt, device=q.device)
         if lse is None and want_lse:
-            lse = _rows(Tq, int(cq[-1]), H, dtype=torch.float32, device=dev)
-        st = lib.mla_prefill(*lead, int(bool(causal)), _ptr(o), _ptr(lse), _stream_handle(use))
+            lse = _rows(Tq, used, H, dtype=torch.float32, device=q.device)
+        st = lib.mla_prefill(*lead, 1 if causal else 0, o.data_ptr(), _ptr(lse), raw)
     _check(st, "mla_prefill")
     return o, lse
 
@@ -266,29 +284,28 @@ def mla_backward(q, k, v, cu_q, cu_k, o, lse, dO, k_rope=None, scale=None, causa
     over the heads).  Rows that belong to no sequence come back zero.
     """
     lib = _lib()
-    (Tq, Tk, H, dn, dr, dv, dev, dt, cq, ck), lead = _packed(q, k, v, cu_q, cu_k, k_rope, scale, cu_q_host, cu_k_host,
+    (Tq, Tk, H, dn, dr, dv, index, dt, cq, ck), lead = _packed(q, k, v, cu_q, cu_k, k_rope, scale, cu_q_host, cu_k_host,
                                                              o, lse, dO)
-    _need(o, "o", dt, dev)
-    _need(lse, "lse", torch.float32, dev)
-    _need(dO, "dO", dt, dev)
+    if o is None or lse is None or dO is None:
+        raise TypeError("o, lse and dO must be torch.Tensors")
     tq, tk = int(cq[-1]), int(ck[-1])
-
     if workspace is not None:
-        _need(workspace, "workspace", None, dev)
-    like = dict(dtype=dt, device=dev)
-    with _on(stream, dev) as use:
+        _verify([("workspace", workspace, workspace.shape, None, _PACKED)], index)
+    like = dict(dtype=dt, device=q.device)
+    context, raw = _on(stream, index)
+    with context:
         out = dict(dq=_rows(Tq, tq, H, dn + dr, **like), dk=_rows(Tk, tk, H, dn, **like), dv=_rows(Tk, tk, H, dv, **like),
                    dk_rope=_rows(Tk, tk, dr, **like) if dr else None)
         if workspace is None:
-            workspace = torch.empty(max(mla_backward_workspace_size(tq, tk, H, dn, dr, dv, dt), 256),
-                                    dtype=torch.uint8, device=dev)
-        st = lib.mla_backward(*lead, int(bool(causal)), _ptr(o), _ptr(lse), _ptr(dO), _ptr(out["dq"]),
-                              _ptr(out["dk"]), _ptr(out["dk_rope"]), _ptr(out["dv"]), _ptr(workspace),
-                              workspace.numel() * workspace.element_size(), _stream_handle(use))
+            size = lib.mla_backward_workspace_size(tq, tk, H, dn, dr, dv, DTYPE_CODE[dt])
+            workspace = torch.empty(max(size, 256), dtype=torch.uint8, device=q.device)
+        st = lib.mla_backward(*lead, 1 if causal else 0, o.data_ptr(), lse.data_ptr(), dO.data_ptr(),
+                              out["dq"].data_ptr(), out["dk"].data_ptr(), _ptr(out["dk_rope"]), out["dv"].data_ptr(),
+                              workspace.data_ptr(), workspace.numel() * workspace.element_size(), raw)
     _check(st, "mla_backward")
     return out
 
 
 def mla_status(stream=None):
     """Waits for the stream; the status flagged by the mla_* kernels run so far on the current device (0 = fine)."""
-    return int(_lib().mla_status(_stream_handle(stream)))
+    return int(_lib().mla_status(_binding._stream_handle(stream)))

@@ -7,8 +7,8 @@
 //   S^T = K Q^T, dP^T = V dO^T  [128 x 64];  dV += P^T dO, dK += dS^T Q, with P^T and dS^T in TMEM
 //   as the left operands; Q and dO tiles serve as [q x d] K-major and as MN-major operand alike.
 //   TMEM: S^T twice 64 columns, dP^T 64, dV 128, dK 192: all 512.
-// dq_tc_kernel: a block owns 128 queries of one head and streams the keys in blocks of 128.
-//   S = Q K^T, dP = dO V^T  [128 x 128];  dQ += dS K, dS in TMEM.  TMEM: S 128, dP 128, dQ 192, dS 64.
+// dq_tc_kernel: a block owns 128 queries of one head and streams the keys in blocks of 96.
+//   S = Q K^T, dP = dO V^T  [128 x 96];  dQ += dS K, dS in TMEM.  TMEM: S 96, dP 96, dQ 192, dS 48.
 // P = exp2(scale log2(e) S - lse2) and dS = P (dP - delta) are rounded to bf16 for their products; the
 // factor `scale` of dq and dk is applied to the float32 sums at the end.
 // Bound by the tensor cores.  Warps 0-7: elementwise work and output, two warpgroups with half of the columns each;
@@ -261,11 +261,11 @@ __global__ void __launch_bounds__(kThreads, 1) dkv_tc_kernel(const __grid_consta
         if (ok && n > 0) ok = tc::wait(&mi.done, 0, dead);
         ptx::tc_fence_after();
         if (ok) {
-            // warpgroup 0 writes dv, warpgroup 1 dk; each half of the shared part's share
-            const uint32_t lanes = tmem + (uint32_t(w) << 21);
-            const int64_t row_at = int64_t(pl.k0 + j) * a.H + h;
-            __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(half ? a.dk : a.dv_out) + row_at * 128;
-            const float f = half ? a.scale : 1.f;
+            // warpgroup 0 writes dv, warpgroup 1 dk; each half of the shared part's share.  The rows pass through
+            // the keys' and values' place, which nothing reads any more.
+            const uint32_t lanes = tmem + (uint32_t(w) << 21), stage = base + warp * tc::RowStage<16>::kBytes;
+            const int rows = pl.lk - (j - lane);
+            const int64_t first_row = int64_t(pl.k0 + j - lane);
             auto load = [&](uint32_t col, uint32_t (&v)[32]) {
                 if (n > 0) {
                     ptx::tmem_ld32(lanes + col, v);
@@ -278,27 +278,18 @@ __global__ void __launch_bounds__(kThreads, 1) dkv_tc_kernel(const __grid_consta
             uint32_t v[32];
             for (int c = 0; c < 4; ++c) {
                 load((half ? kTmDk : kTmDv) + 32 * c, v);
-                if (j < pl.lk) {
-#pragma unroll
-                    for (int e = 0; e < 32; e += 8) {
-                        uint4 x;
-                        x.x = tc::pack_bf16(__uint_as_float(v[e]) * f, __uint_as_float(v[e + 1]) * f);
-                        x.y = tc::pack_bf16(__uint_as_float(v[e + 2]) * f, __uint_as_float(v[e + 3]) * f);
-                        x.z = tc::pack_bf16(__uint_as_float(v[e + 4]) * f, __uint_as_float(v[e + 5]) * f);
-                        x.w = tc::pack_bf16(__uint_as_float(v[e + 6]) * f, __uint_as_float(v[e + 7]) * f);
-                        reinterpret_cast<uint4 *>(out)[4 * c + e / 8] = x;
-                    }
-                }
+                tc::put_bf16<16>(stage, lane, 4 * c, v, half ? a.scale : 1.f);
             }
+            tc::RowStage<16>::store(stage, lane, static_cast<__nv_bfloat16 *>(half ? a.dk : a.dv_out) + (first_row * a.H + h) * 128,
+                                    int64_t(a.H) * 256, rows);
             if (a.dr) {
                 load(kTmDk + 128 + 32 * half, v);
-                float4 *part = reinterpret_cast<float4 *>(a.dkr_partial + (int64_t(h) * a.Tk + pl.k0 + j) * 64 + 32 * half);
-                if (j < pl.lk) {
 #pragma unroll
-                    for (int e = 0; e < 32; e += 4)
-                        part[e / 4] = make_float4(__uint_as_float(v[e]) * a.scale, __uint_as_float(v[e + 1]) * a.scale,
-                                                  __uint_as_float(v[e + 2]) * a.scale, __uint_as_float(v[e + 3]) * a.scale);
+                for (int e = 0; e < 8; ++e) {
+                    auto x = [&](int i) { return __float_as_uint(__uint_as_float(v[4 * e + i]) * a.scale); };
+                    tc::RowStage<8>::put(stage, lane, e, x(0), x(1), x(2), x(3));
                 }
+                tc::RowStage<8>::store(stage, lane, a.dkr_partial + (int64_t(h) * a.Tk + first_row) * 64 + 32 * half, 256, rows);
             }
         }
     }
@@ -311,17 +302,23 @@ __global__ void __launch_bounds__(kThreads, 1) dkv_tc_kernel(const __grid_consta
 }
 
 // ------------------------------------------------------------------------------ dq
-// Shared memory: Q (3 chunks), dO (2), keys twice 3, values 2.
-constexpr uint32_t kOffDo = 3 * kChunk, kOffK = 5 * kChunk, kOffVq = 11 * kChunk, kOffMiscQ = 13 * kChunk;
+// Key blocks of 96: with Q and dO resident (80 KB), three blocks of keys and one and a half of values fit, so that
+// a block's keys, which stay until its dQ product, do not hold up the loads of the next but one (blocks of 128
+// allow two: 3,880 cycles a block instead of the products' 2,048).
+// Shared memory: Q (3 chunks of 128 rows), dO (2), three blocks of keys (3 chunks of 96 rows), three chunks of values.
+constexpr int kKb = 96;
+constexpr uint32_t kKbChunk = kKb * 128;
+constexpr uint32_t kOffDo = 3 * kChunk, kOffK = 5 * kChunk, kOffVq = kOffK + 9 * kKbChunk, kOffMiscQ = kOffVq + 3 * kKbChunk;
 constexpr uint32_t kDqSmem = kOffMiscQ + 1024 + 1024;
-constexpr uint32_t kTqDp = 128, kTqDq = 256, kTqDs = 448;
+constexpr uint32_t kTqDp = 96, kTqDq = 192, kTqDs = 384;
 
 struct DqMisc {
-    uint64_t q_full, do_full, k_full[2], k_empty[2], v_full, v_empty, s_full, s_read, dp_full, ds_full, done;
+    uint64_t q_full, do_full, k_full[3], k_empty[3], v_full[3], v_empty[3], s_full, s_read, dp_full, ds_full, done;
     int64_t find[kThreads / 32 + 2];
     uint32_t tmem, dead;
 };
 static_assert(sizeof(DqMisc) <= 1024, "misc");
+static_assert(kDqSmem <= 232448, "shared memory");
 
 __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constant__ DkvMaps maps, const MlaArgs a) {
     extern __shared__ uint8_t raw[];
@@ -330,9 +327,9 @@ __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constan
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int h = blockIdx.x % a.H, kc = a.dr ? 3 : 2;
     if (tid == 0) {
-        for (uint64_t *b : {&mi.q_full, &mi.do_full, &mi.k_full[0], &mi.k_full[1], &mi.k_empty[0], &mi.k_empty[1],
-                            &mi.v_full, &mi.v_empty, &mi.s_full, &mi.dp_full, &mi.done})
-            ptx::mbar_init(b, 1);
+        for (int i = 0; i < 3; ++i)
+            for (uint64_t *b : {&mi.k_full[i], &mi.k_empty[i], &mi.v_full[i], &mi.v_empty[i]}) ptx::mbar_init(b, 1);
+        for (uint64_t *b : {&mi.q_full, &mi.do_full, &mi.s_full, &mi.dp_full, &mi.done}) ptx::mbar_init(b, 1);
         ptx::mbar_init(&mi.s_read, 256);
         ptx::mbar_init(&mi.ds_full, 256);
         mi.dead = 0;
@@ -352,54 +349,64 @@ __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constan
     const Place pl = place_of(a, seq);
     const int i0 = tile * 128;
     auto key_end = [&](int i) { return a.causal ? max(0, min(pl.lk, i + 1 + pl.off)) : pl.lk; };
-    const int n = (key_end(min(i0 + 128, pl.lq) - 1) + 127) / 128;
+    const int n = (key_end(min(i0 + 128, pl.lq) - 1) + kKb - 1) / kKb;
 
     if (warp == 9) {
         if (tc::elect() && n > 0) {
+            int ks = 0, vs = 0;  // loads begun: blocks of keys, chunks of values
+            bool ok = true;
             auto load_k = [&](int j) {
-                if (j >= 2 && !tc::wait(&mi.k_empty[j & 1], (j / 2 - 1) & 1, dead)) return false;
-                const uint32_t dst = base + kOffK + (j & 1) * 3 * kChunk;
-                ptx::mbar_arrive_expect_tx(&mi.k_full[j & 1], kc * kChunk);
+                if (!ok || j >= n || (j >= 3 && !(ok = tc::wait(&mi.k_empty[j % 3], (j / 3 - 1) & 1, dead)))) return;
+                const uint32_t dst = base + kOffK + (j % 3) * 3 * kKbChunk;
+                ptx::mbar_arrive_expect_tx(&mi.k_full[j % 3], kc * kKbChunk);
                 for (int c = 0; c < 2; ++c)
-                    tc::tma_load_3d(dst + c * kChunk, &maps.k, &mi.k_full[j & 1], 64 * c, h, pl.k0 + j * 128);
-                if (a.dr) tc::tma_load_2d(dst + 2 * kChunk, &maps.kr, &mi.k_full[j & 1], 0, pl.k0 + j * 128);
-                return true;
+                    tc::tma_load_3d(dst + c * kKbChunk, &maps.k, &mi.k_full[j % 3], 64 * c, h, pl.k0 + j * kKb);
+                if (a.dr) tc::tma_load_2d(dst + 2 * kKbChunk, &maps.kr, &mi.k_full[j % 3], 0, pl.k0 + j * kKb);
+                ++ks;
+            };
+            auto load_v = [&](int x) {  // chunk x & 1 of block x / 2
+                if (!ok || x >= 2 * n || (x >= 3 && !(ok = tc::wait(&mi.v_empty[x % 3], (x / 3 - 1) & 1, dead)))) return;
+                ptx::mbar_arrive_expect_tx(&mi.v_full[x % 3], kKbChunk);
+                tc::tma_load_3d(base + kOffVq + (x % 3) * kKbChunk, &maps.v, &mi.v_full[x % 3], 64 * (x & 1), h, pl.k0 + (x >> 1) * kKb);
+                ++vs;
             };
             ptx::mbar_arrive_expect_tx(&mi.q_full, kc * kChunk);
             for (int c = 0; c < kc; ++c) tc::tma_load_3d(base + c * kChunk, &maps.q, &mi.q_full, 64 * c, h, pl.q0 + i0);
-            int ks = 0, vs = 0;  // loads begun
-            bool ok = load_k(ks++);
+            load_k(0);
             ptx::mbar_arrive_expect_tx(&mi.do_full, 2 * kChunk);
             for (int c = 0; c < 2; ++c)
                 tc::tma_load_3d(base + kOffDo + c * kChunk, &maps.dO, &mi.do_full, 64 * c, h, pl.q0 + i0);
-            for (int j = 0; ok && j < n; ++j) {
-                if (j && !(ok = tc::wait(&mi.v_empty, (j - 1) & 1, dead))) break;
-                ptx::mbar_arrive_expect_tx(&mi.v_full, 2 * kChunk);
-                for (int c = 0; c < 2; ++c)
-                    tc::tma_load_3d(base + kOffVq + c * kChunk, &maps.v, &mi.v_full, 64 * c, h, pl.k0 + j * 128);
-                ++vs;
-                if (j + 1 < n && (ok = load_k(j + 1))) ++ks;
+            load_v(0);
+            load_v(1);
+            load_k(1);
+            load_v(2);
+            load_k(2);
+            for (int j = 0; ok && j < n; ++j) {  // in the order in which the products free the slots
+                load_v(2 * j + 3);
+                load_v(2 * j + 4);
+                load_k(j + 3);
             }
             if (!ok) {  // an error: the copies in flight land before the block ends
                 ptx::mbar_wait_bounded(&mi.q_full, 0, tc::kWaitCycles);
                 ptx::mbar_wait_bounded(&mi.do_full, 0, tc::kWaitCycles);
-                for (int j = max(0, ks - 2); j < ks; ++j)
-                    ptx::mbar_wait_bounded(&mi.k_full[j & 1], (j / 2) & 1, tc::kWaitCycles);
-                if (vs) ptx::mbar_wait_bounded(&mi.v_full, (vs - 1) & 1, tc::kWaitCycles);
+                for (int j = max(0, ks - 3); j < ks; ++j)
+                    ptx::mbar_wait_bounded(&mi.k_full[j % 3], (j / 3) & 1, tc::kWaitCycles);
+                for (int x = max(0, vs - 3); x < vs; ++x)
+                    ptx::mbar_wait_bounded(&mi.v_full[x % 3], (x / 3) & 1, tc::kWaitCycles);
             }
         }
         __syncwarp();
     } else if (warp == 8) {
         if (tc::elect() && n > 0) {
-            constexpr uint32_t kIdS = tc::idesc(128, 128, false, false);
+            constexpr uint32_t kIdS = tc::idesc(128, kKb, false, false);
             const uint32_t id_q = tc::idesc(128, 64 * kc, false, true);
-            const uint64_t desc = ptx::sdesc_sw128(base), desc_mn = ptx::sdesc_sw128_mn(base, kChunk, 1024);
-            auto keys = [&](int j) { return kOffK + (j & 1) * 3 * kChunk; };
+            const uint64_t desc = ptx::sdesc_sw128(base), desc_mn = ptx::sdesc_sw128_mn(base, kKbChunk, 1024);
+            auto keys = [&](int j) { return kOffK + (j % 3) * 3 * kKbChunk; };
             auto scores = [&](int j) {
-                if (!tc::wait(&mi.k_full[j & 1], (j >> 1) & 1, dead)) return false;
+                if (!tc::wait(&mi.k_full[j % 3], (j / 3) & 1, dead)) return false;
                 ptx::tc_fence_after();
                 for (int c = 0; c < kc; ++c) {
-                    const uint64_t qd = tc::moved(desc, c * kChunk), kd = tc::moved(qd, keys(j));
+                    const uint64_t qd = tc::moved(desc, c * kChunk), kd = tc::moved(desc, keys(j) + c * kKbChunk);
                     ptx::mma_ss(tmem, qd, kd, kIdS, c > 0);
 #pragma unroll
                     for (int k = 1; k < 4; ++k) ptx::mma_ss(tmem, tc::moved(qd, 32 * k), tc::moved(kd, 32 * k), kIdS, 1);
@@ -408,16 +415,18 @@ __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constan
                 return true;
             };
             auto dprobs = [&](int j) {
-                if (!tc::wait(&mi.v_full, j & 1, dead)) return false;
-                ptx::tc_fence_after();
 #pragma unroll
-                for (int c = 0; c < 2; ++c)
+                for (int c = 0; c < 2; ++c) {
+                    const int x = 2 * j + c;
+                    if (!tc::wait(&mi.v_full[x % 3], (x / 3) & 1, dead)) return false;
+                    ptx::tc_fence_after();
+                    const uint64_t od = tc::moved(desc, kOffDo + c * kChunk), vd = tc::moved(desc, kOffVq + (x % 3) * kKbChunk);
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        ptx::mma_ss(tmem + kTqDp, tc::moved(desc, kOffDo + c * kChunk + 32 * k),
-                                    tc::moved(desc, kOffVq + c * kChunk + 32 * k), kIdS, c + k > 0);
+                        ptx::mma_ss(tmem + kTqDp, tc::moved(od, 32 * k), tc::moved(vd, 32 * k), kIdS, c + k > 0);
+                    ptx::mma_commit(&mi.v_empty[x % 3]);
+                }
                 ptx::mma_commit(&mi.dp_full);
-                ptx::mma_commit(&mi.v_empty);
                 return true;
             };
             bool ok = tc::wait(&mi.q_full, 0, dead) && scores(0) && tc::wait(&mi.do_full, 0, dead) && dprobs(0);
@@ -429,10 +438,11 @@ __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constan
                 }
                 if (!ok || !(ok = tc::wait(&mi.ds_full, j & 1, dead))) break;
                 ptx::tc_fence_after();
+                const uint64_t kd = tc::moved(desc_mn, keys(j));
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    ptx::mma_ts(tmem + kTqDq, tmem + kTqDs + 8 * k, tc::moved(desc_mn, keys(j) + 2048 * k), id_q, j + k > 0);
-                ptx::mma_commit(&mi.k_empty[j & 1]);
+                for (int k = 0; k < kKb / 16; ++k)
+                    ptx::mma_ts(tmem + kTqDq, tmem + kTqDs + 8 * k, tc::moved(kd, 2048 * k), id_q, j + k > 0);
+                ptx::mma_commit(&mi.k_empty[j % 3]);
                 if (j + 1 < n) ok = dprobs(j + 1);
             }
             ptx::mma_commit(&mi.done);
@@ -440,6 +450,7 @@ __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constan
         }
         __syncwarp();
     } else {
+        constexpr int kHalf = kKb / 2;  // columns of this warpgroup
         const int half = warp >> 2, w = warp & 3, row = w * 32 + lane, r = i0 + row;
         const uint32_t lanes = tmem + (uint32_t(w) << 21);
         const float sl2 = a.scale * kLog2e;
@@ -450,45 +461,43 @@ __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constan
         for (int j = 0; j < n; ++j) {
             if (!(ok = tc::wait(&mi.s_full, j & 1, dead))) break;
             ptx::tc_fence_after();
-            uint32_t v[2][32];
-            ptx::tmem_ld32(lanes + 64 * half, v[0]);
-            ptx::tmem_ld32(lanes + 64 * half + 32, v[1]);
+            uint32_t v[32], u[16];
+            ptx::tmem_ld32(lanes + kHalf * half, v);
+            ptx::tmem_ld16(lanes + kHalf * half + 32, u);
             ptx::tmem_wait_ld();
             ptx::tc_fence_before();
             ptx::mbar_arrive(&mi.s_read);
-            const int seen = end - j * 128 - 64 * half;  // columns of this half that the row sees
-            const bool masked = __any_sync(0xffffffffu, seen < 64);
-            float p[64];
+            const int seen = end - j * kKb - kHalf * half;  // columns of this half that the row sees
+            const bool masked = __any_sync(0xffffffffu, seen < kHalf);
+            float p[kHalf];
 #pragma unroll
-            for (int c = 0; c < 64; ++c) {
-                p[c] = ptx::ex2_approx(fmaf(__uint_as_float(v[c >> 5][c & 31]), sl2, -lse2));
-            }
-            if (pl.lk - j * 128 < 128) {
+            for (int c = 0; c < kHalf; ++c)
+                p[c] = ptx::ex2_approx(fmaf(__uint_as_float(c < 32 ? v[c & 31] : u[c & 15]), sl2, -lse2));
+            if (pl.lk - j * kKb < kKb) {
                 // key rows behind the sequence may hold anything: in dQ += dS K they have to be zero
-                const int from = max(0, pl.lk - j * 128) * 8, per = 1024 - from;
+                const int from = max(0, pl.lk - j * kKb) * 8, per = kKb * 8 - from;
                 for (int x = tid; x < per * kc; x += 256)
-                    tc::st_shared_v4(base + kOffK + ((j & 1) * 3 + x / per) * kChunk + (from + x % per) * 16, 0, 0, 0, 0);
+                    tc::st_shared_v4(base + kOffK + ((j % 3) * 3 + x / per) * kKbChunk + (from + x % per) * 16, 0, 0, 0, 0);
                 ptx::fence_proxy_async_smem();
             }
             if (!(ok = tc::wait(&mi.dp_full, j & 1, dead))) break;  // the last dQ has read dS, too
             ptx::tc_fence_after();
+            ptx::tmem_ld32(lanes + kTqDp + kHalf * half, v);
+            ptx::tmem_ld16(lanes + kTqDp + kHalf * half + 32, u);
+            ptx::tmem_wait_ld();
+            uint32_t x[16], y[8];
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {
-                ptx::tmem_ld32(lanes + kTqDp + 64 * half + 32 * g, v[0]);
-                ptx::tmem_wait_ld();
-                uint32_t x[16];
-#pragma unroll
-                for (int c = 0; c < 16; ++c) {
-                    float y = p[32 * g + 2 * c] * (__uint_as_float(v[0][2 * c]) - delta);
-                    float z = p[32 * g + 2 * c + 1] * (__uint_as_float(v[0][2 * c + 1]) - delta);
-                    if (masked) {
-                        if (32 * g + 2 * c >= seen) y = 0.f;
-                        if (32 * g + 2 * c + 1 >= seen) z = 0.f;
-                    }
-                    x[c] = tc::pack_bf16(y, z);
+            for (int c = 0; c < kHalf; c += 2) {
+                float d0 = p[c] * (__uint_as_float(c < 32 ? v[c & 31] : u[c & 15]) - delta);
+                float d1 = p[c + 1] * (__uint_as_float(c < 32 ? v[(c + 1) & 31] : u[(c + 1) & 15]) - delta);
+                if (masked) {
+                    if (c >= seen) d0 = 0.f;
+                    if (c + 1 >= seen) d1 = 0.f;
                 }
-                ptx::tmem_st16(lanes + kTqDs + 32 * half + 16 * g, x);
+                (c < 32 ? x[(c >> 1) & 15] : y[(c >> 1) & 7]) = tc::pack_bf16(d0, d1);
             }
+            ptx::tmem_st16(lanes + kTqDs + kHalf / 2 * half, x);
+            tc::tmem_st8(lanes + kTqDs + kHalf / 2 * half + 16, y);
             ptx::tmem_wait_st();
             ptx::tc_fence_before();
             ptx::mbar_arrive(&mi.ds_full);
@@ -496,30 +505,22 @@ __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constan
         if (ok && n > 0) ok = tc::wait(&mi.done, 0, dead);
         ptx::tc_fence_after();
         if (ok) {
+            // each warpgroup writes half of the channels, through the place of Q and dO, which nothing reads any more
+            const uint32_t stage = base + warp * tc::RowStage<12>::kBytes;
             const int width = 64 * kc;
-            uint4 *out = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.dq) + (int64_t(pl.q0 + r) * a.H + h) * width);
-            for (int c = half; c < 2 * kc; c += 2) {  // 32-column groups, in turn
-                uint32_t v[32];
+            __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.dq) + (int64_t(pl.q0 + r - lane) * a.H + h) * width + half * (width / 2);
+            for (int c = 0; c < kc; ++c) {
+                uint32_t v[32] = {};
                 if (n > 0) {
-                    ptx::tmem_ld32(lanes + kTqDq + 32 * c, v);
+                    ptx::tmem_ld32(lanes + kTqDq + half * (width / 2) + 32 * c, v);
                     ptx::tmem_wait_ld();
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) v[e] = 0;
                 }
-                if (r < pl.lq) {
-#pragma unroll
-                    for (int e = 0; e < 32; e += 8) {
-                        const float f = a.scale;
-                        uint4 x;
-                        x.x = tc::pack_bf16(__uint_as_float(v[e]) * f, __uint_as_float(v[e + 1]) * f);
-                        x.y = tc::pack_bf16(__uint_as_float(v[e + 2]) * f, __uint_as_float(v[e + 3]) * f);
-                        x.z = tc::pack_bf16(__uint_as_float(v[e + 4]) * f, __uint_as_float(v[e + 5]) * f);
-                        x.w = tc::pack_bf16(__uint_as_float(v[e + 6]) * f, __uint_as_float(v[e + 7]) * f);
-                        out[4 * c + e / 8] = x;
-                    }
-                }
+                if (kc == 3) tc::put_bf16<12>(stage, lane, 4 * c, v, a.scale);
+                else tc::put_bf16<8>(stage, lane, 4 * c, v, a.scale);
             }
+            const int64_t row_bytes = int64_t(a.H) * width * 2;
+            if (kc == 3) tc::RowStage<12>::store(stage, lane, out, row_bytes, pl.lq - (r - lane));
+            else tc::RowStage<8>::store(stage, lane, out, row_bytes, pl.lq - (r - lane));
         }
     }
     ptx::tc_fence_before();
@@ -551,11 +552,10 @@ cudaError_t launch_mla_backward_tc(const MlaArgs &a, cudaStream_t st) {
               tc::rows_map(&qs.dO, a.dO, 128, a.H, a.Tq, dO_st, 128, 128) &&
               tc::rows_map(&kv.k, a.k, 128, a.H, a.Tk, a.k_st, a.k_sh, 128) &&
               tc::rows_map(&kv.v, a.v, 128, a.H, a.Tk, a.v_st, a.v_sh, 128) &&
-              (a.dr == 0 || tc::rope_map(&kv.kr, a.k_rope, a.Tk, a.kr_st, 128));
+              tc::rows_map(&qs.k, a.k, 128, a.H, a.Tk, a.k_st, a.k_sh, kKb) &&
+              tc::rows_map(&qs.v, a.v, 128, a.H, a.Tk, a.v_st, a.v_sh, kKb) &&
+              (a.dr == 0 || (tc::rope_map(&kv.kr, a.k_rope, a.Tk, a.kr_st, 128) && tc::rope_map(&qs.kr, a.k_rope, a.Tk, a.kr_st, kKb)));
     if (!ok) return cudaErrorInvalidValue;
-    qs.k = kv.k;
-    qs.v = kv.v;
-    qs.kr = kv.kr;
     const cudaError_t e = launch(dkv_tc_kernel, kv, count_tiles(a.cu_k_host, a.num_seqs, 128), kDkvSmem, a, st);
     if (e != cudaSuccess) return e;
     return launch(dq_tc_kernel, qs, count_tiles(a.cu_q_host, a.num_seqs, 128), kDqSmem, a, st);

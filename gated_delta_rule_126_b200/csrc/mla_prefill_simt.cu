@@ -248,16 +248,28 @@ template <typename T> __global__ void __launch_bounds__(kThreads) dq_kernel(cons
     }
 }
 
-// delta[h][t] = sum_c dO o and lse2[h][t] = lse log2(e), one warp per (token, head) of the sequences' rows.
-template <typename T> __global__ void delta_kernel(const MlaArgs a) {
-    const int64_t row = int64_t(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
+// delta[h][t] = sum_c dO o and lse2[h][t] = lse log2(e) of the sequences' rows.  16 lanes a (token, head), eight
+// channels a lane where a row's start and length allow 16-byte loads (V = 8 bf16 or 4 f32), else channel by
+// channel; bound by memory (2 d_v elements a row).
+template <typename T, int V> __global__ void delta_kernel(const MlaArgs a) {
+    const int64_t row = int64_t(blockIdx.x) * (blockDim.x >> 4) + (threadIdx.x >> 4);
     if (row >= a.Tq * a.H) return;
     const T *x = static_cast<const T *>(a.dO) + row * a.dv, *y = static_cast<const T *>(a.o) + row * a.dv;
     float s = 0.f;
-    for (int c = threadIdx.x & 31; c < a.dv; c += 32) s = fmaf(to_f32(x[c]), to_f32(y[c]), s);
+    for (int c = (threadIdx.x & 15) * V; c < a.dv; c += 16 * V) {
+        if constexpr (V == 1) {
+            s = fmaf(to_f32(x[c]), to_f32(y[c]), s);
+        } else {
+            const uint4 u = *reinterpret_cast<const uint4 *>(x + c), w = *reinterpret_cast<const uint4 *>(y + c);
+            const T *p = reinterpret_cast<const T *>(&u), *q = reinterpret_cast<const T *>(&w);
 #pragma unroll
-    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if ((threadIdx.x & 31) == 0) {
+            for (int e = 0; e < V; ++e) s = fmaf(to_f32(p[e]), to_f32(q[e]), s);
+        }
+    }
+    const unsigned lanes = 0xffffu << (threadIdx.x & 16);  // a row's lanes, which all reach this
+#pragma unroll
+    for (int o = 8; o; o >>= 1) s += __shfl_xor_sync(lanes, s, o);
+    if ((threadIdx.x & 15) == 0) {
         const int64_t at = row % a.H * a.Tq + row / a.H;
         a.delta[at] = s;
         a.lse2[at] = a.lse[row] * 1.4426950408889634f;
@@ -303,12 +315,20 @@ cudaError_t launch_mla_prefill_simt(const MlaArgs &a, cudaStream_t st) {
                                     : launch(prefill_kernel<__nv_bfloat16>, tiles, prefill_smem(a), a, st);
 }
 
-cudaError_t launch_mla_delta(const MlaArgs &a, cudaStream_t st) {
-    const int64_t blocks = (a.Tq * a.H + 7) / 8;
+namespace {
+template <typename T> cudaError_t delta(const MlaArgs &a, cudaStream_t st) {
+    constexpr int V = 16 / sizeof(T);
+    const int64_t blocks = (a.Tq * a.H + 15) / 16;
     if (blocks == 0) return cudaSuccess;
-    if (a.dtype == KDA_DTYPE_F32) delta_kernel<float><<<unsigned(blocks), 256, 0, st>>>(a);
-    else delta_kernel<__nv_bfloat16><<<unsigned(blocks), 256, 0, st>>>(a);
+    const bool vec = a.dv % V == 0 && (reinterpret_cast<uintptr_t>(a.dO) & 15) == 0 && (reinterpret_cast<uintptr_t>(a.o) & 15) == 0;
+    if (vec) delta_kernel<T, V><<<unsigned(blocks), 256, 0, st>>>(a);
+    else delta_kernel<T, 1><<<unsigned(blocks), 256, 0, st>>>(a);
     return cudaGetLastError();
+}
+}  // namespace
+
+cudaError_t launch_mla_delta(const MlaArgs &a, cudaStream_t st) {
+    return a.dtype == KDA_DTYPE_F32 ? delta<float>(a, st) : delta<__nv_bfloat16>(a, st);
 }
 
 cudaError_t launch_mla_dkr_reduce(const MlaArgs &a, cudaStream_t st) {

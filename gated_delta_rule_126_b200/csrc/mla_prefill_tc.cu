@@ -283,29 +283,19 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
         if (ok) {
             const float inv = sum == 0.f ? 0.f : 1.f / sum;
             const int64_t at = int64_t(q0 + r) * a.H + h;
-            uint4 *out = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.o) + at * 128);
+            // through this tile's Q, which nothing reads any more
+            const uint32_t stage = base + 3 * t * kSlotBytes + w * tc::RowStage<16>::kBytes;
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                uint32_t v[32];
+                uint32_t v[32] = {};
                 if (n[t]) {
                     ptx::tmem_ld32(oa + 32 * c, v);
                     ptx::tmem_wait_ld();
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) v[e] = 0;
                 }
-                if (r < lq) {
-#pragma unroll
-                    for (int e = 0; e < 32; e += 8) {
-                        uint4 x;
-                        x.x = tc::pack_bf16(__uint_as_float(v[e]) * inv, __uint_as_float(v[e + 1]) * inv);
-                        x.y = tc::pack_bf16(__uint_as_float(v[e + 2]) * inv, __uint_as_float(v[e + 3]) * inv);
-                        x.z = tc::pack_bf16(__uint_as_float(v[e + 4]) * inv, __uint_as_float(v[e + 5]) * inv);
-                        x.w = tc::pack_bf16(__uint_as_float(v[e + 6]) * inv, __uint_as_float(v[e + 7]) * inv);
-                        out[4 * c + e / 8] = x;
-                    }
-                }
+                tc::put_bf16<16>(stage, lane, 4 * c, v, inv);
             }
+            tc::RowStage<16>::store(stage, lane, static_cast<__nv_bfloat16 *>(a.o) + (at - int64_t(lane) * a.H) * 128,
+                                    int64_t(a.H) * 256, lq - (r - lane));
             if (a.lse && r < lq) a.lse[at] = sum == 0.f ? -INFINITY : top * a.scale + logf(sum);
         }
     }

@@ -111,6 +111,42 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return r;
 }
 
+// A warp's 32 rows of PIECES 16-byte pieces on their way from one row a thread to whole rows in memory (a store of one
+// piece a lane into 32 rows takes the memory pipe 32 turns): put() lays a row's pieces at `stage`, in rows one
+// piece longer so that neighbouring rows fall into different banks; store() writes the first `rows` rows.
+template <int PIECES> struct RowStage {
+    static constexpr uint32_t kPitch = PIECES * 16 + 16, kBytes = 32 * kPitch;
+    static __device__ __forceinline__ void put(uint32_t stage, int lane, int piece, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+        st_shared_v4(stage + lane * kPitch + piece * 16, a, b, c, d);
+    }
+    static __device__ __forceinline__ void store(uint32_t stage, int lane, void *out, int64_t row_bytes, int rows) {
+        __syncwarp();
+#pragma unroll 4
+        for (int x = lane; x < 32 * PIECES; x += 32) {
+            const int row = x / PIECES, piece = x % PIECES;
+            if (row >= rows) break;
+            uint4 v;
+            asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(stage + row * kPitch + piece * 16) : "memory");
+            *reinterpret_cast<uint4 *>(static_cast<char *>(out) + row * row_bytes + piece * 16) = v;
+        }
+        __syncwarp();
+    }
+};
+// 32 float32 values times f as four bf16 pieces from `piece` on.
+template <int PIECES>
+__device__ __forceinline__ void put_bf16(uint32_t stage, int lane, int piece, const uint32_t (&v)[32], float f) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        auto pair = [&](int i) { return pack_bf16(__uint_as_float(v[8 * e + i]) * f, __uint_as_float(v[8 * e + i + 1]) * f); };
+        RowStage<PIECES>::put(stage, lane, piece + e, pair(0), pair(2), pair(4), pair(6));
+    }
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t *v) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]), "r"(v[1]),
+                 "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
 // Tensor map of a bf16 tensor with 128-byte-swizzled boxes; false when it cannot be described.
 // dims and box: `rank` numbers, innermost first; strides: rank - 1 numbers, in elements.
 bool make_map(CUtensorMap *m, const void *base, int rank, const int64_t *dims, const int64_t *strides, const int *box);
