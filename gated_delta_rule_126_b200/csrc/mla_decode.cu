@@ -23,7 +23,7 @@ size_t simt_smem(int W) { return sizeof(float) * ((kRows + kKeys) * simt_row(W) 
 template <typename T>
 __global__ void __launch_bounds__(kThreads) decode_kernel(const MlaDecodeArgs a, const MlaDecodeShape shape) {
     extern __shared__ float sm[];
-    __shared__ int64_t buf[kThreads / 32 + 4];
+    __shared__ int64_t buf[kThreads / 32 + 4], place[kKeys];
     const int W = a.dc + a.dr, W4 = (W + 3) & ~3, ld = simt_row(W), R = a.n * a.H;
     float *Q = sm, *K = Q + kRows * ld, *P = K + kKeys * ld, *Keep = P + kKeys * kRows, *M = Keep + kRows, *L = M + kRows;
     const int tid = threadIdx.x, sr = tid >> 4, sk = tid & 15;
@@ -43,21 +43,42 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(const MlaDecodeArgs a,
     while (w.next(a, kKeys, run)) {
         const int b = w.b, len = w.len;
         __syncthreads();
-        load_tile<T, kThreads>(Q, ld, 0, static_cast<const T *>(a.q) + (int64_t(b) * R + r0) * W, W, W, kRows, rows);
+        load_tile<T, kThreads, kRows>(Q, ld, 0, static_cast<const T *>(a.q) + (int64_t(b) * R + r0) * W, W, W, rows);
         float m = -INFINITY, l = 0.f;  // of row sr, the same in its 16 threads
         float o[kRows][2] = {};        // columns tid and tid + 256
         for (int t = w.t0; t < w.t1; ++t) {
             const int j0 = t * kKeys;
             __syncthreads();
-            for (int i = tid; i < kKeys * W; i += kThreads) {
-                const int j = i / W, c = i - j * W, key = j0 + j;
-                float v = 0.f;
+            if (tid < kKeys) {  // the tile's cache rows; -1: behind the sequence or outside the pool
+                const int key = j0 + tid;
+                int64_t row = -1;
                 if (key < len) {
-                    const int page = a.page_table[int64_t(b) * a.max_pages + key / a.page_size];
-                    if (page >= 0 && page < a.num_pages)
-                        v = to_f32(static_cast<const T *>(a.cache)[(int64_t(page) * a.page_size + key % a.page_size) * W + c]);
+                    const int entry = key / a.page_size, page = a.page_table[int64_t(b) * a.max_pages + entry];
+                    if (page >= 0 && page < a.num_pages) row = int64_t(page) * a.page_size + (key - entry * a.page_size);
                 }
-                K[j * ld + c] = v;
+                place[tid] = row;
+            }
+            __syncthreads();
+            // 16 threads a row, its four elements a load where rows allow
+            const T *pool = static_cast<const T *>(a.cache);
+            if ((W & 3) == 0) {
+                for (int c = 4 * sk; c < W; c += 64) {
+                    float4 v[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int64_t at = place[sr + 16 * e];
+                        v[e] = at >= 0 ? load4(pool + at * W + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) *reinterpret_cast<float4 *>(K + (sr + 16 * e) * ld + c) = v[e];
+                }
+            } else {
+                for (int c = sk; c < W; c += 16)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int64_t at = place[sr + 16 * e];
+                        K[(sr + 16 * e) * ld + c] = at >= 0 ? to_f32(pool[at * W + c]) : 0.f;
+                    }
             }
             __syncthreads();
             float s[2] = {0.f, 0.f};
@@ -73,12 +94,7 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(const MlaDecodeArgs a,
             float top = m;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int key = j0 + sk + 16 * e;
-                bool seen = key < end && key < len;
-                if (seen) {
-                    const int page = a.page_table[int64_t(b) * a.max_pages + key / a.page_size];
-                    seen = page >= 0 && page < a.num_pages;
-                }
+                const bool seen = j0 + sk + 16 * e < end && place[sk + 16 * e] >= 0;
                 s[e] = seen ? s[e] * a.scale : -INFINITY;
                 top = fmaxf(top, s[e]);
             }

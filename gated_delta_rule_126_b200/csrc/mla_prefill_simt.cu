@@ -26,25 +26,25 @@ __device__ __forceinline__ Rows rows_of(const MlaArgs &a, int s) {
 template <typename T>
 __device__ __forceinline__ void load_q(float *Q, int ld, const MlaArgs &a, const Rows &w, int h, int i0) {
     const int d = a.dn + a.dr, n = min(kT, w.lq - i0);
-    load_tile<T, kThreads>(Q, ld, 0, static_cast<const T *>(a.q) + (w.q0 + i0) * a.q_st + h * a.q_sh, a.q_st, d, kT, n);
+    load_tile<T, kThreads, kT>(Q, ld, 0, static_cast<const T *>(a.q) + (w.q0 + i0) * a.q_st + h * a.q_sh, a.q_st, d, n);
 }
 template <typename T>
 __device__ __forceinline__ void load_k(float *K, int ld, const MlaArgs &a, const Rows &w, int h, int j0) {
     const int n = min(kT, w.lk - j0);
-    load_tile<T, kThreads>(K, ld, 0, static_cast<const T *>(a.k) + (w.k0 + j0) * a.k_st + h * a.k_sh, a.k_st, a.dn, kT, n);
+    load_tile<T, kThreads, kT>(K, ld, 0, static_cast<const T *>(a.k) + (w.k0 + j0) * a.k_st + h * a.k_sh, a.k_st, a.dn, n);
     if (a.dr)
-        load_tile<T, kThreads>(K, ld, a.dn, static_cast<const T *>(a.k_rope) + (w.k0 + j0) * a.kr_st, a.kr_st, a.dr, kT, n);
+        load_tile<T, kThreads, kT>(K, ld, a.dn, static_cast<const T *>(a.k_rope) + (w.k0 + j0) * a.kr_st, a.kr_st, a.dr, n);
 }
 template <typename T>
 __device__ __forceinline__ void load_v(float *V, int ld, const MlaArgs &a, const Rows &w, int h, int j0) {
     const int n = min(kT, w.lk - j0);
-    load_tile<T, kThreads>(V, ld, 0, static_cast<const T *>(a.v) + (w.k0 + j0) * a.v_st + h * a.v_sh, a.v_st, a.dv, kT, n);
+    load_tile<T, kThreads, kT>(V, ld, 0, static_cast<const T *>(a.v) + (w.k0 + j0) * a.v_st + h * a.v_sh, a.v_st, a.dv, n);
 }
 template <typename T>
 __device__ __forceinline__ void load_dO(float *D, int ld, const MlaArgs &a, const Rows &w, int h, int i0) {
     const int n = min(kT, w.lq - i0);
-    load_tile<T, kThreads>(D, ld, 0, static_cast<const T *>(a.dO) + (int64_t(w.q0 + i0) * a.H + h) * a.dv,
-                           int64_t(a.H) * a.dv, a.dv, kT, n);
+    load_tile<T, kThreads, kT>(D, ld, 0, static_cast<const T *>(a.dO) + (int64_t(w.q0 + i0) * a.H + h) * a.dv,
+                               int64_t(a.H) * a.dv, a.dv, n);
 }
 // Keys that query i may see end here (bottom-right causal).
 __device__ __forceinline__ int key_end(const MlaArgs &a, const Rows &w, int i) {

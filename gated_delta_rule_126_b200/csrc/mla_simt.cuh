@@ -57,13 +57,47 @@ __device__ bool find_tile(const int32_t *cu, int num_seqs, int tile, int64_t x, 
     return true;
 }
 
-// dst[r][at + c] = src[r * stride + c] for r < rows, c < width, as float32; rows from `valid` on are zero.
-template <typename T, int NT>
-__device__ __forceinline__ void load_tile(float *dst, int ld, int at, const T *src, int64_t stride, int width, int rows,
-                                          int valid) {
-    for (int i = threadIdx.x; i < rows * width; i += NT) {
-        const int r = i / width, c = i - r * width;
-        dst[r * ld + at + c] = r < valid ? to_f32(src[r * stride + c]) : 0.f;
+// Four elements at p (16 bytes of float32, 8 of bf16) as float32.
+template <typename T> __device__ __forceinline__ float4 load4(const T *p);
+template <> __device__ __forceinline__ float4 load4<float>(const float *p) { return *reinterpret_cast<const float4 *>(p); }
+template <> __device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16 *p) {
+    const uint2 w = *reinterpret_cast<const uint2 *>(p);
+    return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
+                       __uint_as_float(w.y & 0xffff0000u));
+}
+// Whether rows of this base, stride and width can be read four elements at a time.
+template <typename T> __device__ __forceinline__ bool by4(const T *p, int64_t stride, int width) {
+    return ((stride | width) & 3) == 0 && (reinterpret_cast<uintptr_t>(p) & (4 * sizeof(T) - 1)) == 0;
+}
+
+// dst[r][at + c] = src[r * stride + c] for r < ROWS, c < width, as float32; rows from `valid` on are zero.
+// 16 threads a row, all rows of a pass in flight together; four elements a load where the layout allows.
+template <typename T, int NT, int ROWS>
+__device__ __forceinline__ void load_tile(float *dst, int ld, int at, const T *src, int64_t stride, int width, int valid) {
+    constexpr int kPer = ROWS / (NT / 16);
+    const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+    if (by4(src, stride, width) && (at & 3) == 0) {
+        for (int c = 4 * tx; c < width; c += 64) {
+            float4 v[kPer];
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                const int r = ty + NT / 16 * i;
+                v[i] = r < valid ? load4(src + r * stride + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) *reinterpret_cast<float4 *>(dst + (ty + NT / 16 * i) * ld + at + c) = v[i];
+        }
+    } else {
+        for (int c = tx; c < width; c += 16) {
+            float v[kPer];
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                const int r = ty + NT / 16 * i;
+                v[i] = r < valid ? to_f32(src[r * stride + c]) : 0.f;
+            }
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) dst[(ty + NT / 16 * i) * ld + at + c] = v[i];
+        }
     }
 }
 // Zeroes columns [from, to) of every row.
