@@ -1,6 +1,6 @@
 // mla_prefill and mla_backward on the CUDA cores, in float32: every type, head size and
-// stride the calls take.  64 x 64 tiles of scores, 256 threads with 4 x 4 scores each; the
-// softmax is kept online (running maximum and sum), so scores never leave the SM.  The
+// stride the calls take.  Tiles of scores with 64 streamed rows and 64 or 32 owned ones (the rows whose
+// output a block makes), 256 threads with 4 x 4 or 4 x 2 scores each; the softmax is kept online (running maximum and sum), so scores never leave the SM.  The
 // backward pass recomputes the scores from lse in two kernels, one per key tile (dk, dv)
 // and one per query tile (dq), so that every sum has one owner and no atomics.
 // Bound by the float32 FMA pipes.
@@ -12,7 +12,7 @@
 namespace kda {
 namespace {
 
-constexpr int kT = 64;         // rows of queries and of keys per tile
+constexpr int kT = 64;  // streamed rows of a tile
 constexpr int kThreads = 256;  // 16 x 16
 constexpr int kLdP = kT + 4;
 
@@ -23,27 +23,27 @@ __device__ __forceinline__ Rows rows_of(const MlaArgs &a, int s) {
     return Rows{a.cu_q[s], a.cu_q[s + 1] - a.cu_q[s], a.cu_k[s], a.cu_k[s + 1] - a.cu_k[s]};
 }
 
-template <typename T>
+template <typename T, int ROWS>
 __device__ __forceinline__ void load_q(float *Q, int ld, const MlaArgs &a, const Rows &w, int h, int i0) {
-    const int d = a.dn + a.dr, n = min(kT, w.lq - i0);
-    load_tile<T, kThreads, kT>(Q, ld, 0, static_cast<const T *>(a.q) + (w.q0 + i0) * a.q_st + h * a.q_sh, a.q_st, d, n);
+    const int d = a.dn + a.dr, n = min(ROWS, w.lq - i0);
+    load_tile<T, kThreads, ROWS>(Q, ld, 0, static_cast<const T *>(a.q) + (w.q0 + i0) * a.q_st + h * a.q_sh, a.q_st, d, n);
 }
-template <typename T>
+template <typename T, int ROWS>
 __device__ __forceinline__ void load_k(float *K, int ld, const MlaArgs &a, const Rows &w, int h, int j0) {
-    const int n = min(kT, w.lk - j0);
-    load_tile<T, kThreads, kT>(K, ld, 0, static_cast<const T *>(a.k) + (w.k0 + j0) * a.k_st + h * a.k_sh, a.k_st, a.dn, n);
+    const int n = min(ROWS, w.lk - j0);
+    load_tile<T, kThreads, ROWS>(K, ld, 0, static_cast<const T *>(a.k) + (w.k0 + j0) * a.k_st + h * a.k_sh, a.k_st, a.dn, n);
     if (a.dr)
-        load_tile<T, kThreads, kT>(K, ld, a.dn, static_cast<const T *>(a.k_rope) + (w.k0 + j0) * a.kr_st, a.kr_st, a.dr, n);
+        load_tile<T, kThreads, ROWS>(K, ld, a.dn, static_cast<const T *>(a.k_rope) + (w.k0 + j0) * a.kr_st, a.kr_st, a.dr, n);
 }
-template <typename T>
+template <typename T, int ROWS>
 __device__ __forceinline__ void load_v(float *V, int ld, const MlaArgs &a, const Rows &w, int h, int j0) {
-    const int n = min(kT, w.lk - j0);
-    load_tile<T, kThreads, kT>(V, ld, 0, static_cast<const T *>(a.v) + (w.k0 + j0) * a.v_st + h * a.v_sh, a.v_st, a.dv, n);
+    const int n = min(ROWS, w.lk - j0);
+    load_tile<T, kThreads, ROWS>(V, ld, 0, static_cast<const T *>(a.v) + (w.k0 + j0) * a.v_st + h * a.v_sh, a.v_st, a.dv, n);
 }
-template <typename T>
+template <typename T, int ROWS>
 __device__ __forceinline__ void load_dO(float *D, int ld, const MlaArgs &a, const Rows &w, int h, int i0) {
-    const int n = min(kT, w.lq - i0);
-    load_tile<T, kThreads, kT>(D, ld, 0, static_cast<const T *>(a.dO) + (int64_t(w.q0 + i0) * a.H + h) * a.dv,
+    const int n = min(ROWS, w.lq - i0);
+    load_tile<T, kThreads, ROWS>(D, ld, 0, static_cast<const T *>(a.dO) + (int64_t(w.q0 + i0) * a.H + h) * a.dv,
                                int64_t(a.H) * a.dv, a.dv, n);
 }
 // Keys that query i may see end here (bottom-right causal).
@@ -61,33 +61,35 @@ __device__ __forceinline__ float half_warp_sum(float x) {
     return x;
 }
 
-template <typename T> __global__ void __launch_bounds__(kThreads) prefill_kernel(const MlaArgs a) {
+// A block owns 16 I queries of a head.
+template <typename T, int I> __global__ void __launch_bounds__(kThreads, I == 2 ? 2 : 1) prefill_kernel(const MlaArgs a) {
     extern __shared__ float sm[];
     __shared__ int64_t buf[kThreads / 32 + 2];
+    constexpr int kOwn = 16 * I;
     const int d = a.dn + a.dr, d4 = (d + 3) & ~3, ldd = simt_row(d), ldv = simt_row(a.dv), h = blockIdx.y;
-    float *Q = sm, *K = Q + kT * ldd, *V = K + kT * ldd, *P = V + kT * ldv;
+    float *Q = sm, *K = Q + kOwn * ldd, *V = K + kT * ldd, *P = V + kT * ldv;
     int seq, tile;
-    if (!find_tile<kThreads>(a.cu_q, a.num_seqs, kT, gridDim.x - 1 - blockIdx.x, buf, &seq, &tile)) return;
+    if (!find_tile<kThreads>(a.cu_q, a.num_seqs, kOwn, gridDim.x - 1 - blockIdx.x, buf, &seq, &tile)) return;
     const Rows w = rows_of(a, seq);
-    const int i0 = tile * kT, tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
-    zero_columns<kThreads>(Q, ldd, d, d4, kT);
+    const int i0 = tile * kOwn, tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+    zero_columns<kThreads>(Q, ldd, d, d4, kOwn);
     zero_columns<kThreads>(K, ldd, d, d4, kT);
     zero_columns<kThreads>(V, ldv, a.dv, (a.dv + 3) & ~3, kT);
-    load_q<T>(Q, ldd, a, w, h, i0);
-    float m[4], l[4], o[4][8] = {};
+    load_q<T, kOwn>(Q, ldd, a, w, h, i0);
+    float m[I], l[I], o[I][8] = {};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) m[i] = -INFINITY, l[i] = 0.f;
-    const int last = key_end(a, w, min(i0 + kT, w.lq) - 1);
+    for (int i = 0; i < I; ++i) m[i] = -INFINITY, l[i] = 0.f;
+    const int last = key_end(a, w, min(i0 + kOwn, w.lq) - 1);
     for (int j0 = 0; j0 < last; j0 += kT) {
         __syncthreads();
-        load_k<T>(K, ldd, a, w, h, j0);
-        load_v<T>(V, ldv, a, w, h, j0);
+        load_k<T, kT>(K, ldd, a, w, h, j0);
+        load_v<T, kT>(V, ldv, a, w, h, j0);
         __syncthreads();
-        float s[4][4] = {};
+        float s[I][4] = {};
         tile_dot(s, Q, ldd, K, ldd, d4, ty, tx);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int end = key_end(a, w, i0 + 4 * ty + i) - j0;
+        for (int i = 0; i < I; ++i) {
+            const int end = key_end(a, w, i0 + I * ty + i) - j0;
             float top = -INFINITY;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -101,7 +103,7 @@ template <typename T> __global__ void __launch_bounds__(kThreads) prefill_kernel
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const float p = expf(s[i][j] - base);
-                P[(4 * ty + i) * kLdP + tx + 16 * j] = p;
+                P[(I * ty + i) * kLdP + tx + 16 * j] = p;
                 sum += p;
             }
             l[i] = l[i] * keep + half_warp_sum(sum);
@@ -110,11 +112,11 @@ template <typename T> __global__ void __launch_bounds__(kThreads) prefill_kernel
             for (int c = 0; c < 8; ++c) o[i][c] *= keep;
         }
         __syncwarp();  // a row of P is written and read by the same half warp
-        tile_apply<2>(o, P, kLdP, V, ldv, a.dv, ty, tx);
+        tile_apply<I, 2>(o, P, kLdP, V, ldv, a.dv, ty, tx);
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = i0 + 4 * ty + i;
+    for (int i = 0; i < I; ++i) {
+        const int r = i0 + I * ty + i;
         if (r >= w.lq) continue;
         const float inv = l[i] > 0.f ? 1.f / l[i] : 0.f;
         T *out = static_cast<T *>(a.o) + (int64_t(w.q0 + r) * a.H + h) * a.dv;
@@ -128,22 +130,23 @@ template <typename T> __global__ void __launch_bounds__(kThreads) prefill_kernel
     }
 }
 
-// P and dS of one tile, from the recomputed scores: p = exp(s - lse), ds = p (dp - delta) scale.
-template <typename T>
+// P and dS of one tile (queries I ty + i, keys tx + 16 j), from the recomputed scores: p = exp(s - lse),
+// ds = p (dp - delta) scale.
+template <int I, int J>
 __device__ __forceinline__ void tile_grads(const MlaArgs &a, const Rows &w, int h, int i0, int j0, const float *Q,
                                            const float *K, const float *V, const float *D, int ldd, int ldv, int d4,
-                                           int dv4, int ty, int tx, float (&p)[4][4], float (&ds)[4][4]) {
-    float s[4][4] = {}, dp[4][4] = {};
+                                           int dv4, int ty, int tx, float (&p)[I][J], float (&ds)[I][J]) {
+    float s[I][J] = {}, dp[I][J] = {};
     tile_dot(s, Q, ldd, K, ldd, d4, ty, tx);
     tile_dot(dp, D, ldv, V, ldv, dv4, ty, tx);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = i0 + 4 * ty + i;
+    for (int i = 0; i < I; ++i) {
+        const int r = i0 + I * ty + i;
         const bool in = r < w.lq;
         const int end = in ? key_end(a, w, r) - j0 : 0;
         const float lse = in ? a.lse[int64_t(w.q0 + r) * a.H + h] : 0.f, delta = in ? a.delta[int64_t(h) * a.Tq + w.q0 + r] : 0.f;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < J; ++j) {
             const bool seen = tx + 16 * j < end;
             p[i][j] = seen ? expf(s[i][j] * a.scale - lse) : 0.f;
             ds[i][j] = seen ? p[i][j] * (dp[i][j] - delta) * a.scale : 0.f;
@@ -151,46 +154,48 @@ __device__ __forceinline__ void tile_grads(const MlaArgs &a, const Rows &w, int 
     }
 }
 
-template <typename T> __global__ void __launch_bounds__(kThreads) dkv_kernel(const MlaArgs a) {
+// A block owns 16 J keys of a head.
+template <typename T, int J> __global__ void __launch_bounds__(kThreads, J == 2 ? 2 : 1) dkv_kernel(const MlaArgs a) {
     extern __shared__ float sm[];
     __shared__ int64_t buf[kThreads / 32 + 2];
+    constexpr int kOwn = 16 * J;
     const int d = a.dn + a.dr, d4 = (d + 3) & ~3, dv4 = (a.dv + 3) & ~3, h = blockIdx.y;
     const int ldd = simt_row(d), ldv = simt_row(a.dv);
-    float *Q = sm, *K = Q + kT * ldd, *V = K + kT * ldd, *D = V + kT * ldv, *Pt = D + kT * ldv, *St = Pt + kT * kLdP;
+    float *Q = sm, *K = Q + kT * ldd, *V = K + kOwn * ldd, *D = V + kOwn * ldv, *Pt = D + kT * ldv, *St = Pt + kOwn * kLdP;
     int seq, tile;
-    if (!find_tile<kThreads>(a.cu_k, a.num_seqs, kT, blockIdx.x, buf, &seq, &tile)) return;
+    if (!find_tile<kThreads>(a.cu_k, a.num_seqs, kOwn, blockIdx.x, buf, &seq, &tile)) return;
     const Rows w = rows_of(a, seq);
-    const int j0 = tile * kT, tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+    const int j0 = tile * kOwn, tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
     zero_columns<kThreads>(Q, ldd, d, d4, kT);
-    zero_columns<kThreads>(K, ldd, d, d4, kT);
-    zero_columns<kThreads>(V, ldv, a.dv, dv4, kT);
+    zero_columns<kThreads>(K, ldd, d, d4, kOwn);
+    zero_columns<kThreads>(V, ldv, a.dv, dv4, kOwn);
     zero_columns<kThreads>(D, ldv, a.dv, dv4, kT);
-    load_k<T>(K, ldd, a, w, h, j0);
-    load_v<T>(V, ldv, a, w, h, j0);
-    float dk[4][12] = {}, dv[4][8] = {};
+    load_k<T, kOwn>(K, ldd, a, w, h, j0);
+    load_v<T, kOwn>(V, ldv, a, w, h, j0);
+    float dk[J][12] = {}, dv[J][8] = {};
     // the first query that sees key j0
     const int first = a.causal ? max(0, j0 - (w.lk - w.lq)) / kT * kT : 0;
     for (int i0 = first; i0 < w.lq; i0 += kT) {
         __syncthreads();
-        load_q<T>(Q, ldd, a, w, h, i0);
-        load_dO<T>(D, ldv, a, w, h, i0);
+        load_q<T, kT>(Q, ldd, a, w, h, i0);
+        load_dO<T, kT>(D, ldv, a, w, h, i0);
         __syncthreads();
-        float p[4][4], ds[4][4];
-        tile_grads<T>(a, w, h, i0, j0, Q, K, V, D, ldd, ldv, d4, dv4, ty, tx, p, ds);
+        float p[4][J], ds[4][J];
+        tile_grads(a, w, h, i0, j0, Q, K, V, D, ldd, ldv, d4, dv4, ty, tx, p, ds);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < J; ++j) {
                 Pt[(tx + 16 * j) * kLdP + 4 * ty + i] = p[i][j];
                 St[(tx + 16 * j) * kLdP + 4 * ty + i] = ds[i][j];
             }
         __syncthreads();
-        tile_apply<2>(dv, Pt, kLdP, D, ldv, a.dv, ty, tx);
-        tile_apply<3>(dk, St, kLdP, Q, ldd, d, ty, tx);
+        tile_apply<J, 2>(dv, Pt, kLdP, D, ldv, a.dv, ty, tx);
+        tile_apply<J, 3>(dk, St, kLdP, Q, ldd, d, ty, tx);
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = j0 + 4 * ty + i;
+    for (int i = 0; i < J; ++i) {
+        const int r = j0 + J * ty + i;
         if (r >= w.lk) continue;
         const int64_t at = int64_t(w.k0 + r) * a.H + h;
 #pragma unroll
@@ -203,41 +208,43 @@ template <typename T> __global__ void __launch_bounds__(kThreads) dkv_kernel(con
     }
 }
 
-template <typename T> __global__ void __launch_bounds__(kThreads) dq_kernel(const MlaArgs a) {
+// A block owns 16 I queries of a head.
+template <typename T, int I> __global__ void __launch_bounds__(kThreads, I == 2 ? 2 : 1) dq_kernel(const MlaArgs a) {
     extern __shared__ float sm[];
     __shared__ int64_t buf[kThreads / 32 + 2];
+    constexpr int kOwn = 16 * I;
     const int d = a.dn + a.dr, d4 = (d + 3) & ~3, dv4 = (a.dv + 3) & ~3, h = blockIdx.y;
     const int ldd = simt_row(d), ldv = simt_row(a.dv);
-    float *Q = sm, *K = Q + kT * ldd, *V = K + kT * ldd, *D = V + kT * ldv, *S = D + kT * ldv;
+    float *Q = sm, *K = Q + kOwn * ldd, *V = K + kT * ldd, *D = V + kT * ldv, *S = D + kOwn * ldv;
     int seq, tile;
-    if (!find_tile<kThreads>(a.cu_q, a.num_seqs, kT, gridDim.x - 1 - blockIdx.x, buf, &seq, &tile)) return;
+    if (!find_tile<kThreads>(a.cu_q, a.num_seqs, kOwn, gridDim.x - 1 - blockIdx.x, buf, &seq, &tile)) return;
     const Rows w = rows_of(a, seq);
-    const int i0 = tile * kT, tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
-    zero_columns<kThreads>(Q, ldd, d, d4, kT);
+    const int i0 = tile * kOwn, tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+    zero_columns<kThreads>(Q, ldd, d, d4, kOwn);
     zero_columns<kThreads>(K, ldd, d, d4, kT);
     zero_columns<kThreads>(V, ldv, a.dv, dv4, kT);
-    zero_columns<kThreads>(D, ldv, a.dv, dv4, kT);
-    load_q<T>(Q, ldd, a, w, h, i0);
-    load_dO<T>(D, ldv, a, w, h, i0);
-    float dq[4][12] = {};
-    const int last = key_end(a, w, min(i0 + kT, w.lq) - 1);
+    zero_columns<kThreads>(D, ldv, a.dv, dv4, kOwn);
+    load_q<T, kOwn>(Q, ldd, a, w, h, i0);
+    load_dO<T, kOwn>(D, ldv, a, w, h, i0);
+    float dq[I][12] = {};
+    const int last = key_end(a, w, min(i0 + kOwn, w.lq) - 1);
     for (int j0 = 0; j0 < last; j0 += kT) {
         __syncthreads();
-        load_k<T>(K, ldd, a, w, h, j0);
-        load_v<T>(V, ldv, a, w, h, j0);
+        load_k<T, kT>(K, ldd, a, w, h, j0);
+        load_v<T, kT>(V, ldv, a, w, h, j0);
         __syncthreads();
-        float p[4][4], ds[4][4];
-        tile_grads<T>(a, w, h, i0, j0, Q, K, V, D, ldd, ldv, d4, dv4, ty, tx, p, ds);
+        float p[I][4], ds[I][4];
+        tile_grads(a, w, h, i0, j0, Q, K, V, D, ldd, ldv, d4, dv4, ty, tx, p, ds);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < I; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) S[(4 * ty + i) * kLdP + tx + 16 * j] = ds[i][j];
+            for (int j = 0; j < 4; ++j) S[(I * ty + i) * kLdP + tx + 16 * j] = ds[i][j];
         __syncwarp();
-        tile_apply<3>(dq, S, kLdP, K, ldd, d, ty, tx);
+        tile_apply<I, 3>(dq, S, kLdP, K, ldd, d, ty, tx);
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = i0 + 4 * ty + i;
+    for (int i = 0; i < I; ++i) {
+        const int r = i0 + I * ty + i;
         if (r >= w.lq) continue;
         T *out = static_cast<T *>(a.dq) + (int64_t(w.q0 + r) * a.H + h) * d;
 #pragma unroll
@@ -285,13 +292,13 @@ template <typename T> __global__ void dkr_kernel(const MlaArgs a) {
     static_cast<T *>(a.dk_rope)[i] = from_f32<T>(s);
 }
 
-size_t prefill_smem(const MlaArgs &a) {
-    return sizeof(float) * kT * (2 * simt_row(a.dn + a.dr) + simt_row(a.dv) + kLdP);
+// Shared memory of a kernel that owns `own` rows (floats): tiles of d and of d_v channels, own and streamed rows, and P.
+size_t prefill_smem(const MlaArgs &a, int own) {
+    return sizeof(float) * ((own + kT) * simt_row(a.dn + a.dr) + kT * simt_row(a.dv) + own * kLdP);
 }
-size_t dq_smem(const MlaArgs &a) {
-    return sizeof(float) * kT * (2 * simt_row(a.dn + a.dr) + 2 * simt_row(a.dv) + kLdP);
+size_t grad_smem(const MlaArgs &a, int own, int tiles) {
+    return sizeof(float) * ((own + kT) * (simt_row(a.dn + a.dr) + simt_row(a.dv)) + tiles * own * kLdP);
 }
-size_t dkv_smem(const MlaArgs &a) { return dq_smem(a) + sizeof(float) * kT * kLdP; }
 
 template <typename K> cudaError_t launch(K *kernel, int64_t tiles, size_t smem, const MlaArgs &a, cudaStream_t st) {
     if (tiles == 0) return cudaSuccess;
@@ -301,18 +308,34 @@ template <typename K> cudaError_t launch(K *kernel, int64_t tiles, size_t smem, 
     return cudaGetLastError();
 }
 
+// 64 owned rows a block, or 32 where blocks of 64 would leave a third of the SMs idle: there the longest block's chain of
+// tiles is the call's time, and smaller tiles shorten it.  One float32 sequence of 1024 tokens, d = 192 and 128, forward
+// and backward: with 6 heads (96 blocks of 64) 163 and 521 us in tiles of 32, 185 and 627 in tiles of 64;
+// with 8 heads (128 blocks) 213 and 681 against 214 and 626.
+bool small_tiles(const int32_t *cu, const MlaArgs &a) { return 3 * count_tiles(cu, a.num_seqs, 64) * a.H < 2 * device_sm_count(); }
+
+template <typename T> cudaError_t prefill(const MlaArgs &a, cudaStream_t st) {
+    if (small_tiles(a.cu_q_host, a))
+        return launch(prefill_kernel<T, 2>, count_tiles(a.cu_q_host, a.num_seqs, 32), prefill_smem(a, 32), a, st);
+    return launch(prefill_kernel<T, 4>, count_tiles(a.cu_q_host, a.num_seqs, 64), prefill_smem(a, 64), a, st);
+}
+
 template <typename T> cudaError_t backward(const MlaArgs &a, cudaStream_t st) {
-    cudaError_t e = launch(dkv_kernel<T>, count_tiles(a.cu_k_host, a.num_seqs, kT), dkv_smem(a), a, st);
-    if (e == cudaSuccess) e = launch(dq_kernel<T>, count_tiles(a.cu_q_host, a.num_seqs, kT), dq_smem(a), a, st);
-    return e;
+    cudaError_t e;
+    if (small_tiles(a.cu_k_host, a))
+        e = launch(dkv_kernel<T, 2>, count_tiles(a.cu_k_host, a.num_seqs, 32), grad_smem(a, 32, 2), a, st);
+    else
+        e = launch(dkv_kernel<T, 4>, count_tiles(a.cu_k_host, a.num_seqs, 64), grad_smem(a, 64, 2), a, st);
+    if (e != cudaSuccess) return e;
+    if (small_tiles(a.cu_q_host, a))
+        return launch(dq_kernel<T, 2>, count_tiles(a.cu_q_host, a.num_seqs, 32), grad_smem(a, 32, 1), a, st);
+    return launch(dq_kernel<T, 4>, count_tiles(a.cu_q_host, a.num_seqs, 64), grad_smem(a, 64, 1), a, st);
 }
 
 }  // namespace
 
 cudaError_t launch_mla_prefill_simt(const MlaArgs &a, cudaStream_t st) {
-    const int64_t tiles = count_tiles(a.cu_q_host, a.num_seqs, kT);
-    return a.dtype == KDA_DTYPE_F32 ? launch(prefill_kernel<float>, tiles, prefill_smem(a), a, st)
-                                    : launch(prefill_kernel<__nv_bfloat16>, tiles, prefill_smem(a), a, st);
+    return a.dtype == KDA_DTYPE_F32 ? prefill<float>(a, st) : prefill<__nv_bfloat16>(a, st);
 }
 
 namespace {

@@ -106,19 +106,21 @@ template <int NT> __device__ __forceinline__ void zero_columns(float *dst, int l
     for (int i = threadIdx.x; i < rows * w; i += NT) dst[(i / w) * ld + from + i % w] = 0.f;
 }
 
-// acc[i][j] += sum_c A[4 ty + i][c] * B[tx + 16 j][c] over c < d4 (a multiple of 4).
-__device__ __forceinline__ void tile_dot(float (&acc)[4][4], const float *A, int lda, const float *B, int ldb, int d4,
+// acc[i][j] += sum_c A[I ty + i][c] * B[tx + 16 j][c] over c < d4 (a multiple of 4).
+template <int I, int J>
+__device__ __forceinline__ void tile_dot(float (&acc)[I][J], const float *A, int lda, const float *B, int ldb, int d4,
                                          int ty, int tx) {
+#pragma unroll 4
     for (int c = 0; c < d4; c += 4) {
-        float4 x[4], y[4];
+        float4 x[I], y[J];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const float4 *>(A + (4 * ty + i) * lda + c);
+        for (int i = 0; i < I; ++i) x[i] = *reinterpret_cast<const float4 *>(A + (I * ty + i) * lda + c);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) y[j] = *reinterpret_cast<const float4 *>(B + (tx + 16 * j) * ldb + c);
+        for (int j = 0; j < J; ++j) y[j] = *reinterpret_cast<const float4 *>(B + (tx + 16 * j) * ldb + c);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < I; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < J; ++j) {
                 acc[i][j] = fmaf(x[i].x, y[j].x, acc[i][j]);
                 acc[i][j] = fmaf(x[i].y, y[j].y, acc[i][j]);
                 acc[i][j] = fmaf(x[i].z, y[j].z, acc[i][j]);
@@ -127,31 +129,42 @@ __device__ __forceinline__ void tile_dot(float (&acc)[4][4], const float *A, int
     }
 }
 
-// acc[i][4 j + e] += sum_r P[4 ty + i][r] * B[r][64 j + 4 tx + e] over r < 64, for the j with 64 j + 4 tx < width.
-template <int J>
-__device__ __forceinline__ void tile_apply(float (&acc)[4][4 * J], const float *P, int ldp, const float *B, int ldb,
-                                           int width, int ty, int tx) {
+// acc[i][4 j + e] += sum_r P[I ty + i][r] * B[r][64 j + 4 tx + e] over r < 64, j < N.
+template <int N, int I, int C>
+__device__ __forceinline__ void tile_apply_n(float (&acc)[I][C], const float *P, int ldp, const float *B, int ldb, int ty, int tx) {
+#pragma unroll 2
     for (int r = 0; r < 64; r += 4) {
-        float4 p[4];
+        float4 p[I], b[4][N];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) p[i] = *reinterpret_cast<const float4 *>(P + (4 * ty + i) * ldp + r);
+        for (int i = 0; i < I; ++i) p[i] = *reinterpret_cast<const float4 *>(P + (I * ty + i) * ldp + r);
 #pragma unroll
         for (int e = 0; e < 4; ++e)
 #pragma unroll
-            for (int j = 0; j < J; ++j) {
-                if (64 * j + 4 * tx < width) {
-                    const float4 b = *reinterpret_cast<const float4 *>(B + (r + e) * ldb + 64 * j + 4 * tx);
+            for (int j = 0; j < N; ++j) b[e][j] = *reinterpret_cast<const float4 *>(B + (r + e) * ldb + 64 * j + 4 * tx);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float w = e == 0 ? p[i].x : e == 1 ? p[i].y : e == 2 ? p[i].z : p[i].w;
-                        acc[i][4 * j + 0] = fmaf(w, b.x, acc[i][4 * j + 0]);
-                        acc[i][4 * j + 1] = fmaf(w, b.y, acc[i][4 * j + 1]);
-                        acc[i][4 * j + 2] = fmaf(w, b.z, acc[i][4 * j + 2]);
-                        acc[i][4 * j + 3] = fmaf(w, b.w, acc[i][4 * j + 3]);
-                    }
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+#pragma unroll
+                for (int i = 0; i < I; ++i) {
+                    const float w = e == 0 ? p[i].x : e == 1 ? p[i].y : e == 2 ? p[i].z : p[i].w;
+                    acc[i][4 * j + 0] = fmaf(w, b[e][j].x, acc[i][4 * j + 0]);
+                    acc[i][4 * j + 1] = fmaf(w, b[e][j].y, acc[i][4 * j + 1]);
+                    acc[i][4 * j + 2] = fmaf(w, b[e][j].z, acc[i][4 * j + 2]);
+                    acc[i][4 * j + 3] = fmaf(w, b[e][j].w, acc[i][4 * j + 3]);
                 }
-            }
     }
+}
+
+// The same for the j with 64 j < width.  Threads whose columns lie behind `width` read what follows a row (the
+// buffers behind B are larger than a row) and make sums that nobody stores: a test inside the loops keeps
+// their loads from running ahead (16,500 cycles a 32 x 64 tile of 80 channels with one, 4,700 without).
+template <int I, int J>
+__device__ __forceinline__ void tile_apply(float (&acc)[I][4 * J], const float *P, int ldp, const float *B, int ldb,
+                                           int width, int ty, int tx) {
+    if (width <= 64) tile_apply_n<1>(acc, P, ldp, B, ldb, ty, tx);
+    else if (width <= 128 || J == 2) tile_apply_n<2>(acc, P, ldp, B, ldb, ty, tx);
+    else tile_apply_n<J>(acc, P, ldp, B, ldb, ty, tx);
 }
 
 }  // namespace kda

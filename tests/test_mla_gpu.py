@@ -161,6 +161,7 @@ PACKED = [  # q_lens, k_lens, H, dn, dr, dv
     ([66], [66], 2, 33, 7, 65),
     ([10, 100], [10, 100], 2, 64, 0, 64),
     ([20], [30], 1, 1, 1, 1),
+    ([150, 70], [150, 190], 34, 24, 8, 20),   # enough blocks for the larger tiles of the CUDA cores
 ]
 
 
