@@ -6,9 +6,10 @@
 // dkv_tc_kernel: a block owns 128 keys of one head and streams the queries in tiles of 64.
 //   S^T = K Q^T, dP^T = V dO^T  [128 x 64];  dV += P^T dO, dK += dS^T Q, with P^T and dS^T in TMEM
 //   as the left operands; Q and dO tiles serve as [q x d] K-major and as MN-major operand alike.
-//   TMEM: S^T twice 64 columns, dP^T 64, dV 128, dK 192: all 512.
+//   TMEM: S^T twice 64 columns, dP^T 64, dV 128, dK 192: all 512; P^T and dS^T lie over their S^T, so that the next
+//   tile's dP^T is formed while this one's dS^T is.
 // dq_tc_kernel: a block owns 128 queries of one head and streams the keys in blocks of 96.
-//   S = Q K^T, dP = dO V^T  [128 x 96];  dQ += dS K, dS in TMEM.  TMEM: S 96, dP 96, dQ 192, dS 48.
+//   S = Q K^T, dP = dO V^T  [128 x 96];  dQ += dS K, dS in TMEM.  TMEM: S 96, dP 96, dQ 192, dS twice 48.
 // P = exp2(scale log2(e) S - lse2) and dS = P (dP - delta) are rounded to bf16 for their products; the
 // factor `scale` of dq and dk is applied to the float32 sums at the end.
 // Bound by the tensor cores.  Warps 0-7: elementwise work and output, two warpgroups with half of the columns each;
@@ -49,7 +50,7 @@ constexpr uint32_t kDkvSmem = kOffMisc + 4096 + 1024;
 constexpr uint32_t kTmDp = 128, kTmDv = 192, kTmDk = 320;
 
 struct DkvMisc {
-    uint64_t full[kStages], empty[kStages], k_full, v_full, s_full[2], dp_full, p_full, ds_full, done;
+    uint64_t full[kStages], empty[kStages], k_full, v_full, s_full[2], dp_full, dp_read, p_full, ds_full, done;
     int64_t find[kThreads / 32 + 2];
     uint32_t tmem, dead;
     alignas(16) float lse2[kStages][kQt], delta[kStages][kQt];
@@ -67,12 +68,13 @@ __global__ void __launch_bounds__(kThreads, 1) dkv_tc_kernel(const __grid_consta
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int h = blockIdx.x % a.H, kc = a.dr ? 3 : 2;
     if (tid == 0) {
-        for (int i = 0; i < kStages; ++i) ptx::mbar_init(&mi.full[i], 1), ptx::mbar_init(&mi.empty[i], 1);
+        for (int i = 0; i < kStages; ++i) ptx::mbar_init(&mi.full[i], 2), ptx::mbar_init(&mi.empty[i], 1);  // full: loads, statistics
         ptx::mbar_init(&mi.k_full, 1);
         ptx::mbar_init(&mi.v_full, 1);
         ptx::mbar_init(&mi.s_full[0], 1);
         ptx::mbar_init(&mi.s_full[1], 1);
         ptx::mbar_init(&mi.dp_full, 1);
+        ptx::mbar_init(&mi.dp_read, 256);
         ptx::mbar_init(&mi.p_full, 256);
         ptx::mbar_init(&mi.ds_full, 256);
         ptx::mbar_init(&mi.done, 1);
@@ -104,16 +106,21 @@ __global__ void __launch_bounds__(kThreads, 1) dkv_tc_kernel(const __grid_consta
             }
             bool ok = true;
             int i = 0;
+            // lse2 and delta of a tile: two queries a lane, read a tile ahead
+            float lse2[2], delta[2];
+            auto stats = [&](int tile_q) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int q = tile_q * kQt + lane + 32 * e;
+                    const int64_t at = int64_t(h) * a.Tq + pl.q0 + q;
+                    lse2[e] = q < pl.lq ? a.lse2[at] : 0.f;
+                    delta[e] = q < pl.lq ? a.delta[at] : 0.f;
+                }
+            };
+            stats(first);
             for (; i < n; ++i) {
                 const int s = i % kStages, i0 = (first + i) * kQt;
                 if (i >= kStages && !(ok = tc::wait(&mi.empty[s], (i / kStages - 1) & 1, dead))) break;
-                for (int e = lane; e < kQt; e += 32) {
-                    const bool in = i0 + e < pl.lq;
-                    const int64_t at = int64_t(h) * a.Tq + pl.q0 + i0 + e;
-                    mi.lse2[s][e] = in ? a.lse2[at] : 0.f;
-                    mi.delta[s][e] = in ? a.delta[at] : 0.f;
-                }
-                __syncwarp();
                 if (tc::elect()) {
                     const uint32_t dst = base + kOffStages + s * kStage;
                     ptx::mbar_arrive_expect_tx(&mi.full[s], (kc + 2) * kQChunk);
@@ -127,6 +134,13 @@ __global__ void __launch_bounds__(kThreads, 1) dkv_tc_kernel(const __grid_consta
                             tc::tma_load_3d(base + kOffV + c * kChunk, &maps.v, &mi.v_full, 64 * c, h, pl.k0 + j0);
                     }
                 }
+                __syncwarp();
+#pragma unroll
+                for (int e = 0; e < 2; ++e) mi.lse2[s][lane + 32 * e] = lse2[e], mi.delta[s][lane + 32 * e] = delta[e];
+                __syncwarp();
+                if (tc::elect()) ptx::mbar_arrive(&mi.full[s]);
+                __syncwarp();
+                stats(first + i + 1);
             }
             if (!ok && lane == 0) {  // an error: the copies in flight land before the block ends
                 for (int x = max(0, i - kStages); x < i; ++x)
@@ -175,14 +189,18 @@ __global__ void __launch_bounds__(kThreads, 1) dkv_tc_kernel(const __grid_consta
                 for (int k = 0; k < 4; ++k)  // columns of P: 16 of each half lie at the start of its 32 of S
                     ptx::mma_ts(tmem + kTmDv, tmem + (i & 1) * 64 + (k >> 1) * 32 + (k & 1) * 8,
                                 tc::moved(dO_desc, 2048 * k), kIdV, i + k > 0);
+                if (i + 1 < n) {
+                    if (!(ok = tc::wait(&mi.dp_read, i & 1, dead))) break;
+                    ptx::tc_fence_after();
+                    dprobs(i + 1);
+                }
                 if (!(ok = tc::wait(&mi.ds_full, i & 1, dead))) break;
                 ptx::tc_fence_after();
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    ptx::mma_ts(tmem + kTmDk, tmem + kTmDp + (k >> 1) * 32 + (k & 1) * 8,
-                                tc::moved(q_desc, 2048 * k), id_k, i + k > 0);
+                for (int k = 0; k < 4; ++k)  // columns of dS: behind P's
+                    ptx::mma_ts(tmem + kTmDk, tmem + (i & 1) * 64 + (k >> 1) * 32 + 16 + (k & 1) * 8, tc::moved(q_desc, 2048 * k), id_k,
+                                i + k > 0);
                 ptx::mma_commit(&mi.empty[i % kStages]);
-                if (i + 1 < n) dprobs(i + 1);
             }
             ptx::mma_commit(&mi.done);
             if (!ok) ptx::mbar_wait_bounded(&mi.done, 0, tc::kWaitCycles);  // an error: nothing in flight at the end
@@ -237,6 +255,8 @@ __global__ void __launch_bounds__(kThreads, 1) dkv_tc_kernel(const __grid_consta
             ptx::tc_fence_after();
             ptx::tmem_ld32(at + kTmDp, v);
             ptx::tmem_wait_ld();
+            ptx::tc_fence_before();
+            ptx::mbar_arrive(&mi.dp_read);
             const float4 *d4 = reinterpret_cast<const float4 *>(&mi.delta[s][half * 32]);
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
@@ -253,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, 1) dkv_tc_kernel(const __grid_consta
             }
 #pragma unroll
             for (int c = 0; c < 16; ++c) x[c] = tc::pack_bf16(p[2 * c], p[2 * c + 1]);
-            ptx::tmem_st16(at + kTmDp, x);
+            ptx::tmem_st16(at + (i & 1) * 64 + 16, x);
             ptx::tmem_wait_st();
             ptx::tc_fence_before();
             ptx::mbar_arrive(&mi.ds_full);
@@ -313,7 +333,7 @@ constexpr uint32_t kDqSmem = kOffMiscQ + 1024 + 1024;
 constexpr uint32_t kTqDp = 96, kTqDq = 192, kTqDs = 384;
 
 struct DqMisc {
-    uint64_t q_full, do_full, k_full[3], k_empty[3], v_full[3], v_empty[3], s_full, s_read, dp_full, ds_full, done;
+    uint64_t q_full, do_full, k_full[3], k_empty[3], v_full[3], v_empty[3], s_full, s_read, dp_full, dp_read, ds_full, done;
     int64_t find[kThreads / 32 + 2];
     uint32_t tmem, dead;
 };
@@ -331,6 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constan
             for (uint64_t *b : {&mi.k_full[i], &mi.k_empty[i], &mi.v_full[i], &mi.v_empty[i]}) ptx::mbar_init(b, 1);
         for (uint64_t *b : {&mi.q_full, &mi.do_full, &mi.s_full, &mi.dp_full, &mi.done}) ptx::mbar_init(b, 1);
         ptx::mbar_init(&mi.s_read, 256);
+        ptx::mbar_init(&mi.dp_read, 256);
         ptx::mbar_init(&mi.ds_full, 256);
         mi.dead = 0;
         ptx::fence_mbar_init();
@@ -436,14 +457,19 @@ __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constan
                     ptx::tc_fence_after();
                     ok = ok && scores(j + 1);
                 }
+                if (ok && j + 1 < n) {
+                    ok = tc::wait(&mi.dp_read, j & 1, dead);
+                    ptx::tc_fence_after();
+                    ok = ok && dprobs(j + 1);
+                }
                 if (!ok || !(ok = tc::wait(&mi.ds_full, j & 1, dead))) break;
                 ptx::tc_fence_after();
                 const uint64_t kd = tc::moved(desc_mn, keys(j));
+                const uint32_t ds = tmem + kTqDs + (j & 1) * (kKb / 2);
 #pragma unroll
                 for (int k = 0; k < kKb / 16; ++k)
-                    ptx::mma_ts(tmem + kTqDq, tmem + kTqDs + 8 * k, tc::moved(kd, 2048 * k), id_q, j + k > 0);
+                    ptx::mma_ts(tmem + kTqDq, ds + 8 * k, tc::moved(kd, 2048 * k), id_q, j + k > 0);
                 ptx::mma_commit(&mi.k_empty[j % 3]);
-                if (j + 1 < n) ok = dprobs(j + 1);
             }
             ptx::mma_commit(&mi.done);
             if (!ok) ptx::mbar_wait_bounded(&mi.done, 0, tc::kWaitCycles);  // an error: nothing in flight at the end
@@ -480,11 +506,13 @@ __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constan
                     tc::st_shared_v4(base + kOffK + ((j % 3) * 3 + x / per) * kKbChunk + (from + x % per) * 16, 0, 0, 0, 0);
                 ptx::fence_proxy_async_smem();
             }
-            if (!(ok = tc::wait(&mi.dp_full, j & 1, dead))) break;  // the last dQ has read dS, too
+            if (!(ok = tc::wait(&mi.dp_full, j & 1, dead))) break;
             ptx::tc_fence_after();
             ptx::tmem_ld32(lanes + kTqDp + kHalf * half, v);
             ptx::tmem_ld16(lanes + kTqDp + kHalf * half + 32, u);
             ptx::tmem_wait_ld();
+            ptx::tc_fence_before();
+            ptx::mbar_arrive(&mi.dp_read);
             uint32_t x[16], y[8];
 #pragma unroll
             for (int c = 0; c < kHalf; c += 2) {
@@ -496,8 +524,10 @@ __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constan
                 }
                 (c < 32 ? x[(c >> 1) & 15] : y[(c >> 1) & 7]) = tc::pack_bf16(d0, d1);
             }
-            ptx::tmem_st16(lanes + kTqDs + kHalf / 2 * half, x);
-            tc::tmem_st8(lanes + kTqDs + kHalf / 2 * half + 16, y);
+            // the product that read this place two blocks ago ended before S of this block was formed
+            const uint32_t to = lanes + kTqDs + (j & 1) * (kKb / 2) + kHalf / 2 * half;
+            ptx::tmem_st16(to, x);
+            tc::tmem_st8(to + 16, y);
             ptx::tmem_wait_st();
             ptx::tc_fence_before();
             ptx::mbar_arrive(&mi.ds_full);

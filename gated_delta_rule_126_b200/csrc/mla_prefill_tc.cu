@@ -35,7 +35,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLazy = 8.f;
 
 struct Misc {
-    uint64_t full[kSlots], empty[kSlots], q_full[2], s_full[2], p_full[2], pv_done[2], drain;
+    uint64_t full[kSlots], k_free[2], v_free[2], q_full[2], s_full[2], p_full[2][2], pv_done[2], drain;
     int64_t find[kThreads / 32 + 2];
     uint32_t tmem, dead;
 };
@@ -53,11 +53,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
     const int h = blockIdx.x % a.H, kc = a.dr ? 3 : 2;  // chunks of a key
 
     if (tid == 0) {
-        for (int i = 0; i < kSlots; ++i) ptx::mbar_init(&mi.full[i], 1), ptx::mbar_init(&mi.empty[i], 1);
+        for (int i = 0; i < kSlots; ++i) ptx::mbar_init(&mi.full[i], 1);
         for (int t = 0; t < 2; ++t) {
+            ptx::mbar_init(&mi.k_free[t], 1);
+            ptx::mbar_init(&mi.v_free[t], 1);
+            ptx::mbar_init(&mi.p_full[t][0], 128);
+            ptx::mbar_init(&mi.p_full[t][1], 128);
             ptx::mbar_init(&mi.q_full[t], 1);
             ptx::mbar_init(&mi.s_full[t], 1);
-            ptx::mbar_init(&mi.p_full[t], 128);
             ptx::mbar_init(&mi.pv_done[t], 1);
         }
         ptx::mbar_init(&mi.drain, 1);
@@ -107,7 +110,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
             for (int j = 0; ok && j < blocks; ++j)
                 for (int c = 0; c < per; ++c, ++idx) {
                     const int slot = idx % kSlots;
-                    if (idx >= kSlots && !(ok = tc::wait(&mi.empty[slot], (idx / kSlots - 1) & 1, dead))) break;
+                    if (idx >= kSlots) {  // what was in the slot: keys or values of block g
+                        const int g = (idx - kSlots) / per;
+                        uint64_t *free = (idx - kSlots) % per < kc ? &mi.k_free[g & 1] : &mi.v_free[g & 1];
+                        if (!(ok = tc::wait(free, (g >> 1) & 1, dead))) break;
+                    }
                     const uint32_t dst = base + kOffRing + slot * kSlotBytes;
                     ptx::mbar_arrive_expect_tx(&mi.full[slot], kSlotBytes);
                     if (c < 2) {
@@ -149,8 +156,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
                 return true;
             };
             auto pv = [&](int t, int j) {
-                if (!tc::wait(&mi.p_full[t], j & 1, dead)) return false;
                 for (int c = 0; c < 2; ++c) {
+                    if (!tc::wait(&mi.p_full[t][c], j & 1, dead)) return false;
                     const int idx = j * per + kc + c, slot = idx % kSlots;
                     if (!tc::wait(&mi.full[slot], (idx / kSlots) & 1, dead)) return false;
                     ptx::tc_fence_after();
@@ -164,21 +171,18 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
                 ptx::mma_commit(&mi.pv_done[t]);
                 return true;
             };
-            auto release = [&](int first, int count) {
-                for (int i = first; i < first + count; ++i) ptx::mma_commit(&mi.empty[i % kSlots]);
-            };
             bool ok = true;
             for (int t = 0; ok && t < 2; ++t)
                 if (n[t]) ok = tc::wait(&mi.q_full[t], 0, dead) && qk(t, 0);
-            if (ok) release(0, kc);
+            if (ok) ptx::mma_commit(&mi.k_free[0]);
             for (int j = 0; ok && j < blocks; ++j) {
                 if (j < n[0]) ok = pv(0, j);
                 if (ok && j + 1 < n[0]) ok = qk(0, j + 1);
                 if (ok && j < n[1]) ok = pv(1, j);
                 if (!ok) break;
-                release(j * per + kc, 2);
+                ptx::mma_commit(&mi.v_free[j & 1]);
                 if (j + 1 < n[1]) ok = qk(1, j + 1);
-                if (ok && j + 1 < blocks) release((j + 1) * per, kc);
+                if (ok && j + 1 < blocks) ptx::mma_commit(&mi.k_free[(j + 1) & 1]);
             }
             if (!ok) {  // an error: the products in flight end before TMEM goes away
                 ptx::mma_commit(&mi.drain);
@@ -260,23 +264,30 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
                 }
             }
             const float off = top == -INFINITY ? 0.f : top * sl2;
-            float add[4] = {};
+            uint64_t add[2] = {0, 0};
+            const uint64_t by = tc::pair(sl2, sl2), less = tc::pair(-off, -off);
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 uint32_t p[16];
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
-                    const float x = ptx::ex2_approx(fmaf(__uint_as_float(s[c][2 * e]), sl2, -off));
-                    const float y = ptx::ex2_approx(fmaf(__uint_as_float(s[c][2 * e + 1]), sl2, -off));
-                    add[e & 3] += x + y;
+                    float x, y;
+                    tc::split(tc::fma2(tc::pair(s[c][2 * e], s[c][2 * e + 1]), by, less), x, y);
+                    x = ptx::ex2_approx(x);
+                    y = ptx::ex2_approx(y);
+                    add[e & 1] = tc::add2(add[e & 1], tc::pair(x, y));
                     p[e] = tc::pack_bf16(x, y);
                 }
                 ptx::tmem_st16(sa + 16 * c, p);
+                if (c & 1) {  // the products of 64 keys can begin
+                    ptx::tmem_wait_st();
+                    ptx::tc_fence_before();
+                    ptx::mbar_arrive(&mi.p_full[t][c >> 1]);
+                }
             }
-            sum += (add[0] + add[1]) + (add[2] + add[3]);
-            ptx::tmem_wait_st();
-            ptx::tc_fence_before();
-            ptx::mbar_arrive(&mi.p_full[t]);
+            float x, y;
+            tc::split(tc::add2(add[0], add[1]), x, y);
+            sum += x + y;
         }
         if (ok && n[t]) ok = tc::wait(&mi.pv_done[t], (n[t] - 1) & 1, dead);
         ptx::tc_fence_after();
