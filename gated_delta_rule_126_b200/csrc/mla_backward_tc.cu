@@ -9,7 +9,7 @@
 //   TMEM: S^T twice 64 columns, dP^T 64, dV 128, dK 192: all 512; P^T and dS^T lie over their S^T, so that the next
 //   tile's dP^T is formed while this one's dS^T is.
 // dq_tc_kernel: a block owns 128 queries of one head and streams the keys in blocks of 96.
-//   S = Q K^T, dP = dO V^T  [128 x 96];  dQ += dS K, dS in TMEM.  TMEM: S 96, dP 96, dQ 192, dS twice 48.
+//   S = Q K^T, dP = dO V^T  [128 x 96];  dQ += dS K, dS in TMEM.  TMEM: S 96, dP 96, dQ 192, dS 48, dO 64.
 // P = exp2(scale log2(e) S - lse2) and dS = P (dP - delta) are rounded to bf16 for their products; the
 // factor `scale` of dq and dk is applied to the float32 sums at the end.
 // Bound by the tensor cores.  Warps 0-7: elementwise work and output, two warpgroups with half of the columns each;
@@ -322,18 +322,19 @@ __global__ void __launch_bounds__(kThreads, 1) dkv_tc_kernel(const __grid_consta
 }
 
 // ------------------------------------------------------------------------------ dq
-// Key blocks of 96: with Q and dO resident (80 KB), three blocks of keys and one and a half of values fit, so that
-// a block's keys, which stay until its dQ product, do not hold up the loads of the next but one (blocks of 128
-// allow two: 3,880 cycles a block instead of the products' 2,048).
-// Shared memory: Q (3 chunks of 128 rows), dO (2), three blocks of keys (3 chunks of 96 rows), three chunks of values.
+// dO is the left operand of dP alone, so it lies in TMEM; with Q in shared memory (48 KB) three key blocks of 96 and
+// two of values fit beside it.  A block's keys stay until its dQ product: with two blocks in flight (of
+// 128 keys, dO in shared memory) the loads of the next but one held the products up (3,880 cycles a block instead of
+// 2,048), and with one and a half blocks of values those held up dP (2,450 a block of 96 instead of 1,630).
+// Shared memory: Q (3 chunks of 128 rows), three blocks of keys (3 chunks of 96 rows), two of values (2 chunks).
 constexpr int kKb = 96;
 constexpr uint32_t kKbChunk = kKb * 128;
-constexpr uint32_t kOffDo = 3 * kChunk, kOffK = 5 * kChunk, kOffVq = kOffK + 9 * kKbChunk, kOffMiscQ = kOffVq + 3 * kKbChunk;
+constexpr uint32_t kOffK = 3 * kChunk, kOffVq = kOffK + 9 * kKbChunk, kOffMiscQ = kOffVq + 4 * kKbChunk;
 constexpr uint32_t kDqSmem = kOffMiscQ + 1024 + 1024;
-constexpr uint32_t kTqDp = 96, kTqDq = 192, kTqDs = 384;
+constexpr uint32_t kTqDp = 96, kTqDq = 192, kTqDs = 384, kTqDo = 432;
 
 struct DqMisc {
-    uint64_t q_full, do_full, k_full[3], k_empty[3], v_full[3], v_empty[3], s_full, s_read, dp_full, dp_read, ds_full, done;
+    uint64_t q_full, do_full, k_full[3], k_empty[3], v_full[2], v_empty[2], s_full, s_read, dp_full, dp_read, ds_full, done;
     int64_t find[kThreads / 32 + 2];
     uint32_t tmem, dead;
 };
@@ -347,9 +348,10 @@ __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constan
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int h = blockIdx.x % a.H, kc = a.dr ? 3 : 2;
     if (tid == 0) {
-        for (int i = 0; i < 3; ++i)
-            for (uint64_t *b : {&mi.k_full[i], &mi.k_empty[i], &mi.v_full[i], &mi.v_empty[i]}) ptx::mbar_init(b, 1);
-        for (uint64_t *b : {&mi.q_full, &mi.do_full, &mi.s_full, &mi.dp_full, &mi.done}) ptx::mbar_init(b, 1);
+        for (int i = 0; i < 3; ++i) ptx::mbar_init(&mi.k_full[i], 1), ptx::mbar_init(&mi.k_empty[i], 1);
+        for (int i = 0; i < 2; ++i) ptx::mbar_init(&mi.v_full[i], 1), ptx::mbar_init(&mi.v_empty[i], 1);
+        for (uint64_t *b : {&mi.q_full, &mi.s_full, &mi.dp_full, &mi.done}) ptx::mbar_init(b, 1);
+        ptx::mbar_init(&mi.do_full, 256);
         ptx::mbar_init(&mi.s_read, 256);
         ptx::mbar_init(&mi.dp_read, 256);
         ptx::mbar_init(&mi.ds_full, 256);
@@ -374,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constan
 
     if (warp == 9) {
         if (tc::elect() && n > 0) {
-            int ks = 0, vs = 0;  // loads begun: blocks of keys, chunks of values
+            int ks = 0, vs = 0;  // loads begun
             bool ok = true;
             auto load_k = [&](int j) {
                 if (!ok || j >= n || (j >= 3 && !(ok = tc::wait(&mi.k_empty[j % 3], (j / 3 - 1) & 1, dead)))) return;
@@ -385,35 +387,30 @@ __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constan
                 if (a.dr) tc::tma_load_2d(dst + 2 * kKbChunk, &maps.kr, &mi.k_full[j % 3], 0, pl.k0 + j * kKb);
                 ++ks;
             };
-            auto load_v = [&](int x) {  // chunk x & 1 of block x / 2
-                if (!ok || x >= 2 * n || (x >= 3 && !(ok = tc::wait(&mi.v_empty[x % 3], (x / 3 - 1) & 1, dead)))) return;
-                ptx::mbar_arrive_expect_tx(&mi.v_full[x % 3], kKbChunk);
-                tc::tma_load_3d(base + kOffVq + (x % 3) * kKbChunk, &maps.v, &mi.v_full[x % 3], 64 * (x & 1), h, pl.k0 + (x >> 1) * kKb);
+            auto load_v = [&](int j) {
+                if (!ok || j >= n || (j >= 2 && !(ok = tc::wait(&mi.v_empty[j & 1], (j / 2 - 1) & 1, dead)))) return;
+                ptx::mbar_arrive_expect_tx(&mi.v_full[j & 1], 2 * kKbChunk);
+                for (int c = 0; c < 2; ++c)
+                    tc::tma_load_3d(base + kOffVq + (2 * (j & 1) + c) * kKbChunk, &maps.v, &mi.v_full[j & 1], 64 * c, h, pl.k0 + j * kKb);
                 ++vs;
             };
             ptx::mbar_arrive_expect_tx(&mi.q_full, kc * kChunk);
             for (int c = 0; c < kc; ++c) tc::tma_load_3d(base + c * kChunk, &maps.q, &mi.q_full, 64 * c, h, pl.q0 + i0);
             load_k(0);
-            ptx::mbar_arrive_expect_tx(&mi.do_full, 2 * kChunk);
-            for (int c = 0; c < 2; ++c)
-                tc::tma_load_3d(base + kOffDo + c * kChunk, &maps.dO, &mi.do_full, 64 * c, h, pl.q0 + i0);
             load_v(0);
-            load_v(1);
             load_k(1);
-            load_v(2);
+            load_v(1);
             load_k(2);
-            for (int j = 0; ok && j < n; ++j) {  // in the order in which the products free the slots
-                load_v(2 * j + 3);
-                load_v(2 * j + 4);
+            for (int j = 0; ok && j < n; ++j) {  // in the order in which the products free the places
+                load_v(j + 2);
                 load_k(j + 3);
             }
             if (!ok) {  // an error: the copies in flight land before the block ends
                 ptx::mbar_wait_bounded(&mi.q_full, 0, tc::kWaitCycles);
-                ptx::mbar_wait_bounded(&mi.do_full, 0, tc::kWaitCycles);
                 for (int j = max(0, ks - 3); j < ks; ++j)
                     ptx::mbar_wait_bounded(&mi.k_full[j % 3], (j / 3) & 1, tc::kWaitCycles);
-                for (int x = max(0, vs - 3); x < vs; ++x)
-                    ptx::mbar_wait_bounded(&mi.v_full[x % 3], (x / 3) & 1, tc::kWaitCycles);
+                for (int j = max(0, vs - 2); j < vs; ++j)
+                    ptx::mbar_wait_bounded(&mi.v_full[j & 1], (j / 2) & 1, tc::kWaitCycles);
             }
         }
         __syncwarp();
@@ -436,17 +433,13 @@ __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constan
                 return true;
             };
             auto dprobs = [&](int j) {
+                if (!tc::wait(&mi.v_full[j & 1], (j >> 1) & 1, dead)) return false;
+                ptx::tc_fence_after();
+                const uint64_t vd = tc::moved(desc, kOffVq + 2 * (j & 1) * kKbChunk);
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    const int x = 2 * j + c;
-                    if (!tc::wait(&mi.v_full[x % 3], (x / 3) & 1, dead)) return false;
-                    ptx::tc_fence_after();
-                    const uint64_t od = tc::moved(desc, kOffDo + c * kChunk), vd = tc::moved(desc, kOffVq + (x % 3) * kKbChunk);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        ptx::mma_ss(tmem + kTqDp, tc::moved(od, 32 * k), tc::moved(vd, 32 * k), kIdS, c + k > 0);
-                    ptx::mma_commit(&mi.v_empty[x % 3]);
-                }
+                for (int k = 0; k < 8; ++k)
+                    ptx::mma_ts(tmem + kTqDp, tmem + kTqDo + 8 * k, tc::moved(vd, (k >> 2) * kKbChunk + 32 * (k & 3)), kIdS, k > 0);
+                ptx::mma_commit(&mi.v_empty[j & 1]);
                 ptx::mma_commit(&mi.dp_full);
                 return true;
             };
@@ -465,10 +458,9 @@ __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constan
                 if (!ok || !(ok = tc::wait(&mi.ds_full, j & 1, dead))) break;
                 ptx::tc_fence_after();
                 const uint64_t kd = tc::moved(desc_mn, keys(j));
-                const uint32_t ds = tmem + kTqDs + (j & 1) * (kKb / 2);
 #pragma unroll
                 for (int k = 0; k < kKb / 16; ++k)
-                    ptx::mma_ts(tmem + kTqDq, ds + 8 * k, tc::moved(kd, 2048 * k), id_q, j + k > 0);
+                    ptx::mma_ts(tmem + kTqDq, tmem + kTqDs + 8 * k, tc::moved(kd, 2048 * k), id_q, j + k > 0);
                 ptx::mma_commit(&mi.k_empty[j % 3]);
             }
             ptx::mma_commit(&mi.done);
@@ -484,6 +476,19 @@ __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constan
         const int64_t stat = int64_t(h) * a.Tq + pl.q0 + r;
         const float lse2 = r < pl.lq ? a.lse2[stat] : 0.f, delta = r < pl.lq ? a.delta[stat] : 0.f;
         bool ok = true;
+        if (n > 0) {  // dO into TMEM, half of the channels each
+            const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.dO) + (int64_t(pl.q0 + r) * a.H + h) * 128 + 64 * half);
+            uint32_t v[32];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const uint4 x = r < pl.lq ? src[e] : make_uint4(0, 0, 0, 0);
+                v[4 * e] = x.x, v[4 * e + 1] = x.y, v[4 * e + 2] = x.z, v[4 * e + 3] = x.w;
+            }
+            ptx::tmem_st32(lanes + kTqDo + 32 * half, v);
+            ptx::tmem_wait_st();
+            ptx::tc_fence_before();
+            ptx::mbar_arrive(&mi.do_full);
+        }
         for (int j = 0; j < n; ++j) {
             if (!(ok = tc::wait(&mi.s_full, j & 1, dead))) break;
             ptx::tc_fence_after();
@@ -524,10 +529,11 @@ __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constan
                 }
                 (c < 32 ? x[(c >> 1) & 15] : y[(c >> 1) & 7]) = tc::pack_bf16(d0, d1);
             }
-            // the product that read this place two blocks ago ended before S of this block was formed
-            const uint32_t to = lanes + kTqDs + (j & 1) * (kKb / 2) + kHalf / 2 * half;
-            ptx::tmem_st16(to, x);
-            tc::tmem_st8(to + 16, y);
+            // the last block's product, which frees its keys, has read dS
+            if (j && !(ok = tc::wait(&mi.k_empty[(j - 1) % 3], ((j - 1) / 3) & 1, dead))) break;
+            ptx::tc_fence_after();
+            ptx::tmem_st16(lanes + kTqDs + kHalf / 2 * half, x);
+            tc::tmem_st8(lanes + kTqDs + kHalf / 2 * half + 16, y);
             ptx::tmem_wait_st();
             ptx::tc_fence_before();
             ptx::mbar_arrive(&mi.ds_full);
@@ -535,7 +541,7 @@ __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constan
         if (ok && n > 0) ok = tc::wait(&mi.done, 0, dead);
         ptx::tc_fence_after();
         if (ok) {
-            // each warpgroup writes half of the channels, through the place of Q and dO, which nothing reads any more
+            // each warpgroup writes half of the channels, through the place of Q and the keys, which nothing reads any more
             const uint32_t stage = base + warp * tc::RowStage<12>::kBytes;
             const int width = 64 * kc;
             __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.dq) + (int64_t(pl.q0 + r - lane) * a.H + h) * width + half * (width / 2);
@@ -579,7 +585,6 @@ cudaError_t launch_mla_backward_tc(const MlaArgs &a, cudaStream_t st) {
     bool ok = tc::rows_map(&kv.q, a.q, 128 + a.dr, a.H, a.Tq, a.q_st, a.q_sh, kQt) &&
               tc::rows_map(&kv.dO, a.dO, 128, a.H, a.Tq, dO_st, 128, kQt) &&
               tc::rows_map(&qs.q, a.q, 128 + a.dr, a.H, a.Tq, a.q_st, a.q_sh, 128) &&
-              tc::rows_map(&qs.dO, a.dO, 128, a.H, a.Tq, dO_st, 128, 128) &&
               tc::rows_map(&kv.k, a.k, 128, a.H, a.Tk, a.k_st, a.k_sh, 128) &&
               tc::rows_map(&kv.v, a.v, 128, a.H, a.Tk, a.v_st, a.v_sh, 128) &&
               tc::rows_map(&qs.k, a.k, 128, a.H, a.Tk, a.k_st, a.k_sh, kKb) &&
