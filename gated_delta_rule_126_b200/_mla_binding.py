@@ -73,8 +73,23 @@ def _rows(rows, used, *shape, dtype, device):
 
 def _verify(specs, index):
     """Checks (name, tensor or None, shape, dtype, contiguous in what) of every tensor before a pointer reaches the
-    library: the kernels trust the sizes they are given.  Shapes come first, then the device of the first
-    tensor, whose index ``index`` is."""
+    library: the kernels trust the sizes they are given.  ``index`` is the first tensor's device."""
+    if index >= 0:
+        try:
+            for _, t, shape, dtype, packed in specs:
+                if t is not None and (t.shape != shape or (t.dtype is not dtype and dtype is not None) or
+                                      t.get_device() != index or
+                                      not (t.is_contiguous() if packed else t.stride(-1) == 1)):
+                    break
+            else:
+                return
+        except (AttributeError, IndexError):
+            pass
+    _explain(specs, index)
+
+
+def _explain(specs, index):
+    """Raises what is wrong with one of the tensors, shapes first; returns when nothing is."""
     for name, t, shape, _, _ in specs:
         if t is None:
             continue
@@ -85,17 +100,40 @@ def _verify(specs, index):
     for name, t, _, dtype, packed in specs:
         if t is None:
             continue
-        if t.get_device() != index or index < 0:
-            if not t.is_cuda:
-                raise ValueError(f"{name} must be a CUDA tensor")
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if t.get_device() != index:
             raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
         if dtype is not None and t.dtype is not dtype:
             raise ValueError(f"{name} must have dtype {dtype}, got {t.dtype}")
         if packed:
             if not t.is_contiguous():
                 raise ValueError(f"{name} must be contiguous")
-        elif t.stride(-1) != 1 and t.shape[-1] > 1:
+        elif t.shape[-1] > 1 and t.stride(-1) != 1:
             raise ValueError(f"{name} must be contiguous in its last dimension")
+
+
+def _sizes(t, name, ndim):
+    """Shape of t, which must be a tensor with ndim dimensions."""
+    try:
+        shape = t.shape
+        if len(shape) == ndim:
+            return shape
+    except (AttributeError, TypeError):
+        pass
+    return _dims(t, name, ndim)
+
+
+def _host_offsets(cu, host, rows):
+    """(sequences, host copy of the offsets, their last): as ``_binding._offsets``, at a serving step's cost."""
+    if isinstance(host, torch.Tensor) and host.dtype is torch.int32 and host.device.type == "cpu" and \
+            host.dim() == 1 and host.is_contiguous() and host.numel() > 0 and isinstance(cu, torch.Tensor) and \
+            cu.shape == host.shape:
+        last = host[-1].item()
+        if last <= rows:
+            return host.numel() - 1, host, last
+    n, host = _offsets(cu, host, rows)
+    return n, host, int(host[-1])
 
 
 def _written(t, name):
@@ -132,11 +170,11 @@ def mla_append(c, k_rope, cache, page_table, past_lens, cu_seqlens, norm_weight=
     itself rotates in place), "c" and "k_rope".
     """
     lib = _lib()
-    T, dc = _dims(c, "c", 2)
-    dr = 0 if k_rope is None else _dims(k_rope, "k_rope", 2)[1]
-    pages, page, _ = _dims(cache, "cache", 3)
-    N, width = _dims(page_table, "page_table", 2)
-    H = 0 if q_rope is None else _dims(q_rope, "q_rope", 3)[1]
+    T, dc = _sizes(c, "c", 2)
+    dr = 0 if k_rope is None else _sizes(k_rope, "k_rope", 2)[1]
+    pages, page, _ = _sizes(cache, "cache", 3)
+    N, width = _sizes(page_table, "page_table", 2)
+    H = 0 if q_rope is None else _sizes(q_rope, "q_rope", 3)[1]
     dt, index = _type(c, "c"), c.get_device()
     i32, f32 = torch.int32, torch.float32
     specs = [("c", c, (T, dc), dt, _LAST), ("k_rope", k_rope, (T, dr), dt, _LAST),
@@ -190,9 +228,9 @@ def mla_decode(q, cache, page_table, seq_lens, d_latent, scale, o=None, lse=None
     told from the absorbed shapes).  Returns ``(o [B,n,H,d_latent], lse [B,n,H] or None)``.
     """
     lib = _lib()
-    B, n, H, W = _dims(q, "q", 4)
-    pages, page, _ = _dims(cache, "cache", 3)
-    width = _dims(page_table, "page_table", 2)[1]
+    B, n, H, W = _sizes(q, "q", 4)
+    pages, page, _ = _sizes(cache, "cache", 3)
+    width = _sizes(page_table, "page_table", 2)[1]
     dc = int(d_latent)
     if not 1 <= dc <= W:
         raise ValueError(f"d_latent must lie in 1..{W}, got {dc}")
@@ -219,20 +257,21 @@ def mla_decode(q, cache, page_table, seq_lens, d_latent, scale, o=None, lse=None
 
 def _packed(q, k, v, cu_q, cu_k, k_rope, scale, cu_q_host, cu_k_host, o, lse, dO=None):
     """Checks shared by mla_prefill and mla_backward; returns sizes and the library's leading arguments."""
-    Tq, H, d = _dims(q, "q", 3)
-    Tk, _, dn = _dims(k, "k", 3)
-    dv = _dims(v, "v", 3)[2]
-    dr = 0 if k_rope is None else _dims(k_rope, "k_rope", 2)[1]
+    Tq, H, d = _sizes(q, "q", 3)
+    Tk, _, dn = _sizes(k, "k", 3)
+    dv = _sizes(v, "v", 3)[2]
+    dr = 0 if k_rope is None else _sizes(k_rope, "k_rope", 2)[1]
     dt, index = _type(q, "q"), q.get_device()
     i32 = torch.int32
     specs = [("q", q, (Tq, H, dn + dr), dt, _LAST), ("k", k, (Tk, H, dn), dt, _LAST), ("v", v, (Tk, H, dv), dt, _LAST),
              ("k_rope", k_rope, (Tk, dr), dt, _LAST), ("o", o, (Tq, H, dv), dt, _PACKED),
              ("lse", lse, (Tq, H), torch.float32, _PACKED), ("dO", dO, (Tq, H, dv), dt, _PACKED)]
-    for name, t, shape, _, _ in specs:  # before the offsets, which may have to come from the device
-        if isinstance(t, torch.Tensor) and t.shape != shape:
-            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    N, cq = _offsets(cu_q, cu_q_host, Tq)
-    M, ck = _offsets(cu_k, cu_k_host, Tk)
+    if cu_q_host is None or cu_k_host is None or index < 0:
+        for name, t, shape, _, _ in specs:  # before the offsets, which may have to come from the device
+            if isinstance(t, torch.Tensor) and t.shape != shape:
+                raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    N, cq, tq = _host_offsets(cu_q, cu_q_host, Tq)
+    M, ck, tk = _host_offsets(cu_k, cu_k_host, Tk)
     if N != M:
         raise ValueError(f"cu_q holds {N} sequences, cu_k {M}")
     specs += [("cu_q", cu_q, (N + 1,), i32, _PACKED), ("cu_k", cu_k, (N + 1,), i32, _PACKED)]
@@ -242,7 +281,7 @@ def _packed(q, k, v, cu_q, cu_k, k_rope, scale, cu_q_host, cu_k_host, o, lse, dO
     lead = (q.data_ptr(), qs[0], qs[1], k.data_ptr(), ks[0], ks[1], _ptr(k_rope), k_rope.stride(0) if dr else 0,
             v.data_ptr(), vs[0], vs[1], DTYPE_CODE[dt], cu_q.data_ptr(), cq.data_ptr(), cu_k.data_ptr(), ck.data_ptr(),
             N, H, dn, dr, dv, scale)
-    return (Tq, Tk, H, dn, dr, dv, index, dt, cq, ck), lead
+    return (Tq, Tk, tq, tk, H, dn, dr, dv, index, dt, cq, ck), lead
 
 
 def mla_prefill(q, k, v, cu_q, cu_k, k_rope=None, scale=None, causal=True, cu_q_host=None, cu_k_host=None, o=None,
@@ -256,15 +295,14 @@ def mla_prefill(q, k, v, cu_q, cu_k, k_rope=None, scale=None, causal=True, cu_q_
     rows that belong to no sequence are zero, or left as they were in a given o or lse.
     """
     lib = _lib()
-    (Tq, Tk, H, dn, dr, dv, index, dt, cq, ck), lead = _packed(q, k, v, cu_q, cu_k, k_rope, scale, cu_q_host, cu_k_host,
-                                                             o, lse)
+    (Tq, _, tq, _, H, _, _, dv, index, dt, cq, ck), lead = _packed(q, k, v, cu_q, cu_k, k_rope, scale, cu_q_host,
+                                                                   cu_k_host, o, lse)
     context, raw = _on(stream, index)
     with context:
-        used = int(cq[-1]) if o is None or (lse is None and want_lse) else Tq
         if o is None:
-            o = _rows(Tq, used, H, dv, dtype=dt, device=q.device)
+            o = _rows(Tq, tq, H, dv, dtype=dt, device=q.device)
         if lse is None and want_lse:
-            lse = _rows(Tq, used, H, dtype=torch.float32, device=q.device)
+            lse = _rows(Tq, tq, H, dtype=torch.float32, device=q.device)
         st = lib.mla_prefill(*lead, 1 if causal else 0, o.data_ptr(), _ptr(lse), raw)
     _check(st, "mla_prefill")
     return o, lse
@@ -284,11 +322,10 @@ def mla_backward(q, k, v, cu_q, cu_k, o, lse, dO, k_rope=None, scale=None, causa
     over the heads).  Rows that belong to no sequence come back zero.
     """
     lib = _lib()
-    (Tq, Tk, H, dn, dr, dv, index, dt, cq, ck), lead = _packed(q, k, v, cu_q, cu_k, k_rope, scale, cu_q_host, cu_k_host,
-                                                             o, lse, dO)
+    (Tq, Tk, tq, tk, H, dn, dr, dv, index, dt, cq, ck), lead = _packed(q, k, v, cu_q, cu_k, k_rope, scale, cu_q_host,
+                                                                       cu_k_host, o, lse, dO)
     if o is None or lse is None or dO is None:
         raise TypeError("o, lse and dO must be torch.Tensors")
-    tq, tk = int(cq[-1]), int(ck[-1])
     if workspace is not None:
         _verify([("workspace", workspace, workspace.shape, None, _PACKED)], index)
     like = dict(dtype=dt, device=q.device)

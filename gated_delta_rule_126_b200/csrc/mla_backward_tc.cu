@@ -61,7 +61,8 @@ struct DkvMaps {
     CUtensorMap q, dO, k, kr, v;
 };
 
-__global__ void __launch_bounds__(kThreads, 1) dkv_tc_kernel(const __grid_constant__ DkvMaps maps, const MlaArgs a) {
+__global__ void __launch_bounds__(kThreads, 1) dkv_tc_kernel(const __grid_constant__ DkvMaps maps, const MlaArgs a,
+                                                                const __grid_constant__ MlaTiles list) {
     extern __shared__ uint8_t raw[];
     const uint32_t base = (ptx::smem_u32(raw) + 1023u) & ~1023u;
     DkvMisc &mi = *reinterpret_cast<DkvMisc *>(raw + (base - ptx::smem_u32(raw)) + kOffMisc);
@@ -81,8 +82,13 @@ __global__ void __launch_bounds__(kThreads, 1) dkv_tc_kernel(const __grid_consta
         mi.dead = 0;
         ptx::fence_mbar_init();
     }
-    int seq = 0, tile = 0;  // the first keys, which most queries see, first
-    if (!find_tile<kThreads>(a.cu_k, a.num_seqs, 128, blockIdx.x / a.H, mi.find, &seq, &tile)) return;
+    int seq = 0, tile = 0;
+    if (list.count > 0) {
+        seq = list.items[blockIdx.x / a.H] >> 16;
+        tile = list.items[blockIdx.x / a.H] & 0xffff;
+    } else if (!find_tile<kThreads>(a.cu_k, a.num_seqs, 128, blockIdx.x / a.H, mi.find, &seq, &tile)) {
+        return;
+    }
     if (warp == 8) {
         ptx::tmem_alloc(&mi.tmem, kTmemColumns);
         ptx::tmem_relinquish();
@@ -341,7 +347,8 @@ struct DqMisc {
 static_assert(sizeof(DqMisc) <= 1024, "misc");
 static_assert(kDqSmem <= 232448, "shared memory");
 
-__global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constant__ DkvMaps maps, const MlaArgs a) {
+__global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constant__ DkvMaps maps, const MlaArgs a,
+                                                               const __grid_constant__ MlaTiles list) {
     extern __shared__ uint8_t raw[];
     const uint32_t base = (ptx::smem_u32(raw) + 1023u) & ~1023u;
     DqMisc &mi = *reinterpret_cast<DqMisc *>(raw + (base - ptx::smem_u32(raw)) + kOffMiscQ);
@@ -358,8 +365,13 @@ __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constan
         mi.dead = 0;
         ptx::fence_mbar_init();
     }
-    int seq = 0, tile = 0;  // the last queries, which see most keys, first
-    if (!find_tile<kThreads>(a.cu_q, a.num_seqs, 128, gridDim.x / a.H - 1 - blockIdx.x / a.H, mi.find, &seq, &tile)) return;
+    int seq = 0, tile = 0;
+    if (list.count > 0) {
+        seq = list.items[blockIdx.x / a.H] >> 16;
+        tile = list.items[blockIdx.x / a.H] & 0xffff;
+    } else if (!find_tile<kThreads>(a.cu_q, a.num_seqs, 128, gridDim.x / a.H - 1 - blockIdx.x / a.H, mi.find, &seq, &tile)) {
+        return;
+    }
     if (warp == 8) {
         ptx::tmem_alloc(&mi.tmem, kTmemColumns);
         ptx::tmem_relinquish();
@@ -567,12 +579,12 @@ __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constan
     }
 }
 
-template <typename K> cudaError_t launch(K *kernel, const DkvMaps &maps, int64_t tiles, uint32_t smem, const MlaArgs &a, cudaStream_t st) {
+template <auto *Kernel> cudaError_t launch(const DkvMaps &maps, const MlaTiles &list, int64_t tiles, uint32_t smem, const MlaArgs &a, cudaStream_t st) {
     if (tiles == 0) return cudaSuccess;
     if (tiles * a.H > INT32_MAX) return cudaErrorInvalidValue;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    const cudaError_t e = tc::allow_smem<Kernel>(int(smem));
     if (e != cudaSuccess) return e;
-    kernel<<<unsigned(tiles * a.H), kThreads, smem, st>>>(maps, a);
+    Kernel<<<unsigned(tiles * a.H), kThreads, smem, st>>>(maps, a, list);
     return cudaGetLastError();
 }
 
@@ -591,9 +603,12 @@ cudaError_t launch_mla_backward_tc(const MlaArgs &a, cudaStream_t st) {
               tc::rows_map(&qs.v, a.v, 128, a.H, a.Tk, a.v_st, a.v_sh, kKb) &&
               (a.dr == 0 || (tc::rope_map(&kv.kr, a.k_rope, a.Tk, a.kr_st, 128) && tc::rope_map(&qs.kr, a.k_rope, a.Tk, a.kr_st, kKb)));
     if (!ok) return cudaErrorInvalidValue;
-    const cudaError_t e = launch(dkv_tc_kernel, kv, count_tiles(a.cu_k_host, a.num_seqs, 128), kDkvSmem, a, st);
+    // first the first keys, which most queries see; then the last queries, which see most keys
+    const cudaError_t e = launch<dkv_tc_kernel>(kv, list_tiles(a.cu_k_host, a.num_seqs, 128, false),
+                                                count_tiles(a.cu_k_host, a.num_seqs, 128), kDkvSmem, a, st);
     if (e != cudaSuccess) return e;
-    return launch(dq_tc_kernel, qs, count_tiles(a.cu_q_host, a.num_seqs, 128), kDqSmem, a, st);
+    return launch<dq_tc_kernel>(qs, list_tiles(a.cu_q_host, a.num_seqs, 128, true), count_tiles(a.cu_q_host, a.num_seqs, 128),
+                                kDqSmem, a, st);
 }
 
 cudaError_t mla_backward_fault(cudaStream_t st, unsigned int *out) { return mla_fault_read(st, out); }

@@ -58,7 +58,7 @@ __host__ __device__ inline Layout layout(int dc, int dr, int rb) {
     // Q, P, misc; with rb = 32 the 64-row reads of Q's last chunk end inside P
     const uint32_t fixed = uint32_t(L.chunks) * rb * 128u + rb * 128u + uint32_t(kMiscBytes);
     const int tile = dc / 128;
-    uint32_t room = 232448u - 1024u - fixed;
+    uint32_t room = 232448u - 1024u - 1024u - fixed;
     L.rope = dr == 0 ? 0 : tile == 4 ? (rb == 32 ? 3 : 2) : kMaxRope;  // as many tiles as the ring holds, at least in part
     room -= L.rope * kRopeBytes;
     L.slots = int(room / kSlotBytes);
@@ -79,6 +79,8 @@ struct Ring {
         if (++slot == n) slot = 0, ++round;
     }
 };
+
+constexpr uint32_t kMaxSmem = 232448 - 1024;  // the kernel's static shared memory is part of an SM's 227 KB
 
 struct Maps {
     CUtensorMap cache, q;
@@ -488,7 +490,7 @@ int box_rows(int page_size) {
 template <int RB>
 cudaError_t launch(const Maps &maps, const MlaDecodeArgs &a, const MlaDecodeShape &s, int box, cudaStream_t st) {
     const Layout L = layout(a.dc, a.dr, RB);
-    const cudaError_t e = cudaFuncSetAttribute(decode_tc_kernel<RB>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(L.total));
+    const cudaError_t e = tc::allow_smem<decode_tc_kernel<RB>>(int(kMaxSmem));
     if (e != cudaSuccess) return e;
     decode_tc_kernel<RB><<<s.grid(), kThreads, L.total, st>>>(maps, a, s, box);
     return cudaGetLastError();

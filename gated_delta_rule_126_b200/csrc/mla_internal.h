@@ -78,6 +78,26 @@ inline int64_t count_tiles(const int32_t *cu, int n, int tile) {
     return s;
 }
 
+// The tiles of a call in the order in which its blocks take them, for calls of few tiles (longer ones find
+// theirs on the device, at a few microseconds a block): sequence by sequence, because the tiles of a sequence share
+// its rows in L2 (sorted by work over all sequences, 4 x 4096 tokens of 32 heads took 15 to 20% longer).
+struct MlaTiles {
+    static constexpr int kMost = 256;
+    int count;
+    uint32_t items[kMost];  // sequence << 16 | tile
+};
+// The tiles of `tile` rows of a host offset array (cu_q or cu_k): the last first where `reversed`.
+inline MlaTiles list_tiles(const int32_t *cu, int num_seqs, int tile, bool reversed) {
+    MlaTiles list;
+    list.count = 0;
+    const int64_t total = count_tiles(cu, num_seqs, tile);
+    if (total > MlaTiles::kMost || num_seqs > 65535) return list;
+    for (int s = 0; s < num_seqs; ++s)
+        for (int t = 0; t * tile < cu[s + 1] - cu[s]; ++t)
+            list.items[reversed ? total - 1 - list.count : list.count] = uint32_t(s) << 16 | uint32_t(t), ++list.count;
+    return list;
+}
+
 cudaError_t launch_mla_append(const MlaAppendArgs &a, cudaStream_t st);
 cudaError_t launch_mla_decode(const MlaDecodeArgs &a, cudaStream_t st);
 bool mla_tc_supported(const MlaArgs &a);

@@ -45,7 +45,8 @@ struct Maps {
     CUtensorMap q, k, kr, v;
 };
 
-__global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_constant__ Maps maps, const MlaArgs a) {
+__global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_constant__ Maps maps, const MlaArgs a,
+                                                                   const __grid_constant__ MlaTiles list) {
     extern __shared__ uint8_t raw[];
     const uint32_t base = (ptx::smem_u32(raw) + 1023u) & ~1023u;
     Misc &mi = *reinterpret_cast<Misc *>(raw + (base - ptx::smem_u32(raw)) + kOffMisc);
@@ -73,8 +74,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
         ptx::prefetch_tmap(&maps.v);
         if (a.dr) ptx::prefetch_tmap(&maps.kr);
     }
-    int seq = 0, tile = 0;  // long tiles (the last queries) first
-    if (!find_tile<kThreads>(a.cu_q, a.num_seqs, 2 * kRows, gridDim.x / a.H - 1 - blockIdx.x / a.H, mi.find, &seq, &tile)) return;
+    int seq = 0, tile = 0;
+    if (list.count > 0) {
+        seq = list.items[blockIdx.x / a.H] >> 16;
+        tile = list.items[blockIdx.x / a.H] & 0xffff;
+    } else if (!find_tile<kThreads>(a.cu_q, a.num_seqs, 2 * kRows, gridDim.x / a.H - 1 - blockIdx.x / a.H, mi.find, &seq, &tile)) {
+        return;
+    }
     if (warp == 8) {
         ptx::tmem_alloc(&mi.tmem, kTmemColumns);
         ptx::tmem_relinquish();
@@ -354,9 +360,10 @@ cudaError_t launch_mla_prefill_tc(const MlaArgs &a, cudaStream_t st) {
         !tc::rows_map(&maps.v, a.v, 128, a.H, a.Tk, a.v_st, a.v_sh, 64) ||
         (a.dr && !tc::rope_map(&maps.kr, a.k_rope, a.Tk, a.kr_st, 128)))
         return cudaErrorInvalidValue;
-    const cudaError_t e = cudaFuncSetAttribute(prefill_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmem));
+    const cudaError_t e = tc::allow_smem<prefill_tc_kernel>(int(kSmem));
     if (e != cudaSuccess) return e;
-    prefill_tc_kernel<<<unsigned(grid), kThreads, kSmem, st>>>(maps, a);
+    const MlaTiles list = list_tiles(a.cu_q_host, a.num_seqs, 2 * kRows, true);  // a sequence's last queries, which see most keys, first
+    prefill_tc_kernel<<<unsigned(grid), kThreads, kSmem, st>>>(maps, a, list);
     return cudaGetLastError();
 }
 
