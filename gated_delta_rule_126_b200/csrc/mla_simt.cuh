@@ -57,6 +57,15 @@ __device__ bool find_tile(const int32_t *cu, int num_seqs, int tile, int64_t x, 
     return true;
 }
 
+// The tile (the k-th of its sequence's n) and head of a block whose tile was found by its number x / H alone: within a
+// sequence, blocks go through GROUP heads at a time, all tiles of those, so that what their tiles share stays in L2.
+template <int GROUP> __device__ __forceinline__ void regroup(int64_t x, int H, int n, int *k, int *head) {
+    const int local = int(x - (x / H - *k) * H);  // number of the block in its sequence
+    const int g = local / (n * GROUP), in = local - g * n * GROUP, width = min(GROUP, H - g * GROUP);
+    *k = in / width;
+    *head = g * GROUP + in % width;
+}
+
 // Four elements at p (16 bytes of float32, 8 of bf16) as float32.
 template <typename T> __device__ __forceinline__ float4 load4(const T *p);
 template <> __device__ __forceinline__ float4 load4<float>(const float *p) { return *reinterpret_cast<const float4 *>(p); }
