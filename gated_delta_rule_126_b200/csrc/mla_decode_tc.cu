@@ -123,7 +123,6 @@ decode_tc_kernel(const __grid_constant__ Maps maps, const MlaDecodeArgs a, const
         ptx::tmem_relinquish();
     }
     const MlaRun run = mla_find_run<kThreads>(a, group, shape.groups, kKeys, buf);
-    mla_empty_sequences<__nv_bfloat16, kThreads>(a, group, shape.groups, r0, rows);
     if (tid == 0) static_cast<MlaJoin *>(a.workspace)[blockIdx.x].parts = 0;
     ptx::tc_fence_before();
     __syncthreads();
@@ -220,8 +219,8 @@ decode_tc_kernel(const __grid_constant__ Maps maps, const MlaDecodeArgs a, const
             const uint64_t q_desc = ptx::sdesc_sw128(base + L.q), p_desc = ptx::sdesc_sw128(base + L.p),
                            k_desc = ptx::sdesc_sw128(base), v_desc = ptx::sdesc_sw128_mn(base, 8192, 1024);
             if (tc::elect()) {
-                // Scores run up to two tiles ahead of O's products (two S buffers).  Whichever of the two has its
-                // input goes; a tile's scores, once begun, take its slots as they arrive.
+                // Scores run up to two tiles ahead of O's products (two S buffers) and take a tile's slots as they arrive;
+                // O's products go as soon as their P is there, between two slots of scores if need be.
                 MlaWalk ws(run), wp(run);
                 bool more = ws.next(a, kKeys, run), ok = true;
                 wp.next(a, kKeys, run);
@@ -229,69 +228,91 @@ decode_tc_kernel(const __grid_constant__ Maps maps, const MlaDecodeArgs a, const
                 int s_tile = ws.t0, p_tile = wp.t0;
                 uint32_t s_item = 0, n_s = 0, n_pv = 0;
                 const uint32_t n_all = uint32_t(run.end - run.start);
-                long long since = clock64();
-                while (n_pv < n_all) {
-                    bool idle = true;
-                    if (more && n_s - n_pv < 2 && (s_tile != ws.t0 || tc::ready(&mi.q_full, s_item & 1)) &&
-                        tc::ready(&mi.full[s_ring.slot], s_ring.round & 1)) {
-                        const uint32_t to = tmem + Tm<RB>::kS + (n_s & 1) * 64;
-                        uint64_t qd = q_desc;
-                        for (int i = 0; i < blocks; ++i, s_ring.next(L.slots), qd = tc::moved(qd, RB * 256)) {
-                            if (!(ok = tc::wait(&mi.full[s_ring.slot], s_ring.round & 1, dead))) break;
-                            ptx::tc_fence_after();
-                            const uint64_t kd = tc::moved(k_desc, s_ring.slot * kSlotBytes);
-                            ptx::mma_ss(to, qd, kd, kIdS, i > 0);
+                auto output = [&]() {  // O's product of the next tile, if its P is there
+                    if (n_s == n_pv || !tc::ready(&mi.p_full, n_pv & 1)) return;
+                    ptx::tc_fence_after();
+                    const uint32_t more_o = p_tile > wp.t0;
+                    for (int i = 0; i < blocks; ++i, p_ring.next(L.slots)) {
+                        const uint64_t vd = tc::moved(v_desc, p_ring.slot * kSlotBytes);
+                        ptx::mma_ss(tmem + i * RB, vd, p_desc, kIdO, more_o);
 #pragma unroll
-                            for (int k = 1; k < 8; ++k)
-                                ptx::mma_ss(to, tc::moved(qd, (k >> 2) * (RB * 128) + 32 * (k & 3)),
-                                            tc::moved(kd, (k >> 2) * 8192 + 32 * (k & 3)), kIdS, 1);
-                        }
-                        if (ok && L.rope) {
-                            ok = tc::wait(&mi.rope_full[s_rope.slot], s_rope.round & 1, dead);
-                            ptx::tc_fence_after();
-                            const uint64_t kd = tc::moved(k_desc, L.rope_at + s_rope.slot * kRopeBytes);
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) ptx::mma_ss(to, tc::moved(qd, 32 * k), tc::moved(kd, 32 * k), kIdS, 1);
-                            ptx::mma_commit(&mi.rope_empty[s_rope.slot]);
-                            s_rope.next(L.rope);
-                        }
-                        if (!ok) break;
-                        ptx::mma_commit(&mi.s_full[n_s & 1]);
-                        ++n_s;
-                        if (++s_tile == ws.t1) {
-                            ptx::mma_commit(&mi.q_empty);
-                            more = ws.next(a, kKeys, run);
-                            s_tile = ws.t0;
-                            ++s_item;
-                        }
-                        idle = false;
+                        for (int k = 1; k < 4; ++k)
+                            ptx::mma_ss(tmem + i * RB, tc::moved(vd, 2048 * k), tc::moved(p_desc, 32 * k), kIdO, 1);
+                        ptx::mma_commit(&mi.empty[p_ring.slot]);
                     }
-                    if (n_s > n_pv && tc::ready(&mi.p_full, n_pv & 1)) {
+                    ptx::mma_commit(&mi.pv_done);
+                    ++n_pv;
+                    if (++p_tile == wp.t1) {
+                        wp.next(a, kKeys, run);
+                        p_tile = wp.t0;
+                    }
+                };
+                auto arrived = [&](uint64_t *bar, uint32_t parity) {  // waits, giving O's products their turn
+                    if (tc::ready(bar, parity)) return true;
+                    const long long t0 = clock64();
+                    while (!tc::ready(bar, parity)) {
+                        output();
+                        if (*dead) return false;
+                        if (clock64() - t0 > tc::kWaitCycles) {
+                            *dead = 1;
+                            atomicExch(&mla_fault, 1u);
+                            return false;
+                        }
+                    }
+                    return true;
+                };
+                while (ok && more) {
+                    if (s_tile == ws.t0 && !(ok = arrived(&mi.q_full, s_item & 1))) break;
+                    const long long t0 = clock64();
+                    while (n_s - n_pv >= 2) {  // both S buffers in use
+                        output();
+                        if (*dead || clock64() - t0 > tc::kWaitCycles) {
+                            if (!*dead) atomicExch(&mla_fault, 1u);
+                            *dead = 1;
+                            ok = false;
+                            break;
+                        }
+                    }
+                    if (!ok) break;
+                    const uint32_t to = tmem + Tm<RB>::kS + (n_s & 1) * 64;
+                    uint64_t qd = q_desc;
+                    for (int i = 0; i < blocks; ++i, s_ring.next(L.slots), qd = tc::moved(qd, RB * 256)) {
+                        if (!(ok = arrived(&mi.full[s_ring.slot], s_ring.round & 1))) break;
                         ptx::tc_fence_after();
-                        const uint32_t more_o = p_tile > wp.t0;
-                        for (int i = 0; i < blocks; ++i, p_ring.next(L.slots)) {
-                            const uint64_t vd = tc::moved(v_desc, p_ring.slot * kSlotBytes);
-                            ptx::mma_ss(tmem + i * RB, vd, p_desc, kIdO, more_o);
+                        const uint64_t kd = tc::moved(k_desc, s_ring.slot * kSlotBytes);
+                        ptx::mma_ss(to, qd, kd, kIdS, i > 0);
 #pragma unroll
-                            for (int k = 1; k < 4; ++k)
-                                ptx::mma_ss(tmem + i * RB, tc::moved(vd, 2048 * k), tc::moved(p_desc, 32 * k), kIdO, 1);
-                            ptx::mma_commit(&mi.empty[p_ring.slot]);
-                        }
-                        ptx::mma_commit(&mi.pv_done);
-                        ++n_pv;
-                        if (++p_tile == wp.t1) {
-                            wp.next(a, kKeys, run);
-                            p_tile = wp.t0;
-                        }
-                        idle = false;
+                        for (int k = 1; k < 8; ++k)
+                            ptx::mma_ss(to, tc::moved(qd, (k >> 2) * (RB * 128) + 32 * (k & 3)),
+                                        tc::moved(kd, (k >> 2) * 8192 + 32 * (k & 3)), kIdS, 1);
                     }
-                    if (!idle) {
-                        since = clock64();
-                    } else if (*dead || clock64() - since > tc::kWaitCycles) {
+                    if (ok && L.rope) {
+                        ok = arrived(&mi.rope_full[s_rope.slot], s_rope.round & 1);
+                        ptx::tc_fence_after();
+                        const uint64_t kd = tc::moved(k_desc, L.rope_at + s_rope.slot * kRopeBytes);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) ptx::mma_ss(to, tc::moved(qd, 32 * k), tc::moved(kd, 32 * k), kIdS, 1);
+                        ptx::mma_commit(&mi.rope_empty[s_rope.slot]);
+                        s_rope.next(L.rope);
+                    }
+                    if (!ok) break;
+                    ptx::mma_commit(&mi.s_full[n_s & 1]);
+                    ++n_s;
+                    if (++s_tile == ws.t1) {
+                        ptx::mma_commit(&mi.q_empty);
+                        more = ws.next(a, kKeys, run);
+                        s_tile = ws.t0;
+                        ++s_item;
+                    }
+                    output();
+                }
+                const long long t0 = clock64();
+                while (ok && n_pv < n_all) {  // the last tiles
+                    output();
+                    if (*dead || clock64() - t0 > 2 * tc::kWaitCycles) {
                         if (!*dead) atomicExch(&mla_fault, 1u);
                         *dead = 1;
                         ok = false;
-                        break;
                     }
                 }
                 if (!ok) {  // an error: the products in flight end before TMEM goes away
@@ -472,6 +493,7 @@ decode_tc_kernel(const __grid_constant__ Maps maps, const MlaDecodeArgs a, const
             }
         }
     }
+    mla_empty_sequences<__nv_bfloat16, kThreads>(a, group, shape.groups, r0, rows);
     ptx::tc_fence_before();
     __syncthreads();
     if (warp == 4) {
