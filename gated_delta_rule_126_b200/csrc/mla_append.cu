@@ -11,7 +11,8 @@
 namespace kda {
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kThreads = 64;
+constexpr int kAhead = 2;  // items of the queries that a thread loads before the walk
 constexpr int kMaxLatent = 512;
 constexpr int kMaxRope = 64;
 
@@ -54,10 +55,21 @@ template <typename T, int V> struct Item {
         b.load(src + second(item, half, interleaved));
     }
     __device__ __forceinline__ void turn(int item, bool interleaved, const float2 *cs) {
+        float2 c[V];  // cos and sin of this item's pairs
+        if constexpr (V == 1) {
+            c[0] = cs[item];
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; i += 2) {
+                const float4 w = *reinterpret_cast<const float4 *>(cs + V * item + i);
+                c[i] = make_float2(w.x, w.y);
+                c[i + 1] = make_float2(w.z, w.w);
+            }
+        }
         if (!interleaved || V == 1) {
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                const float2 w = cs[V * item + i];
+                const float2 w = c[i];
                 const float x = a.get(i), y = b.get(i);
                 a.put(i, x * w.x - y * w.y);
                 b.put(i, x * w.y + y * w.x);
@@ -65,7 +77,7 @@ template <typename T, int V> struct Item {
         } else {
 #pragma unroll
             for (int i = 0; i < V / 2; ++i) {
-                const float2 w = cs[V * item + i], u = cs[V * item + V / 2 + i];
+                const float2 w = c[i], u = c[V / 2 + i];
                 float x = a.get(2 * i), y = a.get(2 * i + 1);
                 a.put(2 * i, x * w.x - y * w.y);
                 a.put(2 * i + 1, x * w.y + y * w.x);
@@ -98,8 +110,8 @@ __device__ __forceinline__ int find_sequence(const int32_t *cu, int num_seqs, in
 
 // The inputs' loads come first: they need only t, and the way to the cache row (offsets, past,
 // page) takes several dependent loads.
-template <typename T, int V> __global__ void __launch_bounds__(kThreads, 12) append_kernel(const MlaAppendArgs a) {
-    __shared__ float2 cs[kMaxRope / 2];
+template <typename T, int V> __global__ void __launch_bounds__(kThreads, 20) append_kernel(const MlaAppendArgs a) {
+    __shared__ alignas(16) float2 cs[kMaxRope / 2];
     __shared__ float warp_sum[kThreads / 32];
     __shared__ int64_t place;  // of the cache row, in elements; -1: none, -2: no token
     const int64_t t = blockIdx.x;
@@ -114,12 +126,19 @@ template <typename T, int V> __global__ void __launch_bounds__(kThreads, 12) app
         const int j = (i * kThreads + tid) * V;
         if (j < a.dc) x[i].load(c_row + j);
     }
-    // the first queries' item of this thread; the last threads take the key part's
-    Item<T, V> q, k;
+    // the first items of the queries of this thread; the last threads take the key part's
+    Item<T, V> q[kAhead], k;
+    int head[kAhead], item[kAhead];
     const T *q_row = static_cast<const T *>(a.q_rope) + t * a.q_st;
     T *q_to = static_cast<T *>(a.q_out) + t * a.qo_st;
     const int k_item = kThreads - 1 - tid;
-    if (tid < q_items) q.load(q_row + tid / items * a.q_sh, tid % items, half, a.interleaved);
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+        const int w = tid + i * kThreads;
+        head[i] = items ? w / items : 0;
+        item[i] = w - head[i] * items;
+        if (w < q_items) q[i].load(q_row + head[i] * a.q_sh, item[i], half, a.interleaved);
+    }
     if (k_item < items) k.load(static_cast<const T *>(a.k_rope) + t * a.k_rope_stride, k_item, half, a.interleaved);
 
     if (tid < 32) {  // the walk to the cache row and the angles, by the first warp for all
@@ -157,7 +176,7 @@ template <typename T, int V> __global__ void __launch_bounds__(kThreads, 12) app
     __syncthreads();
     if (place == -2) return;  // behind the last sequence
     T *row = place >= 0 ? static_cast<T *>(a.cache) + place : nullptr;
-    ss = warp_sum[0] + warp_sum[1] + warp_sum[2] + warp_sum[3];
+    ss = warp_sum[0] + warp_sum[1];
     if (a.norm_weight) {
         const float r = 1.f / sqrtf(ss / float(a.dc) + a.eps);
 #pragma unroll
@@ -191,11 +210,17 @@ template <typename T, int V> __global__ void __launch_bounds__(kThreads, 12) app
         if (row) k.store(row + a.dc, k_item, half, a.interleaved);
         if (a.k_rope_out) k.store(static_cast<T *>(a.k_rope_out) + t * a.dr, k_item, half, a.interleaved);
     }
-    for (int w = tid; w < q_items; w += kThreads) {
-        const int h = w / items, item = w % items;
-        if (w != tid) q.load(q_row + h * a.q_sh, item, half, a.interleaved);
-        if (turn) q.turn(item, a.interleaved, cs);
-        q.store(q_to + h * a.qo_sh, item, half, a.interleaved);
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+        if (tid + i * kThreads < q_items) {
+            if (turn) q[i].turn(item[i], a.interleaved, cs);
+            q[i].store(q_to + head[i] * a.qo_sh, item[i], half, a.interleaved);
+        }
+    for (int w = tid + kAhead * kThreads; w < q_items; w += kThreads) {
+        const int h = w / items, at = w - h * items;
+        q[0].load(q_row + h * a.q_sh, at, half, a.interleaved);
+        if (turn) q[0].turn(at, a.interleaved, cs);
+        q[0].store(q_to + h * a.qo_sh, at, half, a.interleaved);
     }
 }
 
