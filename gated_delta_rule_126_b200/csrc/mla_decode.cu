@@ -220,7 +220,7 @@ template <typename T> cudaError_t launch_simt(const MlaDecodeArgs &a, const MlaD
 }
 
 MlaDecodeShape simt_shape(int n, int H) {  // two blocks fit on an SM
-    const int tiles = (n * H + kRows - 1) / kRows, groups = 2 * device_sm_count() / tiles;
+    const int tiles = n > 0 ? (n * H + kRows - 1) / kRows : 1, groups = 2 * device_sm_count() / tiles;
     return MlaDecodeShape{false, kRows, tiles, groups > 1 ? groups : 1};
 }
 

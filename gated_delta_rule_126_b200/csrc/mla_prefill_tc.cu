@@ -108,102 +108,102 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
 
     if (warp >= 8) {
         ptx::regs_dec<kRegsOther>();
-      if (warp == 9) {
-        // -------------------------------------------------------------------- loads
-        if (tc::elect() && blocks > 0) {
-            auto load_q = [&](int t) {
-                if (n[t] == 0) return;
-                ptx::mbar_arrive_expect_tx(&mi.q_full[t], kc * kSlotBytes);
-                for (int c = 0; c < kc; ++c)
-                    tc::tma_load_3d(base + (3 * t + c) * kSlotBytes, &maps.q, &mi.q_full[t], 64 * c, h, q0 + i0 + t * kRows);
-            };
-            bool ok = true;
-            int idx = 0;
-            load_q(0);
-            for (int j = 0; ok && j < blocks; ++j)
-                for (int c = 0; c < per; ++c, ++idx) {
-                    const int slot = idx % kSlots;
-                    if (idx >= kSlots) {  // what was in the slot: keys or values of block g
-                        const int g = (idx - kSlots) / per;
-                        uint64_t *free = (idx - kSlots) % per < kc ? &mi.k_free[g & 1] : &mi.v_free[g & 1];
-                        if (!(ok = tc::wait(free, (g >> 1) & 1, dead))) break;
+        if (warp == 9) {
+            // -------------------------------------------------------------------- loads
+            if (tc::elect() && blocks > 0) {
+                auto load_q = [&](int t) {
+                    if (n[t] == 0) return;
+                    ptx::mbar_arrive_expect_tx(&mi.q_full[t], kc * kSlotBytes);
+                    for (int c = 0; c < kc; ++c)
+                        tc::tma_load_3d(base + (3 * t + c) * kSlotBytes, &maps.q, &mi.q_full[t], 64 * c, h, q0 + i0 + t * kRows);
+                };
+                bool ok = true;
+                int idx = 0;
+                load_q(0);
+                for (int j = 0; ok && j < blocks; ++j)
+                    for (int c = 0; c < per; ++c, ++idx) {
+                        const int slot = idx % kSlots;
+                        if (idx >= kSlots) {  // what was in the slot: keys or values of block g
+                            const int g = (idx - kSlots) / per;
+                            uint64_t *free = (idx - kSlots) % per < kc ? &mi.k_free[g & 1] : &mi.v_free[g & 1];
+                            if (!(ok = tc::wait(free, (g >> 1) & 1, dead))) break;
+                        }
+                        const uint32_t dst = base + kOffRing + slot * kSlotBytes;
+                        ptx::mbar_arrive_expect_tx(&mi.full[slot], kSlotBytes);
+                        if (c < 2) {
+                            tc::tma_load_3d(dst, &maps.k, &mi.full[slot], 64 * c, h, k0 + j * 128);
+                        } else if (c < kc) {
+                            tc::tma_load_2d(dst, &maps.kr, &mi.full[slot], 0, k0 + j * 128);
+                        } else {
+                            const int key = k0 + j * 128 + (c - kc) * 64;
+                            tc::tma_load_3d(dst, &maps.v, &mi.full[slot], 0, h, key);
+                            tc::tma_load_3d(dst + 8192, &maps.v, &mi.full[slot], 64, h, key);
+                        }
+                        if (idx == kc - 1) load_q(1);
                     }
-                    const uint32_t dst = base + kOffRing + slot * kSlotBytes;
-                    ptx::mbar_arrive_expect_tx(&mi.full[slot], kSlotBytes);
-                    if (c < 2) {
-                        tc::tma_load_3d(dst, &maps.k, &mi.full[slot], 64 * c, h, k0 + j * 128);
-                    } else if (c < kc) {
-                        tc::tma_load_2d(dst, &maps.kr, &mi.full[slot], 0, k0 + j * 128);
-                    } else {
-                        const int key = k0 + j * 128 + (c - kc) * 64;
-                        tc::tma_load_3d(dst, &maps.v, &mi.full[slot], 0, h, key);
-                        tc::tma_load_3d(dst + 8192, &maps.v, &mi.full[slot], 64, h, key);
+                if (!ok) {  // an error: the copies in flight land before the block ends
+                    for (int i = max(0, idx - kSlots); i < idx; ++i)
+                        ptx::mbar_wait_bounded(&mi.full[i % kSlots], (i / kSlots) & 1, tc::kWaitCycles);
+                    for (int t = 0; t < 2; ++t)
+                        if (n[t]) ptx::mbar_wait_bounded(&mi.q_full[t], 0, tc::kWaitCycles);
+                }
+            }
+        } else if (warp == 8) {
+            // -------------------------------------------------------------------- products
+            if (tc::elect() && blocks > 0) {
+                constexpr uint32_t kIdS = tc::idesc(128, 128, false, false), kIdO = tc::idesc(128, 128, false, true);
+                const uint64_t k_desc = ptx::sdesc_sw128(base), v_desc = ptx::sdesc_sw128_mn(base + kOffRing, 8192, 1024);
+                auto qk = [&](int t, int j) {
+                    uint64_t qd = tc::moved(k_desc, 3 * t * kSlotBytes);
+                    for (int c = 0; c < kc; ++c, qd = tc::moved(qd, kSlotBytes)) {
+                        const int idx = j * per + c, slot = idx % kSlots;
+                        if (!tc::wait(&mi.full[slot], (idx / kSlots) & 1, dead)) return false;
+                        ptx::tc_fence_after();
+                        const uint64_t kd = tc::moved(k_desc, kOffRing + slot * kSlotBytes);
+                        ptx::mma_ss(tmem + t * 128, qd, kd, kIdS, c > 0);
+#pragma unroll
+                        for (int k = 1; k < 4; ++k)
+                            ptx::mma_ss(tmem + t * 128, tc::moved(qd, 32 * k), tc::moved(kd, 32 * k), kIdS, 1);
                     }
-                    if (idx == kc - 1) load_q(1);
-                }
-            if (!ok) {  // an error: the copies in flight land before the block ends
-                for (int i = max(0, idx - kSlots); i < idx; ++i)
-                    ptx::mbar_wait_bounded(&mi.full[i % kSlots], (i / kSlots) & 1, tc::kWaitCycles);
-                for (int t = 0; t < 2; ++t)
-                    if (n[t]) ptx::mbar_wait_bounded(&mi.q_full[t], 0, tc::kWaitCycles);
-            }
-        }
-      } else if (warp == 8) {
-        // -------------------------------------------------------------------- products
-        if (tc::elect() && blocks > 0) {
-            constexpr uint32_t kIdS = tc::idesc(128, 128, false, false), kIdO = tc::idesc(128, 128, false, true);
-            const uint64_t k_desc = ptx::sdesc_sw128(base), v_desc = ptx::sdesc_sw128_mn(base + kOffRing, 8192, 1024);
-            auto qk = [&](int t, int j) {
-                uint64_t qd = tc::moved(k_desc, 3 * t * kSlotBytes);
-                for (int c = 0; c < kc; ++c, qd = tc::moved(qd, kSlotBytes)) {
-                    const int idx = j * per + c, slot = idx % kSlots;
-                    if (!tc::wait(&mi.full[slot], (idx / kSlots) & 1, dead)) return false;
-                    ptx::tc_fence_after();
-                    const uint64_t kd = tc::moved(k_desc, kOffRing + slot * kSlotBytes);
-                    ptx::mma_ss(tmem + t * 128, qd, kd, kIdS, c > 0);
+                    ptx::mma_commit(&mi.s_full[t]);
+                    return true;
+                };
+                auto pv = [&](int t, int j) {
+                    for (int c = 0; c < 2; ++c) {
+                        if (!tc::wait(&mi.p_full[t][c], j & 1, dead)) return false;
+                        const int idx = j * per + kc + c, slot = idx % kSlots;
+                        if (!tc::wait(&mi.full[slot], (idx / kSlots) & 1, dead)) return false;
+                        ptx::tc_fence_after();
+                        const uint64_t vd = tc::moved(v_desc, slot * kSlotBytes);
+                        const uint32_t pt = tmem + t * 128 + c * 32;
+                        ptx::mma_ts(tmem + kTmO + t * 128, pt, vd, kIdO, j + c > 0);
 #pragma unroll
-                    for (int k = 1; k < 4; ++k)
-                        ptx::mma_ss(tmem + t * 128, tc::moved(qd, 32 * k), tc::moved(kd, 32 * k), kIdS, 1);
+                        for (int k = 1; k < 4; ++k)
+                            ptx::mma_ts(tmem + kTmO + t * 128, pt + 8 * k, tc::moved(vd, 2048 * k), kIdO, 1);
+                    }
+                    ptx::mma_commit(&mi.pv_done[t]);
+                    return true;
+                };
+                bool ok = true;
+                for (int t = 0; ok && t < 2; ++t)
+                    if (n[t]) ok = tc::wait(&mi.q_full[t], 0, dead) && qk(t, 0);
+                if (ok) ptx::mma_commit(&mi.k_free[0]);
+                for (int j = 0; ok && j < blocks; ++j) {
+                    if (j < n[0]) ok = pv(0, j);
+                    if (ok && j + 1 < n[0]) ok = qk(0, j + 1);
+                    if (ok && j < n[1]) ok = pv(1, j);
+                    if (!ok) break;
+                    ptx::mma_commit(&mi.v_free[j & 1]);
+                    if (j + 1 < n[1]) ok = qk(1, j + 1);
+                    if (ok && j + 1 < blocks) ptx::mma_commit(&mi.k_free[(j + 1) & 1]);
                 }
-                ptx::mma_commit(&mi.s_full[t]);
-                return true;
-            };
-            auto pv = [&](int t, int j) {
-                for (int c = 0; c < 2; ++c) {
-                    if (!tc::wait(&mi.p_full[t][c], j & 1, dead)) return false;
-                    const int idx = j * per + kc + c, slot = idx % kSlots;
-                    if (!tc::wait(&mi.full[slot], (idx / kSlots) & 1, dead)) return false;
-                    ptx::tc_fence_after();
-                    const uint64_t vd = tc::moved(v_desc, slot * kSlotBytes);
-                    const uint32_t pt = tmem + t * 128 + c * 32;
-                    ptx::mma_ts(tmem + kTmO + t * 128, pt, vd, kIdO, j + c > 0);
-#pragma unroll
-                    for (int k = 1; k < 4; ++k)
-                        ptx::mma_ts(tmem + kTmO + t * 128, pt + 8 * k, tc::moved(vd, 2048 * k), kIdO, 1);
+                if (!ok) {  // an error: the products in flight end before TMEM goes away
+                    ptx::mma_commit(&mi.drain);
+                    ptx::mbar_wait_bounded(&mi.drain, 0, tc::kWaitCycles);
                 }
-                ptx::mma_commit(&mi.pv_done[t]);
-                return true;
-            };
-            bool ok = true;
-            for (int t = 0; ok && t < 2; ++t)
-                if (n[t]) ok = tc::wait(&mi.q_full[t], 0, dead) && qk(t, 0);
-            if (ok) ptx::mma_commit(&mi.k_free[0]);
-            for (int j = 0; ok && j < blocks; ++j) {
-                if (j < n[0]) ok = pv(0, j);
-                if (ok && j + 1 < n[0]) ok = qk(0, j + 1);
-                if (ok && j < n[1]) ok = pv(1, j);
-                if (!ok) break;
-                ptx::mma_commit(&mi.v_free[j & 1]);
-                if (j + 1 < n[1]) ok = qk(1, j + 1);
-                if (ok && j + 1 < blocks) ptx::mma_commit(&mi.k_free[(j + 1) & 1]);
             }
-            if (!ok) {  // an error: the products in flight end before TMEM goes away
-                ptx::mma_commit(&mi.drain);
-                ptx::mbar_wait_bounded(&mi.drain, 0, tc::kWaitCycles);
-            }
+            __syncwarp();
         }
-        __syncwarp();
-      }
     } else {
         // -------------------------------------------------------------------- softmax and output
         ptx::regs_inc<kRegsSoftmax>();

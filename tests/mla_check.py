@@ -7,7 +7,7 @@ is rounded once.  So, element by element, with |.| taken inside the sums,
 
     |o  - ref| <= u |ref| + u sum_j P |v|                      + f
     |dv - ref| <= u |ref| + u sum_i P |dO|                     + f
-    |dq - ref| <= u |ref| + sum_j (u |dS| + scale P E) |k|     + f      E = error of delta = sum_c |dO| |o - ref|
+    |dq - ref| <= u |ref| + sum_j (u |dS| + |scale| P E) |k|     + f      E = error of delta = sum_c |dO| |o - ref|
     |dk - ref| <= the same with q
 
 f is float32's share: products of d terms are off by about sqrt(d) 2^-23 of their absolute
@@ -92,8 +92,9 @@ def check_backward(a, dO, g, causal=True, scale=None):
             ds = np.abs(p * (dp - (p * dp).sum(1, keepdims=True)) * scale)
             o_err = u * np.abs(p @ v) + (u + F) * (p @ np.abs(v))
             E = (np.abs(d) * o_err).sum(1, keepdims=True)
-            wide = p * scale * (np.abs(d) @ np.abs(v).T + (p * (np.abs(d) @ np.abs(v).T)).sum(1, keepdims=True))
-            e = (u + F) * ds + scale * p * E + F * wide
+            size = abs(scale)  # an error is at most the sum of absolute terms, scale's sign apart
+            wide = p * size * (np.abs(d) @ np.abs(v).T + (p * (np.abs(d) @ np.abs(v).T)).sum(1, keepdims=True))
+            e = (u + F) * ds + size * p * E + F * wide
             bound["dv"][ks, n] += (u + F) * (p.T @ np.abs(d))
             bound["dq"][qs, n] += e @ np.abs(k)
             dk = e.T @ np.abs(q)

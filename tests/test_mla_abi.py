@@ -62,6 +62,7 @@ def _decode(lib, **kw):
 def test_decode_refusals(lib):
     size = lib.mla_decode_workspace_size
     assert size(2, 1, 4, 512, 64, 1) > 0 and size(2, 1, 4, 513, 64, 1) == 0 and size(-1, 1, 4, 512, 64, 1) == 0
+    assert size(2, 0, 4, 512, 64, 1) > 0 and size(0, 0, 1, 1, 0, 0) > 0          # no tokens is a size like another
     assert size(1, 1, 0, 512, 64, 1) == 0 and size(1, 2, 40000, 512, 64, 1) == 0
     for bad in (dict(dt=5), dict(B=-1), dict(n=-1), dict(H=0), dict(dc=0), dict(dr=-1), dict(page=0), dict(pages=-1),
                 dict(mp=-1), dict(scale=float("inf")), dict(q=None), dict(o=None), dict(lens=None), dict(table=None),

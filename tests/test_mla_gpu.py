@@ -5,7 +5,7 @@ import numpy as np
 import pytest
 import torch
 
-from gated_delta_rule_126_b200 import mla_append, mla_backward, mla_decode, mla_prefill
+from gated_delta_rule_126_b200 import mla_append, mla_backward, mla_decode, mla_prefill, mla_status
 from oracle import mla
 from tests.mla_check import (U, check_backward, check_decode, check_lse, check_prefill, close, host, i32, offsets,
                              packed, pages)
@@ -13,6 +13,12 @@ from tests.mla_check import (U, check_backward, check_decode, check_lse, check_p
 pytestmark = pytest.mark.gpu
 BF, F32 = torch.bfloat16, torch.float32
 NAN = float("nan")
+
+
+@pytest.fixture(autouse=True)
+def no_kernel_flagged_an_error():
+    yield
+    assert mla_status() == 0
 
 
 def rnd(*s, dtype=F32, seed=0):
@@ -240,6 +246,87 @@ def test_strides_alignment_and_scale(dtype):
     o3, lse3 = mla_prefill(**odd, scale=0.2, want_lse=True)
     check_prefill(a, o3, lse3, scale=0.2)
     check_backward(a, dO, mla_backward(**odd, o=o3, lse=lse3, dO=dO, scale=0.2), scale=0.2)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("scale", [0.0, -0.1])
+def test_scales_that_are_not_positive(scale, dtype):
+    a, dO = packed([50, 140], [50, 200], 2, 128, 64, 128, dtype)
+    o, lse = mla_prefill(**a, scale=scale, want_lse=True)
+    check_prefill(a, o, lse, scale=scale)
+    check_backward(a, dO, mla_backward(**a, o=o, lse=lse, dO=dO, scale=scale), scale=scale)
+    table, n = pages([70, 200], 64)
+    cache, q = rnd(n, 64, 576, dtype=dtype), rnd(2, 2, 8, 576, dtype=dtype, seed=1)
+    o, lse = mla_decode(q, cache, i32(table), i32([70, 200]), 512, scale, want_lse=True)
+    check_decode(q, cache, table, [70, 200], 512, scale, o, lse)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_no_queries_or_no_keys(dtype):
+    a, dO = packed([0, 0], [5, 130], 2, 128, 64, 128, dtype)
+    o, lse = mla_prefill(**a, want_lse=True)
+    assert o.shape == (0, 2, 128)
+    g = mla_backward(**a, o=o, lse=lse, dO=dO)
+    assert all((g[n] == 0).all() for n in ("dk", "dv", "dk_rope")) and g["dk"].shape == (135, 2, 128)
+    a, dO = packed([3, 200], [0, 0], 2, 128, 64, 128, dtype)
+    o, lse = mla_prefill(**a, want_lse=True)
+    assert (o == 0).all() and torch.isneginf(lse).all()
+    g = mla_backward(**a, o=o, lse=lse, dO=dO)
+    assert (g["dq"] == 0).all() and g["dk"].shape == (0, 2, 128)
+    a, dO = packed([0], [0], 1, 128, 64, 128, dtype)
+    assert mla_prefill(**a)[0].shape == (0, 1, 128)
+    cache, table = rnd(3, 16, 576, dtype=dtype), i32([[0, 1]] * 2)
+    assert mla_decode(rnd(2, 0, 4, 576, dtype=dtype), cache, table, i32([3, 9]), 512, 0.1)[0].shape == (2, 0, 4, 512)
+    mla_append(rnd(0, 512, dtype=dtype), rnd(0, 64, dtype=dtype), cache, table, i32([3, 9]), i32([0, 0, 0]))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_heads_that_share_keys(dtype):
+    """Keys and values broadcast over the heads (stride 0): the gradients come back per head."""
+    a, dO = packed([60, 33], [60, 90], 1, 128, 64, 128, dtype)
+    q, dO = rnd(93, 3, 192, dtype=dtype, seed=3), rnd(93, 3, 128, dtype=dtype, seed=4)
+    shared = dict(a, q=q, k=a["k"].expand(-1, 3, -1), v=a["v"].expand(-1, 3, -1))
+    o, lse = mla_prefill(**shared, want_lse=True)
+    check_prefill(shared, o, lse)
+    check_backward(shared, dO, mla_backward(**shared, o=o, lse=lse, dO=dO))
+
+
+def test_two_streams_at_once():
+    """Calls that overlap on two streams, each with workspaces of its own, give what they give alone."""
+    table, n = pages([3000, 2500], 64)
+    cache, lens, table_d = rnd(n, 64, 576, dtype=BF), i32([3000, 2500]), i32(table)
+    q = [rnd(2, 1, 32, 576, dtype=BF, seed=s) for s in (1, 2)]
+    a, dO = packed([300, 200], [300, 200], 4, 128, 64, 128, BF)
+
+    def work(x):
+        d, _ = mla_decode(x, cache, table_d, lens, 512, 0.07)
+        o, lse = mla_prefill(**a, want_lse=True)
+        return [d, o, lse] + list(mla_backward(**a, o=o, lse=lse, dO=dO).values())
+
+    want = [work(x) for x in q]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(5):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i] = work(q[i])
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(x, y) for x, y in zip(want[i], got[i]))
+
+
+def test_many_short_sequences():
+    """More tiles than the host lists, and more sequences than a block has threads."""
+    lens = [int(x) for x in np.random.default_rng(5).integers(0, 40, 700)]
+    a, dO = packed(lens, lens, 2, 128, 64, 128, BF)
+    o, lse = mla_prefill(**a, want_lse=True)
+    check_prefill(a, o, lse)
+    check_backward(a, dO, mla_backward(**a, o=o, lse=lse, dO=dO))
+    table, n = pages(lens, 16)
+    cache, q = rnd(n, 16, 192, dtype=BF), rnd(700, 1, 4, 192, dtype=BF, seed=1)
+    o, lse = mla_decode(q, cache, i32(table), i32(lens), 128, 0.1, want_lse=True)
+    check_decode(q, cache, table, lens, 128, 0.1, o, lse)
 
 
 def test_gradient_against_differences():
