@@ -167,47 +167,80 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(const MlaDecodeArgs a,
     }
 }
 
-// Joins the parts of the sequences that are split over groups: o = sum_i e^(m_i - m) o_i / sum_i e^(m_i - m) l_i,
-// the parts in order.  One small block per (block of the main kernel, query row), four channels a
-// thread, so that a call's thousands of short rows are all resident at once.  It is launched while the main
-// kernel still runs and waits for its end on the device.
-constexpr int kJoinThreads = 128;
-template <typename T>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const MlaDecodeArgs a, const MlaDecodeShape shape) {
-    __shared__ float stat[kJoinThreads / 32];
-    const int x = blockIdx.x, row = blockIdx.y, tid = threadIdx.x;
-    const int R = a.n * a.H, r0 = (x % shape.row_tiles) * shape.row_tile;
+// Joins the parts of the sequences that are split over groups: o = sum_i e^(m_i - m) o_i / sum_i e^(m_i - m) l_i.
+// SPLIT = 1: one block of 128 threads, four channels each, per (block of the main kernel, query row); thousands of
+// rows in two or three parts each, as many sequences have them, are resident at once.  SPLIT = 8, for few
+// sequences in many parts: one block per (sequence, query row), eight sets of 128 threads that take the parts in
+// turn and are added in a fixed order.  The kernel is launched while the main one still runs and waits for its
+// end on the device.
+constexpr int kJoinLanes = 128;
+template <typename T, int SPLIT>
+__global__ void __launch_bounds__(kJoinLanes * SPLIT) join_kernel(const MlaDecodeArgs a, const MlaDecodeShape shape) {
+    constexpr int kWarps = kJoinLanes * SPLIT / 32;
+    __shared__ float stat[kWarps], sums[SPLIT];
+    __shared__ float acc[SPLIT][SPLIT > 1 ? 4 * kJoinLanes : 1];
+    const int row = blockIdx.y, tid = threadIdx.x, lane = tid % kJoinLanes, set = tid / kJoinLanes;
+    const int R = a.n * a.H, rt = blockIdx.x % shape.row_tiles, r0 = rt * shape.row_tile;
     if (r0 + row >= R) return;
+    int x = blockIdx.x;  // the block of the main kernel in whose run the sequence begins
+    if constexpr (SPLIT > 1) {
+        const int b = blockIdx.x / shape.row_tiles;
+        int64_t before = 0, total = 0;
+        for (int i = 0; i < a.B; ++i) {
+            const int nt = (mla_len(a, i) + shape.key_tile - 1) / shape.key_tile;
+            before += i < b ? nt : 0;
+            total += nt;
+        }
+        if (mla_len(a, b) == 0) return;
+        x = mla_group_of(before, total, int(total < shape.groups ? total : shape.groups)) * shape.row_tiles + rt;
+    }
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const MlaJoin j = static_cast<const MlaJoin *>(a.workspace)[x];
-    if (j.parts == 0) return;
-    const float *slots = reinterpret_cast<const float *>(static_cast<const char *>(a.workspace) + mla_meta_bytes(gridDim.x));
+    if (j.parts == 0 || (SPLIT > 1 && j.b != int(blockIdx.x) / shape.row_tiles)) return;
+    const float *slots = reinterpret_cast<const float *>(static_cast<const char *>(a.workspace) + mla_meta_bytes(shape.grid()));
     const size_t slot_floats = mla_slot_floats(shape.row_tile, a.dc);
     auto part = [&](int i) { return slots + size_t(i == 0 ? j.first_slot : 2 * (x + i * shape.row_tiles)) * slot_floats; };
     const int ml = shape.row_tile * a.dc + 2 * row;
     float m = -INFINITY;
-    for (int i = tid; i < j.parts; i += kJoinThreads) m = fmaxf(m, part(i)[ml]);
+    for (int i = tid; i < j.parts; i += kJoinLanes * SPLIT) m = fmaxf(m, part(i)[ml]);
 #pragma unroll
     for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
     if ((tid & 31) == 0) stat[tid >> 5] = m;
     __syncthreads();
-    m = fmaxf(fmaxf(stat[0], stat[1]), fmaxf(stat[2], stat[3]));
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) m = fmaxf(m, stat[w]);
     const float base = m == -INFINITY ? 0.f : m;
-    float l = 0.f, o[4] = {};  // channels tid + 128 e
+    float l = 0.f, o[4] = {};  // channels lane + 128 e
 #pragma unroll 4
-    for (int i = 0; i < j.parts; ++i) {
+    for (int i = set; i < j.parts; i += SPLIT) {
         const float *p = part(i);
         const float f = expf(p[ml] - base);
         l = fmaf(f, p[ml + 1], l);
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            if (tid + 128 * e < a.dc) o[e] = fmaf(f, p[row * a.dc + tid + 128 * e], o[e]);
+            if (lane + 128 * e < a.dc) o[e] = fmaf(f, p[row * a.dc + lane + 128 * e], o[e]);
+    }
+    if constexpr (SPLIT > 1) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[set][lane + 128 * e] = o[e];
+        if (lane == 0) sums[set] = l;
+        __syncthreads();
+        if (set > 0) return;
+        l = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] = 0.f;
+#pragma unroll
+        for (int s = 0; s < SPLIT; ++s) {
+            l += sums[s];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[e] += acc[s][lane + 128 * e];
+        }
     }
     const int64_t at = int64_t(j.b) * R + r0 + row;
     const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-        if (tid + 128 * e < a.dc) static_cast<T *>(a.o)[at * a.dc + tid + 128 * e] = from_f32<T>(o[e] * inv);
+        if (lane + 128 * e < a.dc) static_cast<T *>(a.o)[at * a.dc + lane + 128 * e] = from_f32<T>(o[e] * inv);
     if (a.lse && tid == 0) a.lse[at] = l == 0.f ? -INFINITY : m + logf(l);
 }
 
@@ -221,7 +254,7 @@ template <typename T> cudaError_t launch_simt(const MlaDecodeArgs &a, const MlaD
 
 MlaDecodeShape simt_shape(int n, int H) {  // two blocks fit on an SM
     const int tiles = n > 0 ? (n * H + kRows - 1) / kRows : 1, groups = 2 * device_sm_count() / tiles;
-    return MlaDecodeShape{false, kRows, tiles, groups > 1 ? groups : 1};
+    return MlaDecodeShape{false, kRows, kKeys, tiles, groups > 1 ? groups : 1};
 }
 
 size_t scratch(const MlaDecodeShape &s, int dc) {
@@ -243,18 +276,21 @@ cudaError_t launch_mla_decode(const MlaDecodeArgs &a, cudaStream_t st) {
                           : a.dtype == KDA_DTYPE_F32 ? launch_simt<float>(a, s, st)
                                                      : launch_simt<__nv_bfloat16>(a, s, st);
     if (e != cudaSuccess) return e;
-    const dim3 grid(s.grid(), s.row_tile < a.n * a.H ? s.row_tile : a.n * a.H);
+    // A sequence has groups / B parts on average, and one more.
+    const bool many = s.groups > 8 * a.B;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(kJoinThreads);
+    cfg.gridDim = dim3(many ? a.B * s.row_tiles : s.grid(), s.row_tile < a.n * a.H ? s.row_tile : a.n * a.H);
+    cfg.blockDim = dim3(many ? 8 * kJoinLanes : kJoinLanes);
     cfg.stream = st;
     cudaLaunchAttribute early{};
     early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     early.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &early;
     cfg.numAttrs = 1;
-    return a.dtype == KDA_DTYPE_F32 ? cudaLaunchKernelEx(&cfg, join_kernel<float>, a, s)
-                                    : cudaLaunchKernelEx(&cfg, join_kernel<__nv_bfloat16>, a, s);
+    if (a.dtype == KDA_DTYPE_F32)
+        return many ? cudaLaunchKernelEx(&cfg, join_kernel<float, 8>, a, s) : cudaLaunchKernelEx(&cfg, join_kernel<float, 1>, a, s);
+    return many ? cudaLaunchKernelEx(&cfg, join_kernel<__nv_bfloat16, 8>, a, s)
+                : cudaLaunchKernelEx(&cfg, join_kernel<__nv_bfloat16, 1>, a, s);
 }
 
 }  // namespace kda

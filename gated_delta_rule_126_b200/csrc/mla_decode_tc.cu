@@ -531,7 +531,7 @@ bool mla_decode_tc_supported(const MlaDecodeArgs &a) {
 // 32 rows where the call has no more (one token of up to 32 heads), else 64; one block per SM.
 MlaDecodeShape mla_decode_tc_shape(int n, int H) {
     const int R = n * H, rb = R <= 32 ? 32 : 64, tiles = R > 0 ? (R + rb - 1) / rb : 1, groups = device_sm_count() / tiles;
-    return MlaDecodeShape{true, rb, tiles, groups > 1 ? groups : 1};
+    return MlaDecodeShape{true, rb, kKeys, tiles, groups > 1 ? groups : 1};
 }
 
 cudaError_t launch_mla_decode_tc(const MlaDecodeArgs &a, const MlaDecodeShape &s, cudaStream_t st) {

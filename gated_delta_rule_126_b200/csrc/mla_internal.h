@@ -59,9 +59,10 @@ struct MlaArgs {  // mla_prefill and mla_backward
 struct MlaDecodeShape {
     bool tensor;    // tensor-core kernel
     int row_tile;   // query rows (token, head) a block works on
+    int key_tile;   // cache rows of a tile
     int row_tiles;  // blocks of a group
     int groups;
-    int grid() const { return groups * row_tiles; }
+    __host__ __device__ int grid() const { return groups * row_tiles; }
 };
 // Workspace of the larger of the two kernels' needs (the page size, which helps to choose, is not known here).
 size_t mla_decode_scratch(int B, int n, int H, int dc, int dr, kda_dtype_t dtype);
