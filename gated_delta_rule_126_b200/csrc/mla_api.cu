@@ -108,7 +108,7 @@ kda_status_t mla_append(const void *c, int64_t c_stride, const void *k_rope, int
 
 size_t mla_decode_workspace_size(int B, int n, int H, int d_latent, int d_rope, kda_dtype_t dtype) {
     if (check_decode_sizes(B, n, H, d_latent, d_rope, dtype) != KDA_OK) return 0;
-    return align256(kda::mla_decode_scratch(B, n, H, d_latent, d_rope, dtype));
+    return align256(kda::mla_decode_scratch(n, H, d_latent));
 }
 
 kda_status_t mla_decode(const void *q, kda_dtype_t dtype, const void *cache, int num_pages, int page_size,
@@ -123,7 +123,7 @@ kda_status_t mla_decode(const void *q, kda_dtype_t dtype, const void *cache, int
         return KDA_ERR_INVALID_ARG;
     if (!aligned(q, 16) || !aligned(cache, 16) || !aligned(o, 16)) return KDA_ERR_INVALID_ARG;
     if (!workspace || !aligned(workspace, 256) ||
-        workspace_bytes < kda::mla_decode_scratch(B, n, H, d_latent, d_rope, dtype))
+        workspace_bytes < kda::mla_decode_scratch(n, H, d_latent))
         return KDA_ERR_WORKSPACE;
     kda::MlaDecodeArgs a;
     a.q = q; a.cache = cache; a.dtype = dtype;

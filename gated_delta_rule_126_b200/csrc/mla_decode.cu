@@ -254,7 +254,7 @@ template <typename T> cudaError_t launch_simt(const MlaDecodeArgs &a, const MlaD
 
 MlaDecodeShape simt_shape(int n, int H) {  // two blocks fit on an SM
     const int tiles = n > 0 ? (n * H + kRows - 1) / kRows : 1, groups = 2 * device_sm_count() / tiles;
-    return MlaDecodeShape{false, kRows, kKeys, tiles, groups > 1 ? groups : 1};
+    return MlaDecodeShape{kRows, kKeys, tiles, groups > 1 ? groups : 1};
 }
 
 size_t scratch(const MlaDecodeShape &s, int dc) {
@@ -263,8 +263,7 @@ size_t scratch(const MlaDecodeShape &s, int dc) {
 
 }  // namespace
 
-size_t mla_decode_scratch(int B, int n, int H, int dc, int dr, kda_dtype_t dtype) {
-    (void)B, (void)dr, (void)dtype;
+size_t mla_decode_scratch(int n, int H, int dc) {
     const size_t x = scratch(simt_shape(n, H), dc), y = scratch(mla_decode_tc_shape(n, H), dc);
     return x > y ? x : y;
 }

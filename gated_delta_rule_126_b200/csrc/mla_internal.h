@@ -57,7 +57,6 @@ struct MlaArgs {  // mla_prefill and mla_backward
 
 // How mla_decode's work is cut (see mla_decode_plan.cuh).
 struct MlaDecodeShape {
-    bool tensor;    // tensor-core kernel
     int row_tile;   // query rows (token, head) a block works on
     int key_tile;   // cache rows of a tile
     int row_tiles;  // blocks of a group
@@ -65,7 +64,7 @@ struct MlaDecodeShape {
     __host__ __device__ int grid() const { return groups * row_tiles; }
 };
 // Workspace of the larger of the two kernels' needs (the page size, which helps to choose, is not known here).
-size_t mla_decode_scratch(int B, int n, int H, int dc, int dr, kda_dtype_t dtype);
+size_t mla_decode_scratch(int n, int H, int dc);
 bool mla_decode_tc_supported(const MlaDecodeArgs &a);
 MlaDecodeShape mla_decode_tc_shape(int n, int H);
 cudaError_t launch_mla_decode_tc(const MlaDecodeArgs &a, const MlaDecodeShape &s, cudaStream_t st);

@@ -34,7 +34,7 @@ constexpr uint32_t kSmem = kOffMisc + 1024 + 1024;  // misc, alignment
 constexpr uint32_t kTmemColumns = 512, kTmO = 256;
 constexpr float kLog2e = 1.4426950408889634f;
 // The maximum that scales P and O is raised only when the true one has outgrown it by 2^8:
-// sums stay exact enough in float32 (P <= 256), and rescaling O becomes rare.
+// P <= 256 costs a float32 sum nothing, and rescaling O becomes rare.
 constexpr float kLazy = 8.f;
 
 struct Misc {
