@@ -338,18 +338,27 @@ __global__ void __launch_bounds__(kThreads, 1) dkv_tc_kernel(const __grid_consta
 // 128 keys, dO in shared memory) the loads of the next but one held the products up (3,880 cycles a block instead of
 // 2,048), and with one and a half blocks of values those held up dP (2,450 a block of 96 instead of 1,630).
 // Shared memory: Q (3 chunks of 128 rows), three blocks of keys (3 chunks of 96 rows), two of values (2 chunks).
+//
+// A tile that sees at most kExact blocks goes through them twice: first it sums its rows' delta = sum_j P dP from the
+// unrounded P and dP, in float32, and leaves it for dk and dv, then it makes dq.  Delta from the forward pass's o carries the
+// roundings of o and of the P behind it, an error of up to 2^-9 |dO| |o|, which the products of a row carry in full.  With few keys
+// |o| is as large as |v|: over sequences of 64 tokens dq and dk were off by 1.7 times the error that rounding
+// the exact result makes, over pairs of tokens by 2.7 times; with an exact delta for the first 128 rows by 1.4 times at any length, which is
+// what rounding dS adds.  Rows that see many keys average the error away.
 constexpr int kKb = 96;
+constexpr int kExact = 3;
 constexpr uint32_t kKbChunk = kKb * 128;
 constexpr uint32_t kOffK = 3 * kChunk, kOffVq = kOffK + 9 * kKbChunk, kOffMiscQ = kOffVq + 4 * kKbChunk;
-constexpr uint32_t kDqSmem = kOffMiscQ + 1024 + 1024;
+constexpr uint32_t kDqSmem = kOffMiscQ + 2048 + 1024;
 constexpr uint32_t kTqDp = 96, kTqDq = 192, kTqDs = 384, kTqDo = 432;
 
 struct DqMisc {
-    uint64_t q_full, do_full, k_full[3], k_empty[3], v_full[2], v_empty[2], s_full, s_read, dp_full, dp_read, ds_full, done;
+    uint64_t q_full, do_full, k_full[3], k_empty[3], v_full[2], v_empty[2], s_full, s_read, dp_full, dp_read, ds_full, delta_full, done;
     int64_t find[kThreads / 32 + 2];
     uint32_t tmem, dead;
+    float delta[2][128];  // each warpgroup's share of the exact delta
 };
-static_assert(sizeof(DqMisc) <= 1024, "misc");
+static_assert(sizeof(DqMisc) <= 2048, "misc");
 static_assert(kDqSmem <= 232448, "shared memory");
 
 __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constant__ DkvMaps maps, const MlaArgs a,
@@ -364,6 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constan
         for (int i = 0; i < 2; ++i) ptx::mbar_init(&mi.v_full[i], 1), ptx::mbar_init(&mi.v_empty[i], 1);
         for (uint64_t *b : {&mi.q_full, &mi.s_full, &mi.dp_full, &mi.done}) ptx::mbar_init(b, 1);
         ptx::mbar_init(&mi.do_full, 256);
+        ptx::mbar_init(&mi.delta_full, 256);
         ptx::mbar_init(&mi.s_read, 256);
         ptx::mbar_init(&mi.dp_read, 256);
         ptx::mbar_init(&mi.ds_full, 256);
@@ -392,7 +402,10 @@ __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constan
     regroup<kHeads>(blockIdx.x, a.H, tiles, &order, &h);
     const int i0 = (tiles - 1 - order) * 128;
     auto key_end = [&](int i) { return a.causal ? max(0, min(pl.lk, i + 1 + pl.off)) : pl.lk; };
-    const int n = (key_end(min(i0 + 128, pl.lq) - 1) + kKb - 1) / kKb;
+    const int blocks = (key_end(min(i0 + 128, pl.lq) - 1) + kKb - 1) / kKb;
+    const int before = blocks <= kExact ? blocks : 0;  // steps of the pass that makes delta
+    const int n = before + blocks;                     // steps j, of block block_of(j)
+    auto block_of = [&](int j) { return j < before ? j : j - before; };
 
     if (warp == 9) {
         if (tc::elect() && n > 0) {
@@ -403,15 +416,15 @@ __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constan
                 const uint32_t dst = base + kOffK + (j % 3) * 3 * kKbChunk;
                 ptx::mbar_arrive_expect_tx(&mi.k_full[j % 3], kc * kKbChunk);
                 for (int c = 0; c < 2; ++c)
-                    tc::tma_load_3d(dst + c * kKbChunk, &maps.k, &mi.k_full[j % 3], 64 * c, h, pl.k0 + j * kKb);
-                if (a.dr) tc::tma_load_2d(dst + 2 * kKbChunk, &maps.kr, &mi.k_full[j % 3], 0, pl.k0 + j * kKb);
+                    tc::tma_load_3d(dst + c * kKbChunk, &maps.k, &mi.k_full[j % 3], 64 * c, h, pl.k0 + block_of(j) * kKb);
+                if (a.dr) tc::tma_load_2d(dst + 2 * kKbChunk, &maps.kr, &mi.k_full[j % 3], 0, pl.k0 + block_of(j) * kKb);
                 ++ks;
             };
             auto load_v = [&](int j) {
                 if (!ok || j >= n || (j >= 2 && !(ok = tc::wait(&mi.v_empty[j & 1], (j / 2 - 1) & 1, dead)))) return;
                 ptx::mbar_arrive_expect_tx(&mi.v_full[j & 1], 2 * kKbChunk);
                 for (int c = 0; c < 2; ++c)
-                    tc::tma_load_3d(base + kOffVq + (2 * (j & 1) + c) * kKbChunk, &maps.v, &mi.v_full[j & 1], 64 * c, h, pl.k0 + j * kKb);
+                    tc::tma_load_3d(base + kOffVq + (2 * (j & 1) + c) * kKbChunk, &maps.v, &mi.v_full[j & 1], 64 * c, h, pl.k0 + block_of(j) * kKb);
                 ++vs;
             };
             ptx::mbar_arrive_expect_tx(&mi.q_full, kc * kChunk);
@@ -478,9 +491,11 @@ __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constan
                 if (!ok || !(ok = tc::wait(&mi.ds_full, j & 1, dead))) break;
                 ptx::tc_fence_after();
                 const uint64_t kd = tc::moved(desc_mn, keys(j));
+                if (j >= before) {
 #pragma unroll
-                for (int k = 0; k < kKb / 16; ++k)
-                    ptx::mma_ts(tmem + kTqDq, tmem + kTqDs + 8 * k, tc::moved(kd, 2048 * k), id_q, j + k > 0);
+                    for (int k = 0; k < kKb / 16; ++k)
+                        ptx::mma_ts(tmem + kTqDq, tmem + kTqDs + 8 * k, tc::moved(kd, 2048 * k), id_q, j - before + k > 0);
+                }
                 ptx::mma_commit(&mi.k_empty[j % 3]);
             }
             ptx::mma_commit(&mi.done);
@@ -494,7 +509,8 @@ __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constan
         const float sl2 = a.scale * kLog2e;
         const int end = r < pl.lq ? key_end(r) : 0;
         const int64_t stat = int64_t(h) * a.Tq + pl.q0 + r;
-        const float lse2 = r < pl.lq ? a.lse2[stat] : 0.f, delta = r < pl.lq ? a.delta[stat] : 0.f;
+        const float lse2 = r < pl.lq ? a.lse2[stat] : 0.f;
+        float delta = r < pl.lq && before == 0 ? a.delta[stat] : 0.f;
         bool ok = true;
         if (n > 0) {  // dO into TMEM, half of the channels each
             const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.dO) + (int64_t(pl.q0 + r) * a.H + h) * 128 + 64 * half);
@@ -518,15 +534,15 @@ __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constan
             ptx::tmem_wait_ld();
             ptx::tc_fence_before();
             ptx::mbar_arrive(&mi.s_read);
-            const int seen = end - j * kKb - kHalf * half;  // columns of this half that the row sees
+            const int j0 = block_of(j) * kKb, seen = end - j0 - kHalf * half;  // columns of this half that the row sees
             const bool masked = __any_sync(0xffffffffu, seen < kHalf);
             float p[kHalf];
 #pragma unroll
             for (int c = 0; c < kHalf; ++c)
                 p[c] = ptx::ex2_approx(fmaf(__uint_as_float(c < 32 ? v[c & 31] : u[c & 15]), sl2, -lse2));
-            if (pl.lk - j * kKb < kKb) {
+            if (pl.lk - j0 < kKb) {
                 // key rows behind the sequence may hold anything: in dQ += dS K they have to be zero
-                const int from = max(0, pl.lk - j * kKb) * 8, per = kKb * 8 - from;
+                const int from = max(0, pl.lk - j0) * 8, per = kKb * 8 - from;
                 for (int x = tid; x < per * kc; x += 256)
                     tc::st_shared_v4(base + kOffK + ((j % 3) * 3 + x / per) * kKbChunk + (from + x % per) * 16, 0, 0, 0, 0);
                 ptx::fence_proxy_async_smem();
@@ -538,11 +554,27 @@ __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constan
             ptx::tmem_wait_ld();
             ptx::tc_fence_before();
             ptx::mbar_arrive(&mi.dp_read);
+            auto dp = [&](int c) { return __uint_as_float(c < 32 ? v[c & 31] : u[c & 15]); };
+            if (j < before) {
+                float add[2] = {0.f, 0.f};
+#pragma unroll
+                for (int c = 0; c < kHalf; ++c)
+                    if (c < seen) add[c & 1] = fmaf(p[c], dp(c), add[c & 1]);
+                delta += add[0] + add[1];
+                if (j + 1 == before) {  // both halves' shares
+                    mi.delta[half][row] = delta;
+                    ptx::mbar_arrive(&mi.delta_full);
+                    if (!(ok = tc::wait(&mi.delta_full, 0, dead))) break;
+                    delta = mi.delta[0][row] + mi.delta[1][row];
+                    if (half == 0 && r < pl.lq) a.delta[stat] = delta;
+                }
+                ptx::mbar_arrive(&mi.ds_full);
+                continue;
+            }
             uint32_t x[16], y[8];
 #pragma unroll
             for (int c = 0; c < kHalf; c += 2) {
-                float d0 = p[c] * (__uint_as_float(c < 32 ? v[c & 31] : u[c & 15]) - delta);
-                float d1 = p[c + 1] * (__uint_as_float(c < 32 ? v[(c + 1) & 31] : u[(c + 1) & 15]) - delta);
+                float d0 = p[c] * (dp(c) - delta), d1 = p[c + 1] * (dp(c + 1) - delta);
                 if (masked) {
                     if (c >= seen) d0 = 0.f;
                     if (c + 1 >= seen) d1 = 0.f;
@@ -611,12 +643,13 @@ cudaError_t launch_mla_backward_tc(const MlaArgs &a, cudaStream_t st) {
               tc::rows_map(&qs.v, a.v, 128, a.H, a.Tk, a.v_st, a.v_sh, kKb) &&
               (a.dr == 0 || (tc::rope_map(&kv.kr, a.k_rope, a.Tk, a.kr_st, 128) && tc::rope_map(&qs.kr, a.k_rope, a.Tk, a.kr_st, kKb)));
     if (!ok) return cudaErrorInvalidValue;
-    // first the first keys, which most queries see; then the last queries, which see most keys
-    const cudaError_t e = launch<dkv_tc_kernel>(kv, list_tiles(a.cu_k_host, a.num_seqs, 128, false),
-                                                count_tiles(a.cu_k_host, a.num_seqs, 128), kDkvSmem, a, st);
+    // dq first: it leaves the exact delta of the rows that see few keys.  Its tiles from the last queries, which see most
+    // keys, on; dk and dv's from the first keys, which most queries see.
+    const cudaError_t e = launch<dq_tc_kernel>(qs, list_tiles(a.cu_q_host, a.num_seqs, 128, true),
+                                               count_tiles(a.cu_q_host, a.num_seqs, 128), kDqSmem, a, st);
     if (e != cudaSuccess) return e;
-    return launch<dq_tc_kernel>(qs, list_tiles(a.cu_q_host, a.num_seqs, 128, true), count_tiles(a.cu_q_host, a.num_seqs, 128),
-                                kDqSmem, a, st);
+    return launch<dkv_tc_kernel>(kv, list_tiles(a.cu_k_host, a.num_seqs, 128, false), count_tiles(a.cu_k_host, a.num_seqs, 128),
+                                 kDkvSmem, a, st);
 }
 
 cudaError_t mla_backward_fault(cudaStream_t st, unsigned int *out) { return mla_fault_read(st, out); }

@@ -187,6 +187,20 @@ def test_prefill_and_backward(case, causal, dtype):
         assert t is None or torch.equal(t, again[name]), name
 
 
+@pytest.mark.parametrize("lens", [[2] * 60, [64] * 12, [300, 200, 33], [777]])
+def test_gradients_lose_no_precision_where_keys_are_few(lens):
+    """dq and dk against what rounding the exact result makes.  Rounding dS and rounding the output are two independent
+    roundings of the same kind, so the sum's error is sqrt(2) times one's: 1.5 asked (delta from the rounded output
+    would give up to 2.7)."""
+    a, dO = packed(lens, lens, 4, 128, 64, 128, BF, seed=7)
+    o, lse = mla_prefill(**a, want_lse=True)
+    g = mla_backward(**a, o=o, lse=lse, dO=dO)
+    ref = mla.backward(host(a["q"]), host(a["k"]), host(a["v"]), a["cu_q_host"], a["cu_k_host"], host(dO), k_rope=host(a["k_rope"]))
+    for n in ("dq", "dk", "dv"):
+        off = lambda x: np.linalg.norm(x - ref[n])
+        assert off(host(g[n])) <= 1.5 * off(host(torch.tensor(ref[n]).to(BF))), n
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_rows_outside_the_sequences(dtype):
     """Rows behind the last sequence hold NaN: nothing of them is read into a sum, nothing written."""
