@@ -15,6 +15,7 @@ namespace {
 constexpr int kT = 64;  // streamed rows of a tile
 constexpr int kThreads = 256;  // 16 x 16
 constexpr int kLdP = kT + 4;
+constexpr int kExact = 288;  // keys up to which a tile's delta is made from P and dP
 
 struct Rows {  // one sequence's place
     int q0, lq, k0, lk;
@@ -130,26 +131,38 @@ template <typename T, int I> __global__ void __launch_bounds__(kThreads, I == 2 
     }
 }
 
-// P and dS of one tile (queries I ty + i, keys tx + 16 j), from the recomputed scores: p = exp(s - lse),
-// ds = p (dp - delta) scale.
-template <int I, int J>
-__device__ __forceinline__ void tile_grads(const MlaArgs &a, const Rows &w, int h, int i0, int j0, const float *Q,
-                                           const float *K, const float *V, const float *D, int ldd, int ldv, int d4,
-                                           int dv4, int ty, int tx, float (&p)[I][J], float (&ds)[I][J]) {
-    float s[I][J] = {}, dp[I][J] = {};
-    tile_dot(s, Q, ldd, K, ldd, d4, ty, tx);
-    tile_dot(dp, D, ldv, V, ldv, dv4, ty, tx);
+// Statistics of queries i0 + I ty + i (0 behind the sequence).
+template <int I>
+__device__ __forceinline__ void row_stats(const MlaArgs &a, const Rows &w, int h, int i0, int ty, float (&lse)[I], float (&delta)[I]) {
 #pragma unroll
     for (int i = 0; i < I; ++i) {
         const int r = i0 + I * ty + i;
-        const bool in = r < w.lq;
-        const int end = in ? key_end(a, w, r) - j0 : 0;
-        const float lse = in ? a.lse[int64_t(w.q0 + r) * a.H + h] : 0.f, delta = in ? a.delta[int64_t(h) * a.Tq + w.q0 + r] : 0.f;
+        lse[i] = r < w.lq ? a.lse[int64_t(w.q0 + r) * a.H + h] : 0.f;
+        delta[i] = r < w.lq ? a.delta[int64_t(h) * a.Tq + w.q0 + r] : 0.f;
+    }
+}
+
+// P and dP of one tile (queries I ty + i, keys tx + 16 j), from the recomputed scores: p = exp(s - lse); both 0 where
+// the query does not see the key.
+template <int I, int J>
+__device__ __forceinline__ void tile_grads(const MlaArgs &a, const Rows &w, int i0, int j0, const float *Q, const float *K,
+                                           const float *V, const float *D, int ldd, int ldv, int d4, int dv4, int ty, int tx,
+                                           const float (&lse)[I], float (&p)[I][J], float (&dp)[I][J]) {
+    float s[I][J] = {};
+    tile_dot(s, Q, ldd, K, ldd, d4, ty, tx);
+#pragma unroll
+    for (int i = 0; i < I; ++i)
+#pragma unroll
+        for (int j = 0; j < J; ++j) dp[i][j] = 0.f;
+    tile_dot(dp, D, ldv, V, ldv, dv4, ty, tx);
+#pragma unroll
+    for (int i = 0; i < I; ++i) {
+        const int r = i0 + I * ty + i, end = r < w.lq ? key_end(a, w, r) - j0 : 0;
 #pragma unroll
         for (int j = 0; j < J; ++j) {
             const bool seen = tx + 16 * j < end;
-            p[i][j] = seen ? expf(s[i][j] * a.scale - lse) : 0.f;
-            ds[i][j] = seen ? p[i][j] * (dp[i][j] - delta) * a.scale : 0.f;
+            p[i][j] = seen ? expf(s[i][j] * a.scale - lse[i]) : 0.f;
+            dp[i][j] = seen ? dp[i][j] : 0.f;
         }
     }
 }
@@ -180,14 +193,15 @@ template <typename T, int J> __global__ void __launch_bounds__(kThreads, J == 2 
         load_q<T, kT>(Q, ldd, a, w, h, i0);
         load_dO<T, kT>(D, ldv, a, w, h, i0);
         __syncthreads();
-        float p[4][J], ds[4][J];
-        tile_grads(a, w, h, i0, j0, Q, K, V, D, ldd, ldv, d4, dv4, ty, tx, p, ds);
+        float p[4][J], dp[4][J], lse[4], delta[4];
+        row_stats(a, w, h, i0, ty, lse, delta);
+        tile_grads(a, w, i0, j0, Q, K, V, D, ldd, ldv, d4, dv4, ty, tx, lse, p, dp);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int j = 0; j < J; ++j) {
                 Pt[(tx + 16 * j) * kLdP + 4 * ty + i] = p[i][j];
-                St[(tx + 16 * j) * kLdP + 4 * ty + i] = ds[i][j];
+                St[(tx + 16 * j) * kLdP + 4 * ty + i] = p[i][j] * (dp[i][j] - delta[i]) * a.scale;
             }
         __syncthreads();
         tile_apply<J, 2>(dv, Pt, kLdP, D, ldv, a.dv, ty, tx);
@@ -226,21 +240,43 @@ template <typename T, int I> __global__ void __launch_bounds__(kThreads, I == 2 
     zero_columns<kThreads>(D, ldv, a.dv, dv4, kOwn);
     load_q<T, kOwn>(Q, ldd, a, w, h, i0);
     load_dO<T, kOwn>(D, ldv, a, w, h, i0);
-    float dq[I][12] = {};
+    float dq[I][12] = {}, lse[I], delta[I];
+    row_stats(a, w, h, i0, ty, lse, delta);
     const int last = key_end(a, w, min(i0 + kOwn, w.lq) - 1);
-    for (int j0 = 0; j0 < last; j0 += kT) {
-        __syncthreads();
-        load_k<T, kT>(K, ldd, a, w, h, j0);
-        load_v<T, kT>(V, ldv, a, w, h, j0);
-        __syncthreads();
-        float p[I][4], ds[I][4];
-        tile_grads(a, w, h, i0, j0, Q, K, V, D, ldd, ldv, d4, dv4, ty, tx, p, ds);
+    // Rows that see few keys: delta = sum_j P dP first, for dk and dv too, in place of the one from the rounded o
+    // (mla_backward_tc.cu says why); float32's o needs none of it.
+    const bool exact = sizeof(T) == 2 && last <= kExact;
+    float sum[I] = {};
+    for (int pass = exact ? 0 : 1; pass < 2; ++pass) {
+        for (int j0 = 0; j0 < last; j0 += kT) {
+            __syncthreads();
+            load_k<T, kT>(K, ldd, a, w, h, j0);
+            load_v<T, kT>(V, ldv, a, w, h, j0);
+            __syncthreads();
+            float p[I][4], dp[I][4];
+            tile_grads(a, w, i0, j0, Q, K, V, D, ldd, ldv, d4, dv4, ty, tx, lse, p, dp);
+            if (pass == 0) {
 #pragma unroll
-        for (int i = 0; i < I; ++i)
+                for (int i = 0; i < I; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) S[(I * ty + i) * kLdP + tx + 16 * j] = ds[i][j];
-        __syncwarp();
-        tile_apply<I, 3>(dq, S, kLdP, K, ldd, d, ty, tx);
+                    for (int j = 0; j < 4; ++j) sum[i] = fmaf(p[i][j], dp[i][j], sum[i]);
+                continue;
+            }
+#pragma unroll
+            for (int i = 0; i < I; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) S[(I * ty + i) * kLdP + tx + 16 * j] = p[i][j] * (dp[i][j] - delta[i]) * a.scale;
+            __syncwarp();
+            tile_apply<I, 3>(dq, S, kLdP, K, ldd, d, ty, tx);
+        }
+        if (pass == 0) {
+#pragma unroll
+            for (int i = 0; i < I; ++i) {
+                delta[i] = half_warp_sum(sum[i]);
+                const int r = i0 + I * ty + i;
+                if (tx == 0 && r < w.lq) a.delta[int64_t(h) * a.Tq + w.q0 + r] = delta[i];
+            }
+        }
     }
 #pragma unroll
     for (int i = 0; i < I; ++i) {
@@ -321,15 +357,15 @@ template <typename T> cudaError_t prefill(const MlaArgs &a, cudaStream_t st) {
 }
 
 template <typename T> cudaError_t backward(const MlaArgs &a, cudaStream_t st) {
-    cudaError_t e;
-    if (small_tiles(a.cu_k_host, a))
-        e = launch(dkv_kernel<T, 2>, count_tiles(a.cu_k_host, a.num_seqs, 32), grad_smem(a, 32, 2), a, st);
-    else
-        e = launch(dkv_kernel<T, 4>, count_tiles(a.cu_k_host, a.num_seqs, 64), grad_smem(a, 64, 2), a, st);
-    if (e != cudaSuccess) return e;
+    cudaError_t e;  // dq first: it leaves the delta of the rows that see few keys
     if (small_tiles(a.cu_q_host, a))
-        return launch(dq_kernel<T, 2>, count_tiles(a.cu_q_host, a.num_seqs, 32), grad_smem(a, 32, 1), a, st);
-    return launch(dq_kernel<T, 4>, count_tiles(a.cu_q_host, a.num_seqs, 64), grad_smem(a, 64, 1), a, st);
+        e = launch(dq_kernel<T, 2>, count_tiles(a.cu_q_host, a.num_seqs, 32), grad_smem(a, 32, 1), a, st);
+    else
+        e = launch(dq_kernel<T, 4>, count_tiles(a.cu_q_host, a.num_seqs, 64), grad_smem(a, 64, 1), a, st);
+    if (e != cudaSuccess) return e;
+    if (small_tiles(a.cu_k_host, a))
+        return launch(dkv_kernel<T, 2>, count_tiles(a.cu_k_host, a.num_seqs, 32), grad_smem(a, 32, 2), a, st);
+    return launch(dkv_kernel<T, 4>, count_tiles(a.cu_k_host, a.num_seqs, 64), grad_smem(a, 64, 2), a, st);
 }
 
 }  // namespace

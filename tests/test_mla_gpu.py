@@ -187,12 +187,13 @@ def test_prefill_and_backward(case, causal, dtype):
         assert t is None or torch.equal(t, again[name]), name
 
 
+@pytest.mark.parametrize("dims", [(128, 64, 128), (64, 32, 64)])
 @pytest.mark.parametrize("lens", [[2] * 60, [64] * 12, [300, 200, 33], [777]])
-def test_gradients_lose_no_precision_where_keys_are_few(lens):
+def test_gradients_lose_no_precision_where_keys_are_few(lens, dims):
     """dq and dk against what rounding the exact result makes.  Rounding dS and rounding the output are two independent
     roundings of the same kind, so the sum's error is sqrt(2) times one's: 1.5 asked (delta from the rounded output
     would give up to 2.7)."""
-    a, dO = packed(lens, lens, 4, 128, 64, 128, BF, seed=7)
+    a, dO = packed(lens, lens, 4, *dims, BF, seed=7)
     o, lse = mla_prefill(**a, want_lse=True)
     g = mla_backward(**a, o=o, lse=lse, dO=dO)
     ref = mla.backward(host(a["q"]), host(a["k"]), host(a["v"]), a["cu_q_host"], a["cu_k_host"], host(dO), k_rope=host(a["k_rope"]))
