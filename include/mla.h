@@ -150,7 +150,8 @@ KDA_API size_t mla_backward_workspace_size(int64_t total_q, int64_t total_k, int
  *   dq [Tq, H, d_nope + d_rope]   dk [Tk, H, d_nope]   dv [Tk, H, d_v]
  *   dk_rope [Tk, d_rope] (summed over the heads in float32; ignored if d_rope = 0)
  *
- * No atomics: repeated calls give identical results.  The paths are chosen as in
+ * No atomics: repeated calls give identical results.  delta = sum dO o is taken from o; in bf16, rows of tiles that see
+ * at most 288 keys sum it from the recomputed probabilities instead, because o's rounding would show there.  The paths are chosen as in
  * mla_prefill (dO, o and the outputs 16-byte aligned for the tensor cores; there P and dS
  * are rounded to bf16 for their products, all sums are float32).
  * workspace: mla_backward_workspace_size bytes, 256-byte aligned, contents ignored.
