@@ -4,7 +4,7 @@
 // A block works through its run of tiles (mla_decode_plan.cuh): kRows query rows against
 // kKeys cache rows at a time, both in shared memory as float32, so that each cache row is
 // read from memory once for all heads and tokens of a row tile.  The softmax is online.  Bound by latency at
-// small sizes (nine sequences of up to 3,001 rows, 12 heads, d_latent 256, float32: 28 us and 8 of join) and by the FMA
+// small sizes (nine sequences of up to 3,001 rows, 12 heads, d_latent 256, float32: 27 us and 8 of join) and by the FMA
 // pipes and shared memory at large ones.
 #include <cmath>
 
@@ -63,7 +63,15 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(const MlaDecodeArgs a,
             __syncthreads();
             // 16 threads a row, its four elements a load where rows allow
             const T *pool = static_cast<const T *>(a.cache);
-            if ((W & 3) == 0) {
+            if (sizeof(T) == 4 && (W & 3) == 0) {
+                for (int c = 4 * sk; c < W; c += 64)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int64_t at = place[sr + 16 * e];
+                        copy4_async(K + (sr + 16 * e) * ld + c, static_cast<const float *>(a.cache) + (at >= 0 ? at * W + c : 0), at >= 0);
+                    }
+                cp_async_wait();
+            } else if ((W & 3) == 0) {
                 for (int c = 4 * sk; c < W; c += 64) {
                     float4 v[2];
 #pragma unroll
@@ -83,15 +91,22 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(const MlaDecodeArgs a,
                     }
             }
             __syncthreads();
-            float s[2] = {0.f, 0.f};
+            float4 dot[2] = {};  // four partial sums each
+#pragma unroll 6
             for (int c = 0; c < W4; c += 4) {
                 const float4 q = *reinterpret_cast<const float4 *>(Q + sr * ld + c);
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const float4 k = *reinterpret_cast<const float4 *>(K + (sk + 16 * e) * ld + c);
-                    s[e] = fmaf(q.x, k.x, fmaf(q.y, k.y, fmaf(q.z, k.z, fmaf(q.w, k.w, s[e]))));
+                    dot[e].x = fmaf(q.x, k.x, dot[e].x);
+                    dot[e].y = fmaf(q.y, k.y, dot[e].y);
+                    dot[e].z = fmaf(q.z, k.z, dot[e].z);
+                    dot[e].w = fmaf(q.w, k.w, dot[e].w);
                 }
             }
+            float s[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) s[e] = (dot[e].x + dot[e].y) + (dot[e].z + dot[e].w);
             const int end = len - (a.n - 1) + (r0 + sr) / a.H;  // keys that row sr's token sees
             float top = m;
 #pragma unroll
@@ -123,6 +138,7 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(const MlaDecodeArgs a,
                 o[r][0] *= f;
                 o[r][1] *= f;
             }
+#pragma unroll 8
             for (int j = 0; j < kKeys; ++j) {
                 const float v0 = tid < a.dc ? K[j * ld + tid] : 0.f;
                 const float v1 = tid + kThreads < a.dc ? K[j * ld + tid + kThreads] : 0.f;

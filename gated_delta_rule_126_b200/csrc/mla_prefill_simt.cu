@@ -1,11 +1,12 @@
 // mla_prefill and mla_backward on the CUDA cores, in float32: every type, head size and
-// stride the calls take.  Tiles of scores with 64 streamed rows and 64 or 32 owned ones (the rows whose
-// output a block makes), 256 threads with 4 x 4 or 4 x 2 scores each; the softmax is kept online (running maximum and sum), so scores never leave the SM.  The
-// backward pass recomputes the scores from lse in two kernels, one per key tile (dk, dv)
-// and one per query tile (dq), so that every sum has one owner and no atomics.
-// Bound by the float32 FMA pipes and shared memory; three float32 sequences of 700, 33 and 1025 tokens, 4
-// heads, d = 96 and 80, take 146 us forward, 190 us for dq and 256 us for dk and dv, the chain of the longest one's 17
-// tiles.
+// stride the calls take.  Tiles of scores with 64 streamed rows and 64 or 32 owned ones (the
+// rows whose output a block makes), 256 threads with 4 x 4 or 4 x 2 scores each; the softmax
+// is kept online (running maximum and sum), so scores never leave the SM.  The backward pass
+// recomputes the scores from lse in two kernels, one per key tile (dk, dv) and one per query
+// tile (dq), so that every sum has one owner and no atomics.  Bound by the float32 FMA pipes
+// and shared memory; three float32 sequences of 700, 33 and 1025 tokens, 4 heads, d = 96 and
+// 80, take 138 us forward, 182 us for dq and 252 us for dk and dv, the chain of the longest
+// one's 17 tiles (146, 190 and 256 us with tiles loaded through registers, not asynchronously).
 #include <cmath>
 
 #include "mla_internal.h"
@@ -87,6 +88,7 @@ template <typename T, int I> __global__ void __launch_bounds__(kThreads, I == 2 
         __syncthreads();
         load_k<T, kT>(K, ldd, a, w, h, j0);
         load_v<T, kT>(V, ldv, a, w, h, j0);
+        cp_async_wait();
         __syncthreads();
         float s[I][4] = {};
         tile_dot(s, Q, ldd, K, ldd, d4, ty, tx);
@@ -117,6 +119,7 @@ template <typename T, int I> __global__ void __launch_bounds__(kThreads, I == 2 
         __syncwarp();  // a row of P is written and read by the same half warp
         tile_apply<I, 2>(o, P, kLdP, V, ldv, a.dv, ty, tx);
     }
+    cp_async_wait();  // of a loop without turns
 #pragma unroll
     for (int i = 0; i < I; ++i) {
         const int r = i0 + I * ty + i;
@@ -194,6 +197,7 @@ template <typename T, int J> __global__ void __launch_bounds__(kThreads, J == 2 
         __syncthreads();
         load_q<T, kT>(Q, ldd, a, w, h, i0);
         load_dO<T, kT>(D, ldv, a, w, h, i0);
+        cp_async_wait();
         __syncthreads();
         float p[4][J], dp[4][J], lse[4], delta[4];
         row_stats(a, w, h, i0, ty, lse, delta);
@@ -209,6 +213,7 @@ template <typename T, int J> __global__ void __launch_bounds__(kThreads, J == 2 
         tile_apply<J, 2>(dv, Pt, kLdP, D, ldv, a.dv, ty, tx);
         tile_apply<J, 3>(dk, St, kLdP, Q, ldd, d, ty, tx);
     }
+    cp_async_wait();  // of a loop without turns
 #pragma unroll
     for (int i = 0; i < J; ++i) {
         const int r = j0 + J * ty + i;
@@ -254,6 +259,7 @@ template <typename T, int I> __global__ void __launch_bounds__(kThreads, I == 2 
             __syncthreads();
             load_k<T, kT>(K, ldd, a, w, h, j0);
             load_v<T, kT>(V, ldv, a, w, h, j0);
+            cp_async_wait();
             __syncthreads();
             float p[I][4], dp[I][4];
             tile_grads(a, w, i0, j0, Q, K, V, D, ldd, ldv, d4, dv4, ty, tx, lse, p, dp);
@@ -280,6 +286,7 @@ template <typename T, int I> __global__ void __launch_bounds__(kThreads, I == 2 
             }
         }
     }
+    cp_async_wait();  // of a loop without turns
 #pragma unroll
     for (int i = 0; i < I; ++i) {
         const int r = i0 + I * ty + i;

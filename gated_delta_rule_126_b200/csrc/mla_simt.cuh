@@ -79,13 +79,30 @@ template <typename T> __device__ __forceinline__ bool by4(const T *p, int64_t st
     return ((stride | width) & 3) == 0 && (reinterpret_cast<uintptr_t>(p) & (4 * sizeof(T) - 1)) == 0;
 }
 
+// Four float32 from p into shared memory without waiting (cp_async_wait before the barrier after which they are
+// read), or four zeros.
+__device__ __forceinline__ void copy4_async(float *dst, const float *p, bool valid) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(uint32_t(__cvta_generic_to_shared(dst))), "l"(p), "r"(valid ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 // dst[r][at + c] = src[r * stride + c] for r < ROWS, c < width, as float32; rows from `valid` on are zero.
-// 16 threads a row, all rows of a pass in flight together; four elements a load where the layout allows.
+// 16 threads a row.  float32 rows that can be read four elements at a time are copied asynchronously, so that all of a
+// tile's loads, and those of several tiles, are under way together: cp_async_wait() before the barrier.
 template <typename T, int NT, int ROWS>
 __device__ __forceinline__ void load_tile(float *dst, int ld, int at, const T *src, int64_t stride, int width, int valid) {
     constexpr int kPer = ROWS / (NT / 16);
     const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
     if (by4(src, stride, width) && (at & 3) == 0) {
+        if constexpr (sizeof(T) == 4) {
+            for (int c = 4 * tx; c < width; c += 64)
+#pragma unroll
+                for (int i = 0; i < kPer; ++i) {
+                    const int r = ty + NT / 16 * i;
+                    copy4_async(dst + r * ld + at + c, src + (r < valid ? r * stride + c : 0), r < valid);
+                }
+            return;
+        }
         for (int c = 4 * tx; c < width; c += 64) {
             float4 v[kPer];
 #pragma unroll
