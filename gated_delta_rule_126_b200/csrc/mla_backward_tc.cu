@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(kThreads, 1) dkv_tc_kernel(const __grid_consta
             stats(first);
             for (; i < n; ++i) {
                 const int s = i % kStages, i0 = (first + i) * kQt;
-                if (i >= kStages && !(ok = tc::wait(&mi.empty[s], (i / kStages - 1) & 1, dead))) break;
+                if (i >= kStages && !(ok = tc::wait_warp(&mi.empty[s], (i / kStages - 1) & 1, dead))) break;
                 if (tc::elect()) {
                     const uint32_t dst = base + kOffStages + s * kStage;
                     ptx::mbar_arrive_expect_tx(&mi.full[s], (kc + 2) * kQChunk);
@@ -229,8 +229,8 @@ __global__ void __launch_bounds__(kThreads, 1) dkv_tc_kernel(const __grid_consta
         bool ok = true;
         for (int i = 0; i < n; ++i) {
             const int s = i % kStages, i0 = (first + i) * kQt, c0 = i0 + half * 32;
-            if (!(ok = tc::wait(&mi.s_full[i & 1], (i >> 1) & 1, dead))) break;
-            if (!(ok = tc::wait(&mi.full[s], (i / kStages) & 1, dead))) break;  // complete: orders lse2 and delta
+            if (!(ok = tc::wait_warp(&mi.s_full[i & 1], (i >> 1) & 1, dead))) break;
+            if (!(ok = tc::wait_warp(&mi.full[s], (i / kStages) & 1, dead))) break;  // complete: orders lse2 and delta
             ptx::tc_fence_after();
             uint32_t v[32];
             ptx::tmem_ld32(at + (i & 1) * 64, v);
@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(kThreads, 1) dkv_tc_kernel(const __grid_consta
             ptx::tmem_wait_st();
             ptx::tc_fence_before();
             ptx::mbar_arrive(&mi.p_full);
-            if (!(ok = tc::wait(&mi.dp_full, i & 1, dead))) break;
+            if (!(ok = tc::wait_warp(&mi.dp_full, i & 1, dead))) break;
             ptx::tc_fence_after();
             ptx::tmem_ld32(at + kTmDp, v);
             ptx::tmem_wait_ld();
@@ -294,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, 1) dkv_tc_kernel(const __grid_consta
             ptx::tc_fence_before();
             ptx::mbar_arrive(&mi.ds_full);
         }
-        if (ok && n > 0) ok = tc::wait(&mi.done, 0, dead);
+        if (ok && n > 0) ok = tc::wait_warp(&mi.done, 0, dead);
         ptx::tc_fence_after();
         if (ok) {
             // warpgroup 0 writes dv, warpgroup 1 dk; each half of the shared part's share.  The rows pass through
@@ -531,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constan
             ptx::mbar_arrive(&mi.do_full);
         }
         for (int j = 0; j < n; ++j) {
-            if (!(ok = tc::wait(&mi.s_full, j & 1, dead))) break;
+            if (!(ok = tc::wait_warp(&mi.s_full, j & 1, dead))) break;
             ptx::tc_fence_after();
             uint32_t v[32], u[16];
             ptx::tmem_ld32(lanes + kHalf * half, v);
@@ -552,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constan
                     tc::st_shared_v4(base + kOffK + ((j % 3) * 3 + x / per) * kKbChunk + (from + x % per) * 16, 0, 0, 0, 0);
                 ptx::fence_proxy_async_smem();
             }
-            if (!(ok = tc::wait(&mi.dp_full, j & 1, dead))) break;
+            if (!(ok = tc::wait_warp(&mi.dp_full, j & 1, dead))) break;
             ptx::tc_fence_after();
             ptx::tmem_ld32(lanes + kTqDp + kHalf * half, v);
             ptx::tmem_ld16(lanes + kTqDp + kHalf * half + 32, u);
@@ -569,7 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constan
                 if (j + 1 == before) {  // both halves' shares
                     mi.delta[half][row] = delta;
                     ptx::mbar_arrive(&mi.delta_full);
-                    if (!(ok = tc::wait(&mi.delta_full, 0, dead))) break;
+                    if (!(ok = tc::wait_warp(&mi.delta_full, 0, dead))) break;
                     delta = mi.delta[0][row] + mi.delta[1][row];
                     if (half == 0 && r < pl.lq) a.delta[stat] = delta;
                 }
@@ -587,7 +587,7 @@ __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constan
                 (c < 32 ? x[(c >> 1) & 15] : y[(c >> 1) & 7]) = tc::pack_bf16(d0, d1);
             }
             // the last block's product, which frees its keys, has read dS
-            if (j && !(ok = tc::wait(&mi.k_empty[(j - 1) % 3], ((j - 1) / 3) & 1, dead))) break;
+            if (j && !(ok = tc::wait_warp(&mi.k_empty[(j - 1) % 3], ((j - 1) / 3) & 1, dead))) break;
             ptx::tc_fence_after();
             ptx::tmem_st16(lanes + kTqDs + kHalf / 2 * half, x);
             tc::tmem_st8(lanes + kTqDs + kHalf / 2 * half + 16, y);
@@ -595,7 +595,7 @@ __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constan
             ptx::tc_fence_before();
             ptx::mbar_arrive(&mi.ds_full);
         }
-        if (ok && n > 0) ok = tc::wait(&mi.done, 0, dead);
+        if (ok && n > 0) ok = tc::wait_warp(&mi.done, 0, dead);
         ptx::tc_fence_after();
         if (ok) {
             // each warpgroup writes half of the channels, through the place of Q and the keys, which nothing reads any more

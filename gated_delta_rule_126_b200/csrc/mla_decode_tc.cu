@@ -343,8 +343,8 @@ decode_tc_kernel(const __grid_constant__ Maps maps, const MlaDecodeArgs a, const
                 float top[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};  // the scale's maximum (raw scores); this thread's share
                 for (int t = w.t0; t < w.t1; ++t) {
                     // a wait that fails is voted on below: no warp leaves the others at a barrier
-                    ok = tc::wait(&mi.s_full[tile & 1], (tile >> 1) & 1, dead) && ok;
-                    ok = tc::wait(&mi.full[ring.slot], ring.round & 1, dead) && ok;  // complete: orders the mask
+                    ok = tc::wait_warp(&mi.s_full[tile & 1], (tile >> 1) & 1, dead) && ok;
+                    ok = tc::wait_warp(&mi.full[ring.slot], ring.round & 1, dead) && ok;  // complete: orders the mask
                     ptx::tc_fence_after();
                     uint32_t s[32];
                     tc::tmem_ld_16x64(tmem + lanes + Tm<RB>::kS + (tile & 1) * 64, s);
@@ -354,7 +354,7 @@ decode_tc_kernel(const __grid_constant__ Maps maps, const MlaDecodeArgs a, const
                         // rows behind the sequence may hold anything: as values they have to be zero
                         Ring z = ring;
                         for (int i = 0; i < blocks; ++i, z.next(L.slots)) {
-                            ok = tc::wait(&mi.full[z.slot], z.round & 1, dead) && ok;
+                            ok = tc::wait_warp(&mi.full[z.slot], z.round & 1, dead) && ok;
                             const int from = left * 8, per = kKeys * 8 - from;
                             for (int x = tid; x < 2 * per; x += 128)
                                 tc::st_shared_v4(base + z.slot * kSlotBytes + (x / per) * 8192 + (from + x % per) * 16, 0, 0, 0, 0);
@@ -405,7 +405,7 @@ decode_tc_kernel(const __grid_constant__ Maps maps, const MlaDecodeArgs a, const
                     sum[0] += add[0] + add[2];
                     sum[1] += add[1] + add[3];
                     // the last product has read P and added to O
-                    if (tile) ok = tc::wait(&mi.pv_done, (tile - 1) & 1, dead) && ok;
+                    if (tile) ok = tc::wait_warp(&mi.pv_done, (tile - 1) & 1, dead) && ok;
                     if (ptx::named_barrier_or(1, 128, raise || !ok)) {
                         if (pair == 0) mi.factor[r1] = keep[0], mi.factor[r2] = keep[1];
                         if (ptx::named_barrier_or(1, 128, !ok)) {
@@ -444,7 +444,7 @@ decode_tc_kernel(const __grid_constant__ Maps maps, const MlaDecodeArgs a, const
                     ptx::mbar_arrive(&mi.p_full);
                     ++tile;
                 }
-                if (ok) ok = tc::wait(&mi.pv_done, (tile - 1) & 1, dead);
+                if (ok) ok = tc::wait_warp(&mi.pv_done, (tile - 1) & 1, dead);
                 if (ptx::named_barrier_or(1, 128, !ok)) break;  // and factor is free
                 const bool whole = w.whole();
                 float *slot = slots + mla_slot(w) * mla_slot_floats(RB, a.dc);

@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
         float top = -INFINITY, sum = 0.f;
         bool ok = true;
         for (int j = 0; j < n[t]; ++j) {
-            if (!(ok = tc::wait(&mi.s_full[t], j & 1, dead))) break;
+            if (!(ok = tc::wait_warp(&mi.s_full[t], j & 1, dead))) break;
             ptx::tc_fence_after();
             uint32_t s[4][32];
 #pragma unroll
@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
                     for (int c = 0; ok && c < 2; ++c) {
                         const int idx = j * per + kc + c, slot = idx % kSlots, rows0 = min(64, max(0, left - 64 * c));
                         if (rows0 == 64) continue;
-                        if (!(ok = tc::wait(&mi.full[slot], (idx / kSlots) & 1, dead))) break;
+                        if (!(ok = tc::wait_warp(&mi.full[slot], (idx / kSlots) & 1, dead))) break;
                         const uint32_t va = base + kOffRing + slot * kSlotBytes;
                         for (int i = rows0 * 8 + row; i < 512; i += 128) {
                             tc::st_shared_v4(va + 16 * i, 0, 0, 0, 0);
@@ -268,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
                 raise = true;
             }
             if (__any_sync(0xffffffffu, raise)) {  // the last product has added to O
-                if (!(ok = tc::wait(&mi.pv_done[t], (j - 1) & 1, dead))) break;
+                if (!(ok = tc::wait_warp(&mi.pv_done[t], (j - 1) & 1, dead))) break;
                 ptx::tc_fence_after();
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
             tc::split(tc::add2(add[0], add[1]), x, y);
             sum += x + y;
         }
-        if (ok && n[t]) ok = tc::wait(&mi.pv_done[t], (n[t] - 1) & 1, dead);
+        if (ok && n[t]) ok = tc::wait_warp(&mi.pv_done[t], (n[t] - 1) & 1, dead);
         ptx::tc_fence_after();
         if (ok) {
             const float inv = sum == 0.f ? 0.f : 1.f / sum;

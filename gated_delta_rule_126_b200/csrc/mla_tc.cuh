@@ -75,6 +75,11 @@ __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, volatile ui
     return true;
 }
 
+// The same by a whole warp: one answer for all its lanes, which stay together (an error may reach them at different times).
+__device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, volatile uint32_t *dead) {
+    return __all_sync(0xffffffffu, wait(bar, parity, dead));
+}
+
 __device__ __forceinline__ void tma_load_2d(uint32_t smem_dst, const void *tmap, uint64_t *bar, int c0, int c1) {
     asm volatile(
         "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
