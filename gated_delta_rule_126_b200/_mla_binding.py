@@ -55,6 +55,8 @@ def _on(stream, index):
     """Context and raw handle of the device and stream a call runs on: what it allocates belongs to that stream.
     These calls are made once a token, so the usual case (current device and stream) switches nothing."""
     if stream is not None:
+        if stream.device_index != index:
+            raise ValueError(f"stream is on cuda:{stream.device_index}, the tensors on cuda:{index}")
         return _switched(stream, index), stream.cuda_stream
     raw = torch._C._cuda_getCurrentRawStream(index)
     return (_NOTHING if torch.cuda.current_device() == index else torch.cuda.device(index)), raw

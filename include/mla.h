@@ -97,7 +97,9 @@ KDA_API size_t mla_decode_workspace_size(int B, int n, int H, int d_latent, int 
  * A token that sees no row (L = 0, or L < n for the first ones) gets o = 0 and
  * lse = -inf.  Rows behind the page table's width, and pages outside [0, num_pages), are
  * left out of the softmax.  Rows that no token sees are not read into any sum: they may
- * hold anything, NaN included.  Work is split over the keys by a fixed rule, so repeated
+ * hold anything, NaN included.  An infinity or NaN in a row that some token sees stays in its
+ * sequence, but reaches the sequence's other tokens too, those that do not see the row
+ * among them (its probability 0 is multiplied by it).  Work is split over the keys by a fixed rule, so repeated
  * calls give identical results.
  * Supported: 1 <= d_latent <= 512, 0 <= d_rope <= 64, n * H <= 65536, B <= 65536;
  * q, cache and o 16-byte aligned.  bf16 with d_latent a multiple of 128, d_rope 0 or 64,
@@ -125,7 +127,10 @@ KDA_API kda_status_t mla_decode(const void *q, kda_dtype_t dtype, const void *ca
  *   o       [Tq, H, d_v] contiguous;   lse [Tq, H] float32 or NULL
  *
  * A query that sees no key gets o = 0 and lse = -inf.  Rows outside the sequences are not
- * read into any sum and not written.
+ * read into any sum and not written.  Scores of keys that a query does not see count
+ * nowhere, whatever they are; an infinity or NaN in v stays in its sequence, but reaches
+ * queries of its tile that do not see its key (probability 0 times it).  The same holds for
+ * q, k and dO in mla_backward.
  * Supported: d_nope and d_v in 1..128, 0 <= d_rope <= 64.  bf16 with d_nope = d_v = 128,
  * d_rope 0 or 64, strides that are multiples of 8 and 16-byte aligned tensors runs on
  * the tensor cores (probabilities rounded to bf16, sums in float32), everything else on
@@ -150,10 +155,11 @@ KDA_API size_t mla_backward_workspace_size(int64_t total_q, int64_t total_k, int
  *   dq [Tq, H, d_nope + d_rope]   dk [Tk, H, d_nope]   dv [Tk, H, d_v]
  *   dk_rope [Tk, d_rope] (summed over the heads in float32; ignored if d_rope = 0)
  *
- * No atomics: repeated calls give identical results.  delta = sum dO o is taken from o; in bf16, rows of tiles that see
- * at most 288 keys sum it from the recomputed probabilities instead, because o's rounding would show there.  The paths are chosen as in
- * mla_prefill (dO, o and the outputs 16-byte aligned for the tensor cores; there P and dS
- * are rounded to bf16 for their products, all sums are float32).
+ * No atomics: repeated calls give identical results.  delta = sum dO o is taken from o; in
+ * bf16, rows of tiles that see at most 288 keys sum it from the recomputed probabilities
+ * instead, because o's rounding would show there.  The paths are chosen as in mla_prefill
+ * (dO, o and the outputs 16-byte aligned for the tensor cores; there P and dS are rounded to
+ * bf16 for their products, all sums are float32).
  * workspace: mla_backward_workspace_size bytes, 256-byte aligned, contents ignored.
  */
 KDA_API kda_status_t mla_backward(const void *q, int64_t q_stride_t, int64_t q_stride_h, const void *k,

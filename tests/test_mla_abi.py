@@ -167,3 +167,11 @@ def test_overlapping_output_rows_are_refused():
         _mla_binding._written(torch.zeros(1, 4).expand(3, 4), "x")
     _mla_binding._written(torch.zeros(5, 3, 10)[..., 4:], "x")
     _mla_binding._written(torch.zeros(3, 5, 4).transpose(0, 1), "x")
+
+
+def test_binding_refuses_another_devices_stream():
+    class Stream:  # as much of a torch.cuda.Stream as the check sees
+        device_index, cuda_stream = 1, 0
+
+    with pytest.raises(ValueError, match="stream is on cuda:1, the tensors on cuda:0"):
+        _mla_binding._on(Stream(), 0)
