@@ -3,10 +3,15 @@
 // rows whose output a block makes), 256 threads with 4 x 4 or 4 x 2 scores each; the softmax
 // is kept online (running maximum and sum), so scores never leave the SM.  The backward pass
 // recomputes the scores from lse in two kernels, one per key tile (dk, dv) and one per query
-// tile (dq), so that every sum has one owner and no atomics.  Bound by the float32 FMA pipes
-// and shared memory; three float32 sequences of 700, 33 and 1025 tokens, 4 heads, d = 96 and
-// 80, take 138 us forward, 182 us for dq and 252 us for dk and dv, the chain of the longest
-// one's 17 tiles (146, 190 and 256 us with tiles loaded through registers, not asynchronously).
+// tile (dq), so that every sum has one owner and no atomics.  A block streams the tiles
+// that its owned rows meet, one after another; in calls of few blocks that chain is the
+// call's time, so the blocks of a cluster take its tiles in turn and add their parts through
+// distributed shared memory, in the order of their ranks.
+// Bound by the float32 FMA pipes and shared memory (57% of issue slots used while an SM has
+// work, 3.2 shared-memory wavefronts a load); three float32 sequences of 700, 33 and 1025
+// tokens, 4 heads, d = 96 and 80, take 75 us forward, 97 us for dq and 137 us for dk and dv
+// (with one block a chain, heads one after another and columns in whole 64s 138, 182 and 252).
+#include <algorithm>
 #include <cmath>
 
 #include "mla_internal.h"
@@ -18,6 +23,7 @@ namespace {
 constexpr int kT = 64;  // streamed rows of a tile
 constexpr int kThreads = 256;  // 16 x 16
 constexpr int kLdP = kT + 4;
+constexpr int kMostRanks = 8;  // blocks of a cluster
 constexpr int kExact = 288;  // keys up to which a tile's delta is made from P and dP
 
 struct Rows {  // one sequence's place
@@ -65,15 +71,18 @@ __device__ __forceinline__ float half_warp_sum(float x) {
     return x;
 }
 
-// A block owns 16 I queries of a head.
+// A block owns 16 I queries of a head.  A sequence's longest chains, those of its last queries in all heads, come first:
+// a long one that begins late is the call's tail.
 template <typename T, int I> __global__ void __launch_bounds__(kThreads, I == 2 ? 2 : 1) prefill_kernel(const MlaArgs a) {
     extern __shared__ float sm[];
     __shared__ int64_t buf[kThreads / 32 + 2];
     constexpr int kOwn = 16 * I;
-    const int d = a.dn + a.dr, d4 = (d + 3) & ~3, ldd = simt_row(d), ldv = simt_row(a.dv), h = blockIdx.y;
+    const Share share = cluster_share();
+    const int d = a.dn + a.dr, d4 = (d + 3) & ~3, ldd = simt_row(d), ldv = simt_row(a.dv);
+    const int x = int(blockIdx.x) / share.ranks, h = x % a.H;
     float *Q = sm, *K = Q + kOwn * ldd, *V = K + kT * ldd, *P = V + kT * ldv;
     int seq, tile;
-    if (!find_tile<kThreads>(a.cu_q, a.num_seqs, kOwn, gridDim.x - 1 - blockIdx.x, buf, &seq, &tile)) return;
+    if (!find_tile<kThreads>(a.cu_q, a.num_seqs, kOwn, int(gridDim.x) / share.ranks / a.H - 1 - x / a.H, buf, &seq, &tile)) return;
     const Rows w = rows_of(a, seq);
     const int i0 = tile * kOwn, tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
     zero_columns<kThreads>(Q, ldd, d, d4, kOwn);
@@ -84,12 +93,13 @@ template <typename T, int I> __global__ void __launch_bounds__(kThreads, I == 2 
 #pragma unroll
     for (int i = 0; i < I; ++i) m[i] = -INFINITY, l[i] = 0.f;
     const int last = key_end(a, w, min(i0 + kOwn, w.lq) - 1);
-    for (int j0 = 0; j0 < last; j0 += kT) {
-        __syncthreads();
-        load_k<T, kT>(K, ldd, a, w, h, j0);
-        load_v<T, kT>(V, ldv, a, w, h, j0);
+    const int step = share.ranks * kT;
+    // Asynchronous loads have a product to hide behind: a tile's values the scores, the next one's keys P V.
+    if (share.rank * kT < last) load_k<T, kT>(K, ldd, a, w, h, share.rank * kT);
+    for (int j0 = share.rank * kT; j0 < last; j0 += step) {
         cp_async_wait();
-        __syncthreads();
+        __syncthreads();  // the keys are there, the last tile's values read
+        load_v<T, kT>(V, ldv, a, w, h, j0);
         float s[I][4] = {};
         tile_dot(s, Q, ldd, K, ldd, d4, ty, tx);
 #pragma unroll
@@ -116,19 +126,45 @@ template <typename T, int I> __global__ void __launch_bounds__(kThreads, I == 2 
 #pragma unroll
             for (int c = 0; c < 8; ++c) o[i][c] *= keep;
         }
-        __syncwarp();  // a row of P is written and read by the same half warp
-        tile_apply<I, 2>(o, P, kLdP, V, ldv, a.dv, ty, tx);
+        cp_async_wait();
+        __syncthreads();  // the values are there, the keys read
+        if (j0 + step < last) load_k<T, kT>(K, ldd, a, w, h, j0 + step);
+        tile_apply(o, P, kLdP, V, ldv, a.dv, ty, tx);
     }
     cp_async_wait();  // of a loop without turns
+    if (share.ranks > 1) {  // the blocks' parts, brought to one maximum
+        __syncthreads();
+        float *stat = sm + I * 8 * kThreads;  // maximum and sum of each row
+        leave<kThreads>(sm, o);
+        if (tx == 0)
+#pragma unroll
+            for (int i = 0; i < I; ++i) stat[2 * (I * ty + i)] = m[i], stat[2 * (I * ty + i) + 1] = l[i];
+        cluster_sync();
+#pragma unroll
+        for (int i = 0; i < I; ++i) {
+            if (!share.owns(i)) continue;
+            float f[kMostRanks], sum = 0.f;
+#pragma unroll
+            for (int r = 0; r < kMostRanks; ++r)
+                if (r < share.ranks) f[r] = load2_peer(stat + 2 * (I * ty + i), r).x, m[i] = fmaxf(m[i], f[r]);
+            const float base = m[i] == -INFINITY ? 0.f : m[i];
+#pragma unroll
+            for (int r = 0; r < kMostRanks; ++r)
+                if (r < share.ranks) f[r] = expf(f[r] - base), sum = fmaf(f[r], load2_peer(stat + 2 * (I * ty + i), r).y, sum);
+            l[i] = sum;
+            gather<kThreads>(o[i], sm, i, share.ranks, f);
+        }
+        cluster_sync();  // nobody leaves while its part is read
+    }
 #pragma unroll
     for (int i = 0; i < I; ++i) {
         const int r = i0 + I * ty + i;
-        if (r >= w.lq) continue;
+        if (r >= w.lq || !share.owns(i)) continue;
         const float inv = l[i] > 0.f ? 1.f / l[i] : 0.f;
         T *out = static_cast<T *>(a.o) + (int64_t(w.q0 + r) * a.H + h) * a.dv;
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
-            const int col = (c >> 2) * 64 + 4 * tx + (c & 3);
+            const int col = apply_column(c, a.dv, tx);
             // a NaN among the seen scores makes l NaN: it reaches the output
             if (col < a.dv) out[col] = from_f32<T>(l[i] == 0.f ? 0.f : l[i] > 0.f ? o[i][c] * inv : l[i]);
         }
@@ -147,19 +183,13 @@ __device__ __forceinline__ void row_stats(const MlaArgs &a, const Rows &w, int h
     }
 }
 
-// P and dP of one tile (queries I ty + i, keys tx + 16 j), from the recomputed scores: p = exp(s - lse); both 0 where
-// the query does not see the key.
+// P of one tile (queries I ty + i, keys tx + 16 j) from the recomputed scores, p = exp(s - lse), and dP as it is in `dp`;
+// both 0 where the query does not see the key.
 template <int I, int J>
-__device__ __forceinline__ void tile_grads(const MlaArgs &a, const Rows &w, int i0, int j0, const float *Q, const float *K,
-                                           const float *V, const float *D, int ldd, int ldv, int d4, int dv4, int ty, int tx,
-                                           const float (&lse)[I], float (&p)[I][J], float (&dp)[I][J]) {
+__device__ __forceinline__ void tile_probs(const MlaArgs &a, const Rows &w, int i0, int j0, const float *Q, const float *K,
+                                           int ldd, int d4, int ty, int tx, const float (&lse)[I], float (&p)[I][J], float (&dp)[I][J]) {
     float s[I][J] = {};
     tile_dot(s, Q, ldd, K, ldd, d4, ty, tx);
-#pragma unroll
-    for (int i = 0; i < I; ++i)
-#pragma unroll
-        for (int j = 0; j < J; ++j) dp[i][j] = 0.f;
-    tile_dot(dp, D, ldv, V, ldv, dv4, ty, tx);
 #pragma unroll
     for (int i = 0; i < I; ++i) {
         const int r = i0 + I * ty + i, end = r < w.lq ? key_end(a, w, r) - j0 : 0;
@@ -177,11 +207,12 @@ template <typename T, int J> __global__ void __launch_bounds__(kThreads, J == 2 
     extern __shared__ float sm[];
     __shared__ int64_t buf[kThreads / 32 + 2];
     constexpr int kOwn = 16 * J;
-    const int d = a.dn + a.dr, d4 = (d + 3) & ~3, dv4 = (a.dv + 3) & ~3, h = blockIdx.y;
+    const Share share = cluster_share();
+    const int d = a.dn + a.dr, d4 = (d + 3) & ~3, dv4 = (a.dv + 3) & ~3, x = int(blockIdx.x) / share.ranks, h = x % a.H;
     const int ldd = simt_row(d), ldv = simt_row(a.dv);
     float *Q = sm, *K = Q + kT * ldd, *V = K + kOwn * ldd, *D = V + kOwn * ldv, *Pt = D + kT * ldv, *St = Pt + kOwn * kLdP;
     int seq, tile;
-    if (!find_tile<kThreads>(a.cu_k, a.num_seqs, kOwn, blockIdx.x, buf, &seq, &tile)) return;
+    if (!find_tile<kThreads>(a.cu_k, a.num_seqs, kOwn, x / a.H, buf, &seq, &tile)) return;
     const Rows w = rows_of(a, seq);
     const int j0 = tile * kOwn, tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
     zero_columns<kThreads>(Q, ldd, d, d4, kT);
@@ -193,15 +224,19 @@ template <typename T, int J> __global__ void __launch_bounds__(kThreads, J == 2 
     float dk[J][12] = {}, dv[J][8] = {};
     // the first query that sees key j0
     const int first = a.causal ? max(0, j0 - (w.lk - w.lq)) / kT * kT : 0;
-    for (int i0 = first; i0 < w.lq; i0 += kT) {
-        __syncthreads();
+    const int step = share.ranks * kT, begin = first + share.rank * kT;
+    // Asynchronous loads have a product to hide behind: a tile's queries dP, the next one's dO that of dk.
+    if (begin < w.lq) load_dO<T, kT>(D, ldv, a, w, h, begin);
+    for (int i0 = begin; i0 < w.lq; i0 += step) {
+        float p[4][J], dp[4][J] = {}, lse[4], delta[4];
+        row_stats(a, w, h, i0, ty, lse, delta);
+        cp_async_wait();
+        __syncthreads();  // dO is there, the last tile's queries read
         load_q<T, kT>(Q, ldd, a, w, h, i0);
-        load_dO<T, kT>(D, ldv, a, w, h, i0);
+        tile_dot(dp, D, ldv, V, ldv, dv4, ty, tx);
         cp_async_wait();
         __syncthreads();
-        float p[4][J], dp[4][J], lse[4], delta[4];
-        row_stats(a, w, h, i0, ty, lse, delta);
-        tile_grads(a, w, i0, j0, Q, K, V, D, ldd, ldv, d4, dv4, ty, tx, lse, p, dp);
+        tile_probs(a, w, i0, j0, Q, K, ldd, d4, ty, tx, lse, p, dp);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -210,21 +245,37 @@ template <typename T, int J> __global__ void __launch_bounds__(kThreads, J == 2 
                 St[(tx + 16 * j) * kLdP + 4 * ty + i] = p[i][j] * (dp[i][j] - delta[i]) * a.scale;
             }
         __syncthreads();
-        tile_apply<J, 2>(dv, Pt, kLdP, D, ldv, a.dv, ty, tx);
-        tile_apply<J, 3>(dk, St, kLdP, Q, ldd, d, ty, tx);
+        tile_apply(dv, Pt, kLdP, D, ldv, a.dv, ty, tx);
+        if (i0 + step < w.lq) {
+            __syncthreads();
+            load_dO<T, kT>(D, ldv, a, w, h, i0 + step);
+        }
+        tile_apply(dk, St, kLdP, Q, ldd, d, ty, tx);
     }
     cp_async_wait();  // of a loop without turns
+    if (share.ranks > 1) {
+        __syncthreads();
+        float *at = sm + J * 12 * kThreads;
+        leave<kThreads>(sm, dk);
+        leave<kThreads>(at, dv);
+        cluster_sync();
+#pragma unroll
+        for (int i = 0; i < J; ++i)
+            if (share.owns(i)) gather<kThreads>(dk[i], sm, i, share.ranks), gather<kThreads>(dv[i], at, i, share.ranks);
+        cluster_sync();  // nobody leaves while its part is read
+    }
 #pragma unroll
     for (int i = 0; i < J; ++i) {
         const int r = j0 + J * ty + i;
-        if (r >= w.lk) continue;
+        if (r >= w.lk || !share.owns(i)) continue;
         const int64_t at = int64_t(w.k0 + r) * a.H + h;
 #pragma unroll
         for (int c = 0; c < 12; ++c) {
-            const int col = (c >> 2) * 64 + 4 * tx + (c & 3);
+            const int col = apply_column(c, d, tx);
             if (col < a.dn) static_cast<T *>(a.dk)[at * a.dn + col] = from_f32<T>(dk[i][c]);
             else if (col < d) a.dkr_partial[(int64_t(h) * a.Tk + w.k0 + r) * a.dr + col - a.dn] = dk[i][c];
-            if (c < 8 && col < a.dv) static_cast<T *>(a.dv_out)[at * a.dv + col] = from_f32<T>(dv[i][c & 7]);
+            const int col_v = apply_column(c, a.dv, tx);
+            if (c < 8 && col_v < a.dv) static_cast<T *>(a.dv_out)[at * a.dv + col_v] = from_f32<T>(dv[i][c & 7]);
         }
     }
 }
@@ -234,11 +285,12 @@ template <typename T, int I> __global__ void __launch_bounds__(kThreads, I == 2 
     extern __shared__ float sm[];
     __shared__ int64_t buf[kThreads / 32 + 2];
     constexpr int kOwn = 16 * I;
-    const int d = a.dn + a.dr, d4 = (d + 3) & ~3, dv4 = (a.dv + 3) & ~3, h = blockIdx.y;
+    const Share share = cluster_share();
+    const int d = a.dn + a.dr, d4 = (d + 3) & ~3, dv4 = (a.dv + 3) & ~3, x = int(blockIdx.x) / share.ranks, h = x % a.H;
     const int ldd = simt_row(d), ldv = simt_row(a.dv);
     float *Q = sm, *K = Q + kOwn * ldd, *V = K + kT * ldd, *D = V + kT * ldv, *S = D + kOwn * ldv;
     int seq, tile;
-    if (!find_tile<kThreads>(a.cu_q, a.num_seqs, kOwn, gridDim.x - 1 - blockIdx.x, buf, &seq, &tile)) return;
+    if (!find_tile<kThreads>(a.cu_q, a.num_seqs, kOwn, int(gridDim.x) / share.ranks / a.H - 1 - x / a.H, buf, &seq, &tile)) return;
     const Rows w = rows_of(a, seq);
     const int i0 = tile * kOwn, tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
     zero_columns<kThreads>(Q, ldd, d, d4, kOwn);
@@ -255,14 +307,20 @@ template <typename T, int I> __global__ void __launch_bounds__(kThreads, I == 2 
     const bool exact = sizeof(T) == 2 && last <= kExact;
     float sum[I] = {};
     for (int pass = exact ? 0 : 1; pass < 2; ++pass) {
-        for (int j0 = 0; j0 < last; j0 += kT) {
-            __syncthreads();
-            load_k<T, kT>(K, ldd, a, w, h, j0);
-            load_v<T, kT>(V, ldv, a, w, h, j0);
+        // the first pass is short: every block of the cluster makes it whole
+        const int begin = pass ? share.rank * kT : 0, step = (pass ? share.ranks : 1) * kT;
+        // Asynchronous loads have a product to hide behind: a tile's keys dP, the next one's values those with the keys.
+        if (begin < last) load_v<T, kT>(V, ldv, a, w, h, begin);
+        for (int j0 = begin; j0 < last; j0 += step) {
             cp_async_wait();
-            __syncthreads();
-            float p[I][4], dp[I][4];
-            tile_grads(a, w, i0, j0, Q, K, V, D, ldd, ldv, d4, dv4, ty, tx, lse, p, dp);
+            __syncthreads();  // the values are there, the last tile's keys read
+            load_k<T, kT>(K, ldd, a, w, h, j0);
+            float p[I][4], dp[I][4] = {};
+            tile_dot(dp, D, ldv, V, ldv, dv4, ty, tx);
+            cp_async_wait();
+            __syncthreads();  // the keys are there, the values read
+            if (j0 + step < last) load_v<T, kT>(V, ldv, a, w, h, j0 + step);
+            tile_probs(a, w, i0, j0, Q, K, ldd, d4, ty, tx, lse, p, dp);
             if (pass == 0) {
 #pragma unroll
                 for (int i = 0; i < I; ++i)
@@ -275,26 +333,35 @@ template <typename T, int I> __global__ void __launch_bounds__(kThreads, I == 2 
 #pragma unroll
                 for (int j = 0; j < 4; ++j) S[(I * ty + i) * kLdP + tx + 16 * j] = p[i][j] * (dp[i][j] - delta[i]) * a.scale;
             __syncwarp();
-            tile_apply<I, 3>(dq, S, kLdP, K, ldd, d, ty, tx);
+            tile_apply(dq, S, kLdP, K, ldd, d, ty, tx);
         }
         if (pass == 0) {
 #pragma unroll
             for (int i = 0; i < I; ++i) {
                 delta[i] = half_warp_sum(sum[i]);
                 const int r = i0 + I * ty + i;
-                if (tx == 0 && r < w.lq) a.delta[int64_t(h) * a.Tq + w.q0 + r] = delta[i];
+                if (tx == 0 && r < w.lq && share.rank == 0) a.delta[int64_t(h) * a.Tq + w.q0 + r] = delta[i];
             }
         }
     }
     cp_async_wait();  // of a loop without turns
+    if (share.ranks > 1) {
+        __syncthreads();
+        leave<kThreads>(sm, dq);
+        cluster_sync();
+#pragma unroll
+        for (int i = 0; i < I; ++i)
+            if (share.owns(i)) gather<kThreads>(dq[i], sm, i, share.ranks);
+        cluster_sync();  // nobody leaves while its part is read
+    }
 #pragma unroll
     for (int i = 0; i < I; ++i) {
         const int r = i0 + I * ty + i;
-        if (r >= w.lq) continue;
+        if (r >= w.lq || !share.owns(i)) continue;
         T *out = static_cast<T *>(a.dq) + (int64_t(w.q0 + r) * a.H + h) * d;
 #pragma unroll
         for (int c = 0; c < 12; ++c) {
-            const int col = (c >> 2) * 64 + 4 * tx + (c & 3);
+            const int col = apply_column(c, d, tx);
             if (col < d) out[col] = from_f32<T>(dq[i][c]);
         }
     }
@@ -337,44 +404,90 @@ template <typename T> __global__ void dkr_kernel(const MlaArgs a) {
     static_cast<T *>(a.dk_rope)[i] = from_f32<T>(s);
 }
 
-// Shared memory of a kernel that owns `own` rows (floats): tiles of d and of d_v channels, own and streamed rows, and P.
-size_t prefill_smem(const MlaArgs &a, int own) {
-    return sizeof(float) * ((own + kT) * simt_row(a.dn + a.dr) + kT * simt_row(a.dv) + own * kLdP);
+// Shared memory of a kernel that owns `own` rows (floats): tiles of d and of d_v channels, own and streamed rows, and P;
+// in a cluster at least the sums that a block leaves for the others, `sums` floats an owned row.
+size_t prefill_smem(const MlaArgs &a, int own, int ranks) {
+    const size_t x = (own + kT) * simt_row(a.dn + a.dr) + kT * simt_row(a.dv) + own * kLdP, y = own * (128 + 2);
+    return sizeof(float) * (ranks > 1 && y > x ? y : x);
 }
-size_t grad_smem(const MlaArgs &a, int own, int tiles) {
-    return sizeof(float) * ((own + kT) * (simt_row(a.dn + a.dr) + simt_row(a.dv)) + tiles * own * kLdP);
+size_t grad_smem(const MlaArgs &a, int own, int tiles, int sums, int ranks) {
+    const size_t x = (own + kT) * (simt_row(a.dn + a.dr) + simt_row(a.dv)) + tiles * own * kLdP, y = own * sums;
+    return sizeof(float) * (ranks > 1 && y > x ? y : x);
 }
 
-template <typename K> cudaError_t launch(K *kernel, int64_t tiles, size_t smem, const MlaArgs &a, cudaStream_t st) {
-    if (tiles == 0) return cudaSuccess;
+struct Shape {
+    int own, ranks;   // owned rows of a block; blocks of a cluster
+    int64_t tiles;    // of `own` rows, in all sequences
+};
+// 64 owned rows a block, or 32 in very small calls and where most sequences would fill no more of 64.  A block's chain of
+// streamed tiles is worked through one after another; where the longest chain is long beside an SM's share of all tiles
+// it is the call's time, and the blocks of a cluster share each chain.  Eight only where the clusters find place at once
+// (the SMs come in groups of 16 and more).  Forward and backward in us, float32, d = 192 and 128, 64-row tiles, by
+// the longest chain over the SM's share, with 1, 2, 4 and 8 blocks a cluster:
+//   18   1 x 900 tokens, 1 head: 733, 412, 226, 139            6.2  3 heads: 733, 413, 229, 331
+//   4.8  six of 5 to 900, 3 heads: 734, 415, 322, 498          2.9  1 x 1024, 6 heads: 784, 419, 465, 671
+//   0.8  3 x 900, 8 heads: 1337, 1167, 1555, 2320              0.6  2 x 2048, 8 heads: 2891, 3021, 3720, 4970
+// 32-row tiles: 1 x 300 tokens, 1 head, 103 in clusters of four (64-row: 133); 64 x 16 tokens, 8 heads, d = 64 and 64,
+// 91 (64-row: 160); 1 x 1024 tokens, 6 heads, 510 at best.
+Shape shape(const MlaArgs &a, bool keys) {  // of the kernel whose blocks own queries, or keys
+    const int32_t *owned = keys ? a.cu_k_host : a.cu_q_host, *streamed = keys ? a.cu_q_host : a.cu_k_host;
+    const int64_t t32 = count_tiles(owned, a.num_seqs, 32), t64 = count_tiles(owned, a.num_seqs, 64), sms = device_sm_count();
+    Shape s;
+    s.own = 9 * t32 * a.H <= sms || 4 * t32 <= 5 * t64 ? 32 : 64;
+    s.tiles = s.own == 32 ? t32 : t64;
+    s.ranks = 1;
+    const int64_t blocks = s.tiles * a.H;
+    if (blocks > 4 * sms) return s;  // chains even out
+    int64_t longest = 0, sum = 0;
+    for (int i = 0; i < a.num_seqs; ++i) {
+        const int64_t lo = int64_t(owned[i + 1]) - owned[i], ls = int64_t(streamed[i + 1]) - streamed[i];
+        for (int64_t at = 0; at < lo; at += s.own) {
+            int64_t rows = ls;  // that meet a row of the tile
+            if (a.causal) rows = keys ? std::min(ls, lo - at) : std::max<int64_t>(0, std::min(at + s.own, lo) + ls - lo);
+            const int64_t chain = (rows + kT - 1) / kT;
+            longest = std::max(longest, chain);
+            sum += chain;
+        }
+    }
+    const double ratio = double(longest) * double(s.own == 32 ? 2 * sms : sms) / (double(sum) * a.H + 1.);
+    s.ranks = ratio >= 8. && 9 * blocks <= sms ? 8 : ratio >= 4.5 ? 4 : ratio >= 0.75 ? 2 : 1;
+    while (s.ranks > longest) s.ranks /= 2;
+    if (s.ranks < 1) s.ranks = 1;
+    return s;
+}
+
+template <typename K> cudaError_t launch(K *kernel, const Shape &s, size_t smem, const MlaArgs &a, cudaStream_t st) {
+    if (s.tiles == 0) return cudaSuccess;
+    if (s.tiles * a.H > INT32_MAX / kMostRanks) return cudaErrorInvalidValue;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
     if (e != cudaSuccess) return e;
-    kernel<<<dim3(unsigned(tiles), unsigned(a.H)), kThreads, smem, st>>>(a);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(unsigned(s.tiles * a.H * s.ranks));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute cluster{};
+    cluster.id = cudaLaunchAttributeClusterDimension;
+    cluster.val.clusterDim.x = unsigned(s.ranks);
+    cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
+    cfg.attrs = &cluster;
+    cfg.numAttrs = s.ranks > 1;
+    return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
-// 64 owned rows a block, or 32 where blocks of 64 would leave a third of the SMs idle: there the longest block's chain of
-// tiles is the call's time, and smaller tiles shorten it.  One float32 sequence of 1024 tokens, d = 192 and 128, forward
-// and backward: with 6 heads (96 blocks of 64) 163 and 521 us in tiles of 32, 185 and 627 in tiles of 64;
-// with 8 heads (128 blocks) 213 and 681 against 214 and 626.
-bool small_tiles(const int32_t *cu, const MlaArgs &a) { return 3 * count_tiles(cu, a.num_seqs, 64) * a.H < 2 * device_sm_count(); }
-
 template <typename T> cudaError_t prefill(const MlaArgs &a, cudaStream_t st) {
-    if (small_tiles(a.cu_q_host, a))
-        return launch(prefill_kernel<T, 2>, count_tiles(a.cu_q_host, a.num_seqs, 32), prefill_smem(a, 32), a, st);
-    return launch(prefill_kernel<T, 4>, count_tiles(a.cu_q_host, a.num_seqs, 64), prefill_smem(a, 64), a, st);
+    const Shape s = shape(a, false);
+    const size_t smem = prefill_smem(a, s.own, s.ranks);
+    return s.own == 32 ? launch(prefill_kernel<T, 2>, s, smem, a, st) : launch(prefill_kernel<T, 4>, s, smem, a, st);
 }
 
 template <typename T> cudaError_t backward(const MlaArgs &a, cudaStream_t st) {
-    cudaError_t e;  // dq first: it leaves the delta of the rows that see few keys
-    if (small_tiles(a.cu_q_host, a))
-        e = launch(dq_kernel<T, 2>, count_tiles(a.cu_q_host, a.num_seqs, 32), grad_smem(a, 32, 1), a, st);
-    else
-        e = launch(dq_kernel<T, 4>, count_tiles(a.cu_q_host, a.num_seqs, 64), grad_smem(a, 64, 1), a, st);
+    const Shape q = shape(a, false), k = shape(a, true);
+    const size_t q_smem = grad_smem(a, q.own, 1, 192, q.ranks), k_smem = grad_smem(a, k.own, 2, 320, k.ranks);
+    // dq first: it leaves the delta of the rows that see few keys
+    const cudaError_t e = q.own == 32 ? launch(dq_kernel<T, 2>, q, q_smem, a, st) : launch(dq_kernel<T, 4>, q, q_smem, a, st);
     if (e != cudaSuccess) return e;
-    if (small_tiles(a.cu_k_host, a))
-        return launch(dkv_kernel<T, 2>, count_tiles(a.cu_k_host, a.num_seqs, 32), grad_smem(a, 32, 2), a, st);
-    return launch(dkv_kernel<T, 4>, count_tiles(a.cu_k_host, a.num_seqs, 64), grad_smem(a, 64, 2), a, st);
+    return k.own == 32 ? launch(dkv_kernel<T, 2>, k, k_smem, a, st) : launch(dkv_kernel<T, 4>, k, k_smem, a, st);
 }
 
 }  // namespace

@@ -126,6 +126,62 @@ __device__ __forceinline__ void load_tile(float *dst, int ld, int at, const T *s
         }
     }
 }
+// The blocks of a cluster, which share the work on one tile of owned rows.
+struct Share {
+    int rank, ranks;
+    // Rows I ty + i of the owned tile whose sums this block makes and writes.
+    __device__ __forceinline__ bool owns(int i) const { return i % ranks == rank; }
+};
+__device__ __forceinline__ Share cluster_share() {
+    Share s;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(s.rank));
+    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(s.ranks));
+    return s;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// What block `rank` of the cluster holds where this one has p.
+__device__ __forceinline__ uint32_t peer_smem(const float *p, int rank) {
+    uint32_t at;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(uint32_t(__cvta_generic_to_shared(p))), "r"(rank));
+    return at;
+}
+__device__ __forceinline__ float4 load4_peer(const float *p, int rank) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(peer_smem(p, rank)) : "memory");
+    return v;
+}
+__device__ __forceinline__ float2 load2_peer(const float *p, int rank) {
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(peer_smem(p, rank)) : "memory");
+    return v;
+}
+// Leaves this block's sums at `at` (I * C * NT floats, 16-byte aligned) for the cluster.
+template <int NT, int I, int C> __device__ __forceinline__ void leave(float *at, const float (&acc)[I][C]) {
+#pragma unroll
+    for (int i = 0; i < I; ++i)
+#pragma unroll
+        for (int c = 0; c < C; c += 4)
+            *reinterpret_cast<float4 *>(at + ((i * C + c) * NT + 4 * threadIdx.x)) = make_float4(acc[i][c], acc[i][c + 1], acc[i][c + 2], acc[i][c + 3]);
+}
+// After a cluster_sync: row i's sums over all blocks, in the order of their ranks, block r's times f[r] where given.
+template <int NT, int C> __device__ __forceinline__ void gather(float (&row)[C], const float *at, int i, int ranks, const float *f = nullptr) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) row[c] = 0.f;
+    for (int r = 0; r < ranks; ++r) {
+        const float w = f ? f[r] : 1.f;
+#pragma unroll
+        for (int c = 0; c < C; c += 4) {
+            const float4 v = load4_peer(at + ((i * C + c) * NT + 4 * threadIdx.x), r);
+            row[c] = fmaf(w, v.x, row[c]);
+            row[c + 1] = fmaf(w, v.y, row[c + 1]);
+            row[c + 2] = fmaf(w, v.z, row[c + 2]);
+            row[c + 3] = fmaf(w, v.w, row[c + 3]);
+        }
+    }
+}
 // Zeroes columns [from, to) of every row.
 template <int NT> __device__ __forceinline__ void zero_columns(float *dst, int ld, int from, int to, int rows) {
     const int w = to - from;
@@ -155,42 +211,58 @@ __device__ __forceinline__ void tile_dot(float (&acc)[I][J], const float *A, int
     }
 }
 
-// acc[i][4 j + e] += sum_r P[I ty + i][r] * B[r][64 j + 4 tx + e] over r < 64, j < N.
-template <int N, int I, int C>
+// Columns of a row of `width`: pieces of 64, four neighbours a thread (of 16), then one of 32 with two a thread where
+// that covers the rest.  Column c of the sums of the thread at place tx; `width` itself when there is none.
+__device__ __forceinline__ int full_pieces(int width) { return (width + 31) / 64; }
+__device__ __forceinline__ int apply_column(int c, int width, int tx) {
+    const int full = full_pieces(width);
+    if (c < 4 * full) return (c >> 2) * 64 + 4 * tx + (c & 3);
+    return c < 4 * full + 2 ? 64 * full + 2 * tx + (c & 1) : width;
+}
+
+// acc[i][c] += sum_r P[I ty + i][r] * B[r][column c] over r < 64, of N pieces of 64 columns and TAIL of 32.
+template <int N, int TAIL, int I, int C>
 __device__ __forceinline__ void tile_apply_n(float (&acc)[I][C], const float *P, int ldp, const float *B, int ldb, int ty, int tx) {
 #pragma unroll 2
     for (int r = 0; r < 64; r += 4) {
-        float4 p[I], b[4][N];
+        float4 p[I], b[4][N + 1];
 #pragma unroll
         for (int i = 0; i < I; ++i) p[i] = *reinterpret_cast<const float4 *>(P + (I * ty + i) * ldp + r);
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
+        for (int e = 0; e < 4; ++e) {
 #pragma unroll
             for (int j = 0; j < N; ++j) b[e][j] = *reinterpret_cast<const float4 *>(B + (r + e) * ldb + 64 * j + 4 * tx);
+            if constexpr (TAIL) {
+                const float2 t = *reinterpret_cast<const float2 *>(B + (r + e) * ldb + 64 * N + 2 * tx);
+                b[e][N].x = t.x, b[e][N].y = t.y;
+            }
+        }
 #pragma unroll
         for (int e = 0; e < 4; ++e)
 #pragma unroll
-            for (int j = 0; j < N; ++j)
+            for (int j = 0; j < N + TAIL; ++j)
 #pragma unroll
                 for (int i = 0; i < I; ++i) {
                     const float w = e == 0 ? p[i].x : e == 1 ? p[i].y : e == 2 ? p[i].z : p[i].w;
-                    acc[i][4 * j + 0] = fmaf(w, b[e][j].x, acc[i][4 * j + 0]);
+                    acc[i][4 * j] = fmaf(w, b[e][j].x, acc[i][4 * j]);
                     acc[i][4 * j + 1] = fmaf(w, b[e][j].y, acc[i][4 * j + 1]);
+                    if (j == N) continue;
                     acc[i][4 * j + 2] = fmaf(w, b[e][j].z, acc[i][4 * j + 2]);
                     acc[i][4 * j + 3] = fmaf(w, b[e][j].w, acc[i][4 * j + 3]);
                 }
     }
 }
 
-// The same for the j with 64 j < width.  Threads whose columns lie behind `width` read what follows a row (the
-// buffers behind B are larger than a row) and make sums that nobody stores: a test inside the loops keeps
-// their loads from running ahead (16,500 cycles a 32 x 64 tile of 80 channels with one, 4,700 without).
-template <int I, int J>
-__device__ __forceinline__ void tile_apply(float (&acc)[I][4 * J], const float *P, int ldp, const float *B, int ldb,
-                                           int width, int ty, int tx) {
-    if (width <= 64) tile_apply_n<1>(acc, P, ldp, B, ldb, ty, tx);
-    else if (width <= 128 || J == 2) tile_apply_n<2>(acc, P, ldp, B, ldb, ty, tx);
-    else tile_apply_n<J>(acc, P, ldp, B, ldb, ty, tx);
+// The same for the columns below `width` (at most 16 C).  Threads whose columns lie behind `width` read what pads a
+// row, or what follows it, and make sums that nobody stores: a test inside the loops keeps their loads from running
+// ahead (16,500 cycles a 32 x 64 tile of 80 channels with one, 4,700 without, of 128 columns then).
+template <int I, int C, int N = 0>
+__device__ __forceinline__ void tile_apply(float (&acc)[I][C], const float *P, int ldp, const float *B, int ldb, int width, int ty, int tx) {
+    if constexpr (4 * N < C) {
+        if (width > 64 * N + 32) return tile_apply<I, C, N + 1>(acc, P, ldp, B, ldb, width, ty, tx);
+        if (width > 64 * N) return tile_apply_n<N, 1>(acc, P, ldp, B, ldb, ty, tx);
+    }
+    tile_apply_n<N, 0>(acc, P, ldp, B, ldb, ty, tx);
 }
 
 }  // namespace kda

@@ -203,6 +203,28 @@ def test_gradients_lose_no_precision_where_keys_are_few(lens, dims):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("q_lens,k_lens,H,causal", [
+    ([500], [500], 2, True),                        # 64-row tiles, clusters of eight blocks
+    ([700, 33], [700, 40], 3, True),                # of four
+    ([600, 33, 600], [600, 33, 500], 5, True),      # of two, queries that see nothing
+    ([200] * 30, [200] * 30, 4, True),              # one block
+    ([300], [300], 1, True),                        # 32-row tiles
+    ([5], [1000], 1, False),                        # a long chain of keys, dk and dv of one short one
+    ([1000], [3], 2, False),
+    ([16] * 20, [16] * 20, 8, True)])
+def test_clusters_share_chains(q_lens, k_lens, H, causal, dtype):
+    """Blocks that share a tile's chain on the CUDA cores give the formula's sums, the same ones every time."""
+    a, dO = packed(q_lens, k_lens, H, 40, 8, 48, dtype, seed=3)
+    o, lse = mla_prefill(**a, causal=causal, want_lse=True)
+    check_prefill(a, o, lse, causal=causal)
+    g = mla_backward(**a, o=o, lse=lse, dO=dO, causal=causal)
+    check_backward(a, dO, g, causal=causal)
+    o2, lse2 = mla_prefill(**a, causal=causal, want_lse=True)
+    g2 = mla_backward(**a, o=o, lse=lse, dO=dO, causal=causal)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2) and all(torch.equal(g[n], g2[n]) for n in g)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
 def test_rows_outside_the_sequences(dtype):
     """Rows behind the last sequence hold NaN: nothing of them is read into a sum, nothing written."""
     a, dO = packed([70, 130], [70, 200], 2, 128, 64, 128, dtype)
