@@ -3,9 +3,12 @@
 //
 // A block works through its run of tiles (mla_decode_plan.cuh): kRows query rows against
 // kKeys cache rows at a time, both in shared memory as float32, so that each cache row is
-// read from memory once for all heads and tokens of a row tile.  The softmax is online.  Bound by latency at
-// small sizes (nine sequences of up to 3,001 rows, 12 heads, d_latent 256, float32: 27 us and 8 of join) and by the FMA
-// pipes and shared memory at large ones.
+// read from memory once for all heads and tokens of a row tile.  The softmax is online.
+// Bound by latency at small sizes and by the FMA pipes and shared memory at large ones.
+// Float32, d_latent 256: nine sequences of up to 3,001 rows, 12 heads 19 us and 8 of join;
+// d_latent 512 and 64 shared, 16 heads: 60 sequences of 1,000 rows 101 us, one of 60,000
+// 109 us (166 and 176 us with one score of a row's whole width a thread and a key, and
+// registers for one block an SM).
 #include <cmath>
 
 #include "mla_decode_plan.cuh"
@@ -19,15 +22,17 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kRows = 16;
 constexpr int kKeys = 32;
+constexpr int kLdP = kRows + 4;
 
-size_t simt_smem(int W) { return sizeof(float) * ((kRows + kKeys) * simt_row(W) + kKeys * kRows + 3 * kRows); }
+size_t simt_smem(int W) { return sizeof(float) * ((kRows + kKeys) * simt_row(W) + kKeys * kLdP + 3 * kRows); }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads) decode_kernel(const MlaDecodeArgs a, const MlaDecodeShape shape) {
+// C output columns a thread: tid and, where d_latent is above 256, tid + 256.
+template <typename T, int C>
+__global__ void __launch_bounds__(kThreads, 2) decode_kernel(const MlaDecodeArgs a, const MlaDecodeShape shape) {
     extern __shared__ float sm[];
     __shared__ int64_t buf[kThreads / 32 + 4], place[kKeys];
     const int W = a.dc + a.dr, W4 = (W + 3) & ~3, ld = simt_row(W), R = a.n * a.H;
-    float *Q = sm, *K = Q + kRows * ld, *P = K + kKeys * ld, *Keep = P + kKeys * kRows, *M = Keep + kRows, *L = M + kRows;
+    float *Q = sm, *K = Q + kRows * ld, *P = K + kKeys * ld, *Keep = P + kKeys * kLdP, *M = Keep + kRows, *L = M + kRows;
     const int tid = threadIdx.x, sr = tid >> 4, sk = tid & 15;
     MlaJoin *join = static_cast<MlaJoin *>(a.workspace);
     float *slots = reinterpret_cast<float *>(static_cast<char *>(a.workspace) + mla_meta_bytes(gridDim.x));
@@ -47,7 +52,7 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(const MlaDecodeArgs a,
         __syncthreads();
         load_tile<T, kThreads, kRows>(Q, ld, 0, static_cast<const T *>(a.q) + (int64_t(b) * R + r0) * W, W, W, rows);
         float m = -INFINITY, l = 0.f;  // of row sr, the same in its 16 threads
-        float o[kRows][2] = {};        // columns tid and tid + 256
+        float o[kRows][C] = {};
         for (int t = w.t0; t < w.t1; ++t) {
             const int j0 = t * kKeys;
             __syncthreads();
@@ -70,7 +75,6 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(const MlaDecodeArgs a,
                         const int64_t at = place[sr + 16 * e];
                         copy4_async(K + (sr + 16 * e) * ld + c, static_cast<const float *>(a.cache) + (at >= 0 ? at * W + c : 0), at >= 0);
                     }
-                cp_async_wait();
             } else if ((W & 3) == 0) {
                 for (int c = 4 * sk; c < W; c += 64) {
                     float4 v[2];
@@ -90,23 +94,44 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(const MlaDecodeArgs a,
                         K[(sr + 16 * e) * ld + c] = at >= 0 ? to_f32(pool[at * W + c]) : 0.f;
                     }
             }
+            cp_async_wait();
             __syncthreads();
-            float4 dot[2] = {};  // four partial sums each
-#pragma unroll 6
-            for (int c = 0; c < W4; c += 4) {
-                const float4 q = *reinterpret_cast<const float4 *>(Q + sr * ld + c);
+            {
+                // A thread makes 4 x 4 scores over every eighth group of four channels: a third of the shared-memory loads a
+                // product that two whole scores a thread take.  Eight lanes then add theirs and keep two scores each.
+                const int cg = tid & 7, qr = tid >> 6 << 2, kr = tid >> 3 & 7;  // channels; rows qr + i; keys kr + 8 e
+                float v[16] = {};
+#pragma unroll 3
+                for (int c = 4 * cg; c < W4; c += 32) {
+                    float4 q[4], k[4];
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float4 k = *reinterpret_cast<const float4 *>(K + (sk + 16 * e) * ld + c);
-                    dot[e].x = fmaf(q.x, k.x, dot[e].x);
-                    dot[e].y = fmaf(q.y, k.y, dot[e].y);
-                    dot[e].z = fmaf(q.z, k.z, dot[e].z);
-                    dot[e].w = fmaf(q.w, k.w, dot[e].w);
+                    for (int i = 0; i < 4; ++i) q[i] = *reinterpret_cast<const float4 *>(Q + (qr + i) * ld + c);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) k[e] = *reinterpret_cast<const float4 *>(K + (kr + 8 * e) * ld + c);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            v[4 * i + e] = fmaf(q[i].x, k[e].x, fmaf(q[i].y, k[e].y, fmaf(q[i].z, k[e].z, fmaf(q[i].w, k[e].w, v[4 * i + e]))));
                 }
+                __syncwarp();
+#pragma unroll
+                for (int n = 8; n > 1; n >>= 1) {  // n values stay; the partner, whose bit n / 2 of cg differs, takes the others
+                    const bool upper = cg & (n >> 1);
+#pragma unroll
+                    for (int i = 0; i < n; ++i) {
+                        const float other = __shfl_xor_sync(0xffffffffu, upper ? v[i] : v[i + n], n >> 1);
+                        v[i] = (upper ? v[i + n] : v[i]) + other;
+                    }
+                }
+                const int e = 2 * (cg & 1);
+                P[(kr + 8 * e) * kLdP + qr + (cg >> 1)] = v[0];
+                P[(kr + 8 * e + 8) * kLdP + qr + (cg >> 1)] = v[1];
             }
+            __syncthreads();
             float s[2];
 #pragma unroll
-            for (int e = 0; e < 2; ++e) s[e] = (dot[e].x + dot[e].y) + (dot[e].z + dot[e].w);
+            for (int e = 0; e < 2; ++e) s[e] = P[(sk + 16 * e) * kLdP + sr];
             const int end = len - (a.n - 1) + (r0 + sr) / a.H;  // keys that row sr's token sees
             float top = m;
 #pragma unroll
@@ -123,7 +148,7 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(const MlaDecodeArgs a,
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const float p = expf(s[e] - base);
-                P[(sk + 16 * e) * kRows + sr] = p;
+                P[(sk + 16 * e) * kLdP + sr] = p;
                 sum += p;
             }
 #pragma unroll
@@ -135,24 +160,24 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(const MlaDecodeArgs a,
 #pragma unroll
             for (int r = 0; r < kRows; ++r) {
                 const float f = Keep[r];
-                o[r][0] *= f;
-                o[r][1] *= f;
+#pragma unroll
+                for (int c = 0; c < C; ++c) o[r][c] *= f;
             }
-#pragma unroll 8
+#pragma unroll 4
             for (int j = 0; j < kKeys; ++j) {
-                const float v0 = tid < a.dc ? K[j * ld + tid] : 0.f;
-                const float v1 = tid + kThreads < a.dc ? K[j * ld + tid + kThreads] : 0.f;
+                float v[C];
+#pragma unroll
+                for (int c = 0; c < C; ++c) v[c] = K[j * ld + min(tid + c * kThreads, W - 1)];  // columns from d_latent on are not stored
 #pragma unroll
                 for (int r = 0; r < kRows; r += 4) {
-                    const float4 p = *reinterpret_cast<const float4 *>(P + j * kRows + r);
-                    o[r + 0][0] = fmaf(p.x, v0, o[r + 0][0]);
-                    o[r + 0][1] = fmaf(p.x, v1, o[r + 0][1]);
-                    o[r + 1][0] = fmaf(p.y, v0, o[r + 1][0]);
-                    o[r + 1][1] = fmaf(p.y, v1, o[r + 1][1]);
-                    o[r + 2][0] = fmaf(p.z, v0, o[r + 2][0]);
-                    o[r + 2][1] = fmaf(p.z, v1, o[r + 2][1]);
-                    o[r + 3][0] = fmaf(p.w, v0, o[r + 3][0]);
-                    o[r + 3][1] = fmaf(p.w, v1, o[r + 3][1]);
+                    const float4 p = *reinterpret_cast<const float4 *>(P + j * kLdP + r);
+#pragma unroll
+                    for (int c = 0; c < C; ++c) {
+                        o[r + 0][c] = fmaf(p.x, v[c], o[r + 0][c]);
+                        o[r + 1][c] = fmaf(p.y, v[c], o[r + 1][c]);
+                        o[r + 2][c] = fmaf(p.z, v[c], o[r + 2][c]);
+                        o[r + 3][c] = fmaf(p.w, v[c], o[r + 3][c]);
+                    }
                 }
             }
         }
@@ -164,18 +189,19 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(const MlaDecodeArgs a,
             for (int r = 0; r < kRows; ++r)
                 if (r < rows) {
                     const float lr = L[r], inv = lr == 0.f ? 0.f : 1.f / lr;
-                    if (tid < a.dc) out[r * a.dc + tid] = from_f32<T>(o[r][0] * inv);
-                    if (tid + kThreads < a.dc) out[r * a.dc + tid + kThreads] = from_f32<T>(o[r][1] * inv);
+#pragma unroll
+                    for (int c = 0; c < C; ++c)
+                        if (tid + c * kThreads < a.dc) out[r * a.dc + tid + c * kThreads] = from_f32<T>(o[r][c] * inv);
                 }
             if (a.lse && tid < rows)
                 a.lse[int64_t(b) * R + r0 + tid] = L[tid] == 0.f ? -INFINITY : M[tid] + logf(L[tid]);
         } else {
             float *p = slots + mla_slot(w) * slot_floats;
 #pragma unroll
-            for (int r = 0; r < kRows; ++r) {
-                if (tid < a.dc) p[r * a.dc + tid] = o[r][0];
-                if (tid + kThreads < a.dc) p[r * a.dc + tid + kThreads] = o[r][1];
-            }
+            for (int r = 0; r < kRows; ++r)
+#pragma unroll
+                for (int c = 0; c < C; ++c)
+                    if (tid + c * kThreads < a.dc) p[r * a.dc + tid + c * kThreads] = o[r][c];
             if (tid < kRows) {
                 p[kRows * a.dc + 2 * tid] = M[tid];
                 p[kRows * a.dc + 2 * tid + 1] = L[tid];
@@ -264,9 +290,10 @@ __global__ void __launch_bounds__(kJoinLanes * SPLIT) join_kernel(const MlaDecod
 
 template <typename T> cudaError_t launch_simt(const MlaDecodeArgs &a, const MlaDecodeShape &s, cudaStream_t st) {
     const size_t smem = simt_smem(a.dc + a.dr);
-    const cudaError_t e = cudaFuncSetAttribute(decode_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    const auto kernel = a.dc > kThreads ? decode_kernel<T, 2> : decode_kernel<T, 1>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
     if (e != cudaSuccess) return e;
-    decode_kernel<T><<<s.grid(), kThreads, smem, st>>>(a, s);
+    kernel<<<s.grid(), kThreads, smem, st>>>(a, s);
     return cudaGetLastError();
 }
 
