@@ -3,6 +3,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import math
 
 import torch
@@ -59,7 +60,7 @@ def _on(stream, index):
             raise ValueError(f"stream is on cuda:{stream.device_index}, the tensors on cuda:{index}")
         return _switched(stream, index), stream.cuda_stream
     raw = torch._C._cuda_getCurrentRawStream(index)
-    return (_NOTHING if torch.cuda.current_device() == index else torch.cuda.device(index)), raw
+    return (_NOTHING if torch._C._cuda_getDevice() == index else torch.cuda.device(index)), raw
 
 
 _NOTHING = contextlib.nullcontext()
@@ -128,12 +129,12 @@ def _sizes(t, name, ndim):
 
 def _host_offsets(cu, host, rows):
     """(sequences, host copy of the offsets, their last): as ``_binding._offsets``, at a serving step's cost."""
-    if isinstance(host, torch.Tensor) and host.dtype is torch.int32 and host.device.type == "cpu" and \
-            host.dim() == 1 and host.is_contiguous() and host.numel() > 0 and isinstance(cu, torch.Tensor) and \
-            cu.shape == host.shape:
-        last = host[-1].item()
+    if isinstance(host, torch.Tensor) and host.dtype is torch.int32 and host.is_cpu and host.dim() == 1 and \
+            host.is_contiguous() and isinstance(cu, torch.Tensor) and cu.shape == host.shape:
+        n = host.numel()
+        last = host.tolist()[-1] if 0 < n <= 32 else host[-1].item() if n else rows + 1  # the list is quicker if short
         if last <= rows:
-            return host.numel() - 1, host, last
+            return n - 1, host, last
     n, host = _offsets(cu, host, rows)
     return n, host, int(host[-1])
 
@@ -216,6 +217,12 @@ def mla_append(c, k_rope, cache, page_table, past_lens, cu_seqlens, norm_weight=
     return res
 
 
+@functools.lru_cache(maxsize=256)
+def _decode_workspace(index, *sizes):
+    """Workspace bytes on device ``index``, which is the current one."""
+    return max(_lib().mla_decode_workspace_size(*sizes), 256)
+
+
 def mla_decode_workspace_size(B, n, H, d_latent, d_rope, dtype=torch.bfloat16):
     return int(_lib().mla_decode_workspace_size(int(B), int(n), int(H), int(d_latent), int(d_rope), DTYPE_CODE[dtype]))
 
@@ -248,8 +255,8 @@ def mla_decode(q, cache, page_table, seq_lens, d_latent, scale, o=None, lse=None
         if lse is None and want_lse:
             lse = torch.empty(B, n, H, dtype=torch.float32, device=q.device)
         if workspace is None:
-            size = lib.mla_decode_workspace_size(B, n, H, dc, W - dc, DTYPE_CODE[dt])
-            workspace = torch.empty(max(size, 256), dtype=torch.uint8, device=q.device)
+            workspace = torch.empty(_decode_workspace(index, B, n, H, dc, W - dc, DTYPE_CODE[dt]), dtype=torch.uint8,
+                                    device=q.device)
         st = lib.mla_decode(q.data_ptr(), DTYPE_CODE[dt], cache.data_ptr(), pages, page, page_table.data_ptr(), width,
                             seq_lens.data_ptr(), B, n, H, dc, W - dc, scale, o.data_ptr(), _ptr(lse),
                             workspace.data_ptr(), workspace.numel() * workspace.element_size(), raw)
