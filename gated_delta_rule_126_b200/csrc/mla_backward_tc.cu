@@ -650,10 +650,10 @@ cudaError_t launch_mla_backward_tc(const MlaArgs &a, cudaStream_t st) {
     if (!ok) return cudaErrorInvalidValue;
     // dq first: it leaves the exact delta of the rows that see few keys.  Its tiles from the last queries, which see most
     // keys, on; dk and dv's from the first keys, which most queries see.
-    const cudaError_t e = launch<dq_tc_kernel>(qs, list_tiles(a.cu_q_host, a.cu_k_host, a.num_seqs, 128, true),
+    const cudaError_t e = launch<dq_tc_kernel>(qs, list_tiles(a.cu_q_host, a.num_seqs, 128, true),
                                                count_tiles(a.cu_q_host, a.num_seqs, 128), kDqSmem, a, st);
     if (e != cudaSuccess) return e;
-    return launch<dkv_tc_kernel>(kv, list_tiles(a.cu_k_host, a.cu_q_host, a.num_seqs, 128, false), count_tiles(a.cu_k_host, a.num_seqs, 128),
+    return launch<dkv_tc_kernel>(kv, list_tiles(a.cu_k_host, a.num_seqs, 128, false), count_tiles(a.cu_k_host, a.num_seqs, 128),
                                  kDkvSmem, a, st);
 }
 

@@ -5,8 +5,6 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
-#include <algorithm>
-
 #include "mla.h"
 
 namespace kda {
@@ -82,30 +80,21 @@ inline int64_t count_tiles(const int32_t *cu, int n, int tile) {
 
 // The tiles of a call in the order in which its blocks take them, for calls of few tiles (longer ones find
 // theirs on the device, at a few microseconds a block): sequence by sequence, because the tiles of a sequence share
-// its rows in L2 (sorted by work over all sequences, 4 x 4096 tokens of 32 heads took 15 to 20% longer), those with the
-// longest chains of streamed rows first, so that the call ends with short ones.
+// its rows in L2 (sorted by work over all sequences, 4 x 4096 tokens of 32 heads took 15 to 20% longer).
 struct MlaTiles {
     static constexpr int kMost = 256;
     int count;
     uint32_t items[kMost];  // sequence << 16 | tile
 };
-// The tiles of `tile` rows of the host offsets `owned` (cu_q or cu_k; `streamed` is the other): a sequence's last first
-// where `reversed`.
-inline MlaTiles list_tiles(const int32_t *owned, const int32_t *streamed, int num_seqs, int tile, bool reversed) {
+// The tiles of `tile` rows of a host offset array (cu_q or cu_k): the last first where `reversed`.
+inline MlaTiles list_tiles(const int32_t *cu, int num_seqs, int tile, bool reversed) {
     MlaTiles list;
     list.count = 0;
-    if (count_tiles(owned, num_seqs, tile) > MlaTiles::kMost || num_seqs > 65535) return list;
-    struct Sequence {
-        int32_t rows, s;
-    } order[MlaTiles::kMost];
-    int n = 0;
+    const int64_t total = count_tiles(cu, num_seqs, tile);
+    if (total > MlaTiles::kMost || num_seqs > 65535) return list;
     for (int s = 0; s < num_seqs; ++s)
-        if (owned[s + 1] > owned[s]) order[n++] = Sequence{streamed[s + 1] - streamed[s], s};
-    std::sort(order, order + n, [](const Sequence &x, const Sequence &y) { return x.rows != y.rows ? x.rows > y.rows : x.s < y.s; });
-    for (int i = 0; i < n; ++i) {
-        const int s = order[i].s, tiles = (owned[s + 1] - owned[s] - 1) / tile + 1;
-        for (int t = 0; t < tiles; ++t) list.items[list.count++] = uint32_t(s) << 16 | uint32_t(reversed ? tiles - 1 - t : t);
-    }
+        for (int t = 0; t * tile < cu[s + 1] - cu[s]; ++t)
+            list.items[reversed ? total - 1 - list.count : list.count] = uint32_t(s) << 16 | uint32_t(t), ++list.count;
     return list;
 }
 

@@ -373,7 +373,7 @@ cudaError_t launch_mla_prefill_tc(const MlaArgs &a, cudaStream_t st) {
         return cudaErrorInvalidValue;
     const cudaError_t e = tc::allow_smem<prefill_tc_kernel>(int(kSmem));
     if (e != cudaSuccess) return e;
-    const MlaTiles list = list_tiles(a.cu_q_host, a.cu_k_host, a.num_seqs, 2 * kRows, true);  // a sequence's last queries, which see most keys, first
+    const MlaTiles list = list_tiles(a.cu_q_host, a.num_seqs, 2 * kRows, true);  // a sequence's last queries, which see most keys, first
     prefill_tc_kernel<<<unsigned(grid), kThreads, kSmem, st>>>(maps, a, list);
     return cudaGetLastError();
 }
