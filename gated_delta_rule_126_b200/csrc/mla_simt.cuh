@@ -192,13 +192,18 @@ template <int NT> __device__ __forceinline__ void zero_columns(float *dst, int l
 template <int I, int J>
 __device__ __forceinline__ void tile_dot(float (&acc)[I][J], const float *A, int lda, const float *B, int ldb, int d4,
                                          int ty, int tx) {
+    float4 x[I], y[J];
+#pragma unroll
+    for (int i = 0; i < I; ++i) x[i] = *reinterpret_cast<const float4 *>(A + (I * ty + i) * lda);
+#pragma unroll
+    for (int j = 0; j < J; ++j) y[j] = *reinterpret_cast<const float4 *>(B + (tx + 16 * j) * ldb);
 #pragma unroll 4
-    for (int c = 0; c < d4; c += 4) {
-        float4 x[I], y[J];
+    for (int c = 4; c <= d4; c += 4) {  // the next four channels' loads run behind these products (the last ones read padding)
+        float4 u[I], v[J];
 #pragma unroll
-        for (int i = 0; i < I; ++i) x[i] = *reinterpret_cast<const float4 *>(A + (I * ty + i) * lda + c);
+        for (int i = 0; i < I; ++i) u[i] = *reinterpret_cast<const float4 *>(A + (I * ty + i) * lda + c);
 #pragma unroll
-        for (int j = 0; j < J; ++j) y[j] = *reinterpret_cast<const float4 *>(B + (tx + 16 * j) * ldb + c);
+        for (int j = 0; j < J; ++j) v[j] = *reinterpret_cast<const float4 *>(B + (tx + 16 * j) * ldb + c);
 #pragma unroll
         for (int i = 0; i < I; ++i)
 #pragma unroll
@@ -208,6 +213,10 @@ __device__ __forceinline__ void tile_dot(float (&acc)[I][J], const float *A, int
                 acc[i][j] = fmaf(x[i].z, y[j].z, acc[i][j]);
                 acc[i][j] = fmaf(x[i].w, y[j].w, acc[i][j]);
             }
+#pragma unroll
+        for (int i = 0; i < I; ++i) x[i] = u[i];
+#pragma unroll
+        for (int j = 0; j < J; ++j) y[j] = v[j];
     }
 }
 
