@@ -232,33 +232,39 @@ __device__ __forceinline__ int apply_column(int c, int width, int tx) {
 // acc[i][c] += sum_r P[I ty + i][r] * B[r][column c] over r < 64, of N pieces of 64 columns and TAIL of 32.
 template <int N, int TAIL, int I, int C>
 __device__ __forceinline__ void tile_apply_n(float (&acc)[I][C], const float *P, int ldp, const float *B, int ldb, int ty, int tx) {
+    constexpr int M = N + TAIL;
+    float4 b[M], next[M];
+    auto fetch = [&](float4 (&to)[M], int r) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) to[j] = *reinterpret_cast<const float4 *>(B + r * ldb + 64 * j + 4 * tx);
+        if constexpr (TAIL) {
+            const float2 t = *reinterpret_cast<const float2 *>(B + r * ldb + 64 * N + 2 * tx);
+            to[N].x = t.x, to[N].y = t.y;
+        }
+    };
+    fetch(b, 0);
 #pragma unroll 2
     for (int r = 0; r < 64; r += 4) {
-        float4 p[I], b[4][N + 1];
+        float4 p[I];
 #pragma unroll
         for (int i = 0; i < I; ++i) p[i] = *reinterpret_cast<const float4 *>(P + (I * ty + i) * ldp + r);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
+            fetch(next, min(r + e + 1, 63));  // behind this row's products
 #pragma unroll
-            for (int j = 0; j < N; ++j) b[e][j] = *reinterpret_cast<const float4 *>(B + (r + e) * ldb + 64 * j + 4 * tx);
-            if constexpr (TAIL) {
-                const float2 t = *reinterpret_cast<const float2 *>(B + (r + e) * ldb + 64 * N + 2 * tx);
-                b[e][N].x = t.x, b[e][N].y = t.y;
-            }
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-#pragma unroll
-            for (int j = 0; j < N + TAIL; ++j)
+            for (int j = 0; j < M; ++j)
 #pragma unroll
                 for (int i = 0; i < I; ++i) {
                     const float w = e == 0 ? p[i].x : e == 1 ? p[i].y : e == 2 ? p[i].z : p[i].w;
-                    acc[i][4 * j] = fmaf(w, b[e][j].x, acc[i][4 * j]);
-                    acc[i][4 * j + 1] = fmaf(w, b[e][j].y, acc[i][4 * j + 1]);
+                    acc[i][4 * j] = fmaf(w, b[j].x, acc[i][4 * j]);
+                    acc[i][4 * j + 1] = fmaf(w, b[j].y, acc[i][4 * j + 1]);
                     if (j == N) continue;
-                    acc[i][4 * j + 2] = fmaf(w, b[e][j].z, acc[i][4 * j + 2]);
-                    acc[i][4 * j + 3] = fmaf(w, b[e][j].w, acc[i][4 * j + 3]);
+                    acc[i][4 * j + 2] = fmaf(w, b[j].z, acc[i][4 * j + 2]);
+                    acc[i][4 * j + 3] = fmaf(w, b[j].w, acc[i][4 * j + 3]);
                 }
+#pragma unroll
+            for (int j = 0; j < M; ++j) b[j] = next[j];
+        }
     }
 }
 
@@ -271,7 +277,7 @@ __device__ __forceinline__ void tile_apply(float (&acc)[I][C], const float *P, i
         if (width > 64 * N + 32) return tile_apply<I, C, N + 1>(acc, P, ldp, B, ldb, width, ty, tx);
         if (width > 64 * N) return tile_apply_n<N, 1>(acc, P, ldp, B, ldb, ty, tx);
     }
-    tile_apply_n<N, 0>(acc, P, ldp, B, ldb, ty, tx);
+    if constexpr (N > 0) tile_apply_n<N, 0>(acc, P, ldp, B, ldb, ty, tx);
 }
 
 }  // namespace kda
