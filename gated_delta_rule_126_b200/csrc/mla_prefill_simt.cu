@@ -7,10 +7,11 @@
 // that its owned rows meet, one after another; in calls of few blocks that chain is the
 // call's time, so the blocks of a cluster take its tiles in turn and add their parts through
 // distributed shared memory, in the order of their ranks.
-// Bound by the float32 FMA pipes and shared memory (57% of issue slots used while an SM has
-// work, 3.2 shared-memory wavefronts a load); three float32 sequences of 700, 33 and 1025
-// tokens, 4 heads, d = 96 and 80, take 75 us forward, 97 us for dq and 137 us for dk and dv
-// (with one block a chain, heads one after another and columns in whole 64s 138, 182 and 252).
+// Bound by shared-memory loads (3.2 wavefronts each; 57% of issue slots used while an SM has
+// work; sums of two products an instruction change nothing); three float32 sequences of 700,
+// 33 and 1025 tokens, 4 heads, d = 96 and 80, take 71 us forward, 94 us for dq and 132 us for
+// dk and dv (with one block a chain, heads one after another, columns in whole 64s and loads
+// not ahead 138, 182 and 252).
 #include <algorithm>
 #include <cmath>
 
