@@ -5,7 +5,8 @@ import numpy as np
 import pytest
 import torch
 
-from gated_delta_rule_126_b200 import mla_append, mla_backward, mla_decode, mla_prefill, mla_status
+from gated_delta_rule_126_b200 import (mla_append, mla_backward, mla_decode, mla_decode_workspace_size, mla_prefill,
+                                       mla_status)
 from oracle import mla
 from tests.mla_check import (U, check_backward, check_decode, check_lse, check_prefill, close, host, i32, offsets,
                              packed, pages)
@@ -466,6 +467,37 @@ def test_streams_and_graphs():
         check_decode(q, cache, table, [8 + k, 301], 512, 0.07, og, None)
         assert torch.equal(cache[int(table[0, 0]), 7 + k], row[0])
         assert torch.equal(pg, o) and all(torch.equal(g[x], gg[x]) for x in g)
+
+
+def test_captured_on_the_cuda_cores():
+    """Float32 calls, their clusters and their join, captured with one workspace for two decodes and replayed on new data."""
+    a, dO = packed([300, 90], [300, 90], 2, 72, 24, 80, F32)
+    lens = [700, 31]
+    table, n = pages(lens, 16)
+    cache, q = rnd(n, 16, 288, dtype=F32), rnd(2, 1, 12, 288, dtype=F32, seed=1)
+    table_d, lens_d = i32(table), i32(lens)
+    ws = torch.empty(mla_decode_workspace_size(2, 1, 12, 256, 32, F32), dtype=torch.uint8, device="cuda")
+    mla_prefill(**a)
+    mla_decode(q, cache, table_d, lens_d, 256, 0.07)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o, lse = mla_prefill(**a, want_lse=True)
+        g = mla_backward(**a, o=o, lse=lse, dO=dO)
+        first, _ = mla_decode(q, cache, table_d, lens_d, 256, 0.07, workspace=ws)
+        second, _ = mla_decode(q, cache, table_d, lens_d, 256, 0.2, workspace=ws)
+    for k in range(2):
+        b, dO2 = packed([300, 90], [300, 90], 2, 72, 24, 80, F32, seed=30 + k)
+        for name in ("q", "k", "v", "k_rope"):
+            a[name].copy_(b[name])
+        dO.copy_(dO2)
+        q.copy_(rnd(2, 1, 12, 288, dtype=F32, seed=40 + k))
+        graph.replay()
+        torch.cuda.synchronize()
+        check_prefill(a, o, lse)
+        check_backward(a, dO, g)
+        check_decode(q, cache, table, lens, 256, 0.07, first, None)
+        check_decode(q, cache, table, lens, 256, 0.2, second, None)
 
 
 def test_long_cache_offsets():
