@@ -425,11 +425,13 @@ struct Shape {
 // it is the call's time, and the blocks of a cluster share each chain.  Eight only where the clusters find place at once
 // (the SMs come in groups of 16 and more).  Forward and backward in us, float32, d = 192 and 128, 64-row tiles, by
 // the longest chain over the SM's share, with 1, 2, 4 and 8 blocks a cluster:
-//   18   1 x 900 tokens, 1 head: 733, 412, 226, 139            6.2  3 heads: 733, 413, 229, 331
-//   4.8  six of 5 to 900, 3 heads: 734, 415, 322, 498          2.9  1 x 1024, 6 heads: 784, 419, 465, 671
-//   0.8  3 x 900, 8 heads: 1337, 1167, 1555, 2320              0.6  2 x 2048, 8 heads: 2891, 3021, 3720, 4970
-// 32-row tiles: 1 x 300 tokens, 1 head, 103 in clusters of four (64-row: 133); 64 x 16 tokens, 8 heads, d = 64 and 64,
-// 91 (64-row: 160); 1 x 1024 tokens, 6 heads, 510 at best.
+//   18   1 x 900 tokens, 1 head: 717, 404, 220, 137            6.2  3 heads: 717, 406, 225, 326
+//   4.8  six of 5 to 900, 3 heads: 717, 407, 316, 491          2.9  1 x 1024, 6 heads: 767, 412, 456, 659
+//   0.8  3 x 900, 8 heads: 1306, 1143, 1523, 2283              0.6  2 x 2048, 8 heads: 2823, 2950, 3636, 4872
+// Chains of few tiles gain less than the joining costs unless they are much longer than the share (bf16, d = 96 and
+// 64, four sequences of 20 to 300 tokens, 16 heads, chains of five at 1.7: 193, 238, 391).
+// 32-row tiles: 1 x 300 tokens, 1 head, 99 in clusters of four (64-row: 131); 64 x 16 tokens, 8 heads, d = 64 and 64,
+// 90 (64-row: 159); 1 x 1024 tokens, 6 heads, 500 at best.
 Shape shape(const MlaArgs &a, bool keys) {  // of the kernel whose blocks own queries, or keys
     const int32_t *owned = keys ? a.cu_k_host : a.cu_q_host, *streamed = keys ? a.cu_q_host : a.cu_k_host;
     const int64_t t32 = count_tiles(owned, a.num_seqs, 32), t64 = count_tiles(owned, a.num_seqs, 64), sms = device_sm_count();
@@ -451,7 +453,7 @@ Shape shape(const MlaArgs &a, bool keys) {  // of the kernel whose blocks own qu
         }
     }
     const double ratio = double(longest) * double(s.own == 32 ? 2 * sms : sms) / (double(sum) * a.H + 1.);
-    s.ranks = ratio >= 8. && 9 * blocks <= sms ? 8 : ratio >= 4.5 ? 4 : ratio >= 0.75 ? 2 : 1;
+    s.ranks = ratio >= 8. && 9 * blocks <= sms ? 8 : ratio >= 4.5 ? 4 : ratio >= (longest < 8 ? 2. : 0.75) ? 2 : 1;
     while (s.ranks > longest) s.ranks /= 2;
     if (s.ranks < 1) s.ranks = 1;
     return s;
