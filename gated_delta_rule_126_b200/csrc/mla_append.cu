@@ -160,9 +160,12 @@ template <typename T, int V> __global__ void __launch_bounds__(kThreads, 20) app
         if (a.inv_freq != nullptr && tid < half) {
             const double ang = double(pos) * double(a.inv_freq[tid]);
             const double two_pi = 6.283185307179586476925, turns = rint(ang * (1.0 / two_pi));
+            const double within = fma(-turns, two_pi, ang);
+            // The angle in float32 is off by up to 2^-23, twice what rounding a cosine costs: `rest` puts that right.
+            const float turn = float(within), rest = float(within - double(turn));
             float s, c;
-            sincosf(float(fma(-turns, two_pi, ang)), &s, &c);
-            cs[tid] = make_float2(c, s);
+            sincosf(turn, &s, &c);
+            cs[tid] = make_float2(fmaf(-rest, s, c), fmaf(rest, c, s));
         }
     }
     const bool turn = a.inv_freq != nullptr;
